@@ -23,7 +23,9 @@ EXPORTS = ("kda_fwd", "gdn_fwd", "kda_fwd_workspace_size", "gdn_fwd_workspace_si
            "kda_fwd_split_workspace_size", "kda_fwd_split", "gdn_fwd_split", "kda_prep",
            "gdn_prep", "kda_recur", "kda_prep_timed", "kda_recur_timed", "kda_decode", "gdn_decode", "kda_bwd_workspace_size",
            "kda_bwd", "gdn_bwd", "kda_fwd_save", "gdn_fwd_save", "kda_bwd_saved",
-           "gdn_bwd_saved", "kda_status_str", "kda_version")
+           "gdn_bwd_saved", "la_fwd_workspace_size", "la_fwd", "la_bwd_workspace_size", "la_bwd",
+           "la_decode", "gated_norm_fwd", "gated_norm_bwd_workspace_size", "gated_norm_bwd",
+           "kda_status_str", "kda_version")
 
 
 class LibKdaError(RuntimeError):
@@ -111,6 +113,27 @@ def load(path: Path | str | None = None):
         fn = getattr(lib, name)
         fn.restype = ctypes.c_size_t
         fn.argtypes = [i32] * 6
+    for name in ("la_fwd_workspace_size", "la_bwd_workspace_size"):
+        getattr(lib, name).restype = ctypes.c_size_t
+        getattr(lib, name).argtypes = [i32] * 7
+    lib.la_fwd.restype = ctypes.c_int
+    lib.la_fwd.argtypes = [u16p, u16p, u16p, f32p, f32, f32p, f32p, i32p, i32, i32, i32, i32, i32,
+                           i32, u16p, vp, sz, i32, vp]
+    lib.la_bwd.restype = ctypes.c_int
+    lib.la_bwd.argtypes = [u16p, u16p, u16p, f32p, f32, f32p, i32p, i32, i32, i32, i32, i32, i32,
+                           u16p, f32p, u16p, u16p, u16p, f32p, vp, sz, i32, vp]
+    lib.la_decode.restype = ctypes.c_int
+    lib.la_decode.argtypes = [u16p, u16p, u16p, f32p, f32, f32p, f32p, i32, i32, i32, i32, u16p,
+                              vp]
+    i64 = ctypes.c_int64
+    lib.gated_norm_fwd.restype = ctypes.c_int
+    lib.gated_norm_fwd.argtypes = [u16p, u16p, f32p, u16p, f32p, i32, f32, i64, i32, i32, u16p,
+                                   vp]
+    lib.gated_norm_bwd_workspace_size.restype = ctypes.c_size_t
+    lib.gated_norm_bwd_workspace_size.argtypes = [i64, i32, i32]
+    lib.gated_norm_bwd.restype = ctypes.c_int
+    lib.gated_norm_bwd.argtypes = [u16p, u16p, f32p, u16p, f32p, i32, f32, i64, i32, i32, u16p,
+                                   u16p, u16p, f32p, u16p, f32p, vp, sz, vp]
     lib.kda_status_str.restype = ctypes.c_char_p
     lib.kda_status_str.argtypes = [ctypes.c_int]
     lib.kda_version.restype = ctypes.c_int
@@ -624,3 +647,217 @@ def gdn_bwd(q, k, v, g, beta, do, scale=None, initial_state=None, dfinal=None, c
               _ptr(o["dk"]), _ptr(o["dv"]), _ptr(o["dg"]), _ptr(o["dbeta"]), _ptr(o["dh0"]),
               _ptr(ws), _nbytes(ws), a["stream"]))
     return o
+
+
+# ------------------------------------------ linear attention, a decay for each head
+def _on(dev):
+    """The device made current for the launches (they go to its current stream)."""
+    torch = _torch()
+    return torch.cuda.device(dev)
+
+
+def la_workspace_size(B, T, H, K, V, num_seqs=None, segment_chunks=0, backward=False) -> int:
+    """Workspace bytes of la_fwd (or la_bwd).  0: unsupported sizes."""
+    fn = load().la_bwd_workspace_size if backward else load().la_fwd_workspace_size
+    return int(fn(B, T, H, K, V, B if num_seqs is None else num_seqs, int(segment_chunks)))
+
+
+def _la_prepare(q, k, v, log_decay, scale, initial_state, cu_seqlens, workspace, segment_chunks,
+                backward):
+    torch = _torch()
+    _need(q, "q", torch.bfloat16)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, T, H, K]")
+    dev = q.device
+    B, T, H, K = q.shape
+    _need(k, "k", torch.bfloat16, (B, T, H, K), dev)
+    _need(v, "v", torch.bfloat16, None, dev)
+    if v.dim() != 4 or v.shape[:3] != q.shape[:3]:
+        raise ValueError(f"v must be [B, T, H, V] with q's {tuple(q.shape[:3])}, got "
+                         f"{tuple(v.shape)}")
+    V = v.shape[3]
+    _need(log_decay, "log_decay", torch.float32, (H,), dev)
+    N = B
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be 1-D with num_seqs + 1 entries")
+        if B != 1:
+            raise ValueError("cu_seqlens needs B == 1 (sequences packed along T)")
+        N = cu_seqlens.numel() - 1
+    if initial_state is not None:
+        _need(initial_state, "initial_state", torch.float32, (N, H, K, V), dev)
+    need = la_workspace_size(B, T, H, K, V, N, segment_chunks, backward)
+    if need == 0:
+        raise LibKdaError(2, status_str(2))
+    if workspace is None:
+        if need > 256:  # (one alignment unit: no segments, no workspace)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif _nbytes(workspace) < need or workspace.device != dev:
+        raise LibKdaError(3, status_str(3))
+    return (dev, B, T, H, K, V, N, float(K ** -0.5 if scale is None else scale), workspace,
+            0 if workspace is None else _nbytes(workspace),
+            ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream))
+
+
+def la_fwd(q, k, v, log_decay, scale=None, initial_state=None, output_final_state=True,
+           cu_seqlens=None, workspace=None, out=None, final_out=None, segment_chunks=0):
+    """Linear attention with a decay for each head, over prompts: S_t = exp(log_decay[h])
+    S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.  q, k [B,T,H,K], v [B,T,H,V] bf16 (used
+    as given: no norm); log_decay [H] fp32 (<= 0); initial_state [N,H,K,V] fp32 or None;
+    cu_seqlens int32 [N+1] or None (B must then be 1; rows outside every sequence get
+    zeros).  ``segment_chunks``: 0 automatic, < 0 whole sequences, > 0 segments of that
+    many 64-token chunks.  ``workspace`` (la_workspace_size bytes), ``out`` and
+    ``final_out`` optionally supply device buffers.  Returns (o [B,T,H,V] bf16,
+    final_state [N,H,K,V] fp32 or None)."""
+    torch = _torch()
+    dev, B, T, H, K, V, N, sc, ws, wsb, stream = _la_prepare(
+        q, k, v, log_decay, scale, initial_state, cu_seqlens, workspace, segment_chunks, False)
+    if out is None:
+        out = torch.empty((B, T, H, V), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, "out", torch.bfloat16, (B, T, H, V), dev)
+    final = None
+    if output_final_state:
+        if final_out is None:
+            final_out = torch.empty((N, H, K, V), dtype=torch.float32, device=dev)
+        else:
+            _need(final_out, "final_out", torch.float32, (N, H, K, V), dev)
+        final = final_out
+    with _on(dev):
+        _check(load().la_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), sc, _ptr(initial_state),
+                             _ptr(final), _ptr(cu_seqlens), N, B, T, H, K, V, _ptr(out), _ptr(ws),
+                             wsb, int(segment_chunks), stream))
+    return out, final
+
+
+def la_bwd(q, k, v, log_decay, do, scale=None, initial_state=None, dfinal=None, cu_seqlens=None,
+           workspace=None, need_dh0=True, segment_chunks=0):
+    """Gradients of la_fwd for dL/do = ``do`` [B,T,H,V] bf16 and dL/d(final state) =
+    ``dfinal`` [N,H,K,V] fp32 (None: zero).  Returns a dict with dq, dk [B,T,H,K], dv
+    [B,T,H,V] (bf16) and dh0 [N,H,K,V] (fp32; None unless ``need_dh0``).  No gradient is
+    formed for log_decay."""
+    torch = _torch()
+    dev, B, T, H, K, V, N, sc, ws, wsb, stream = _la_prepare(
+        q, k, v, log_decay, scale, initial_state, cu_seqlens, workspace, segment_chunks, True)
+    _need(do, "do", torch.bfloat16, (B, T, H, V), dev)
+    if dfinal is not None:
+        _need(dfinal, "dfinal", torch.float32, (N, H, K, V), dev)
+    r = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
+         "dh0": torch.empty((N, H, K, V), dtype=torch.float32, device=dev) if need_dh0 else None}
+    with _on(dev):
+        _check(load().la_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), sc, _ptr(initial_state),
+                             _ptr(cu_seqlens), N, B, T, H, K, V, _ptr(do), _ptr(dfinal),
+                             _ptr(r["dq"]), _ptr(r["dk"]), _ptr(r["dv"]), _ptr(r["dh0"]),
+                             _ptr(ws), wsb, int(segment_chunks), stream))
+    return r
+
+
+def la_decode(q, k, v, log_decay, scale=None, state=None, state_out=None, out=None):
+    """One token of linear attention for N sequences: q, k [N,H,K], v [N,H,V] bf16;
+    log_decay [H] fp32; state [N,H,K,V] fp32 or None (zeros).  ``state_out`` may be
+    ``state`` (update in place).  Returns (o [N,H,V] bf16, new state [N,H,K,V] fp32)."""
+    torch = _torch()
+    _need(q, "q", torch.bfloat16)
+    if q.dim() != 3:
+        raise ValueError("q must be [N, H, K]")
+    dev = q.device
+    N, H, K = q.shape
+    _need(k, "k", torch.bfloat16, (N, H, K), dev)
+    _need(v, "v", torch.bfloat16, None, dev)
+    if v.dim() != 3 or v.shape[:2] != q.shape[:2]:
+        raise ValueError(f"v must be [N, H, V] with q's {tuple(q.shape[:2])}, got "
+                         f"{tuple(v.shape)}")
+    V = v.shape[2]
+    _need(log_decay, "log_decay", torch.float32, (H,), dev)
+    if state is not None:
+        _need(state, "state", torch.float32, (N, H, K, V), dev)
+    if state_out is None:
+        state_out = torch.empty((N, H, K, V), dtype=torch.float32, device=dev)
+    else:
+        _need(state_out, "state_out", torch.float32, (N, H, K, V), dev)
+    if out is None:
+        out = torch.empty((N, H, V), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, "out", torch.bfloat16, (N, H, V), dev)
+    stream = ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    with _on(dev):
+        _check(load().la_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                                float(K ** -0.5 if scale is None else scale), _ptr(state),
+                                _ptr(state_out), N, H, K, V, _ptr(out), stream))
+    return out, state_out
+
+
+# ---------------------------------------------------------------- gated norm
+_ACTIVATIONS = {"sigmoid": 0, "silu": 1}
+
+
+def _norm_prepare(x, gate, weight, activation, eps, residual, residual_scale):
+    torch = _torch()
+    _need(x, "x", torch.bfloat16)
+    if x.dim() < 2:
+        raise ValueError("x must be [..., H, D]")
+    dev = x.device
+    H, D = x.shape[-2:]
+    if gate is not None:
+        _need(gate, "gate", torch.bfloat16, x.shape, dev)
+    _need(weight, "weight", torch.float32, (D,), dev)
+    if (residual is None) != (residual_scale is None):
+        raise ValueError("residual and residual_scale come together")
+    if residual is not None:
+        _need(residual, "residual", torch.bfloat16, x.shape, dev)
+        _need(residual_scale, "residual_scale", torch.float32, (H,), dev)
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}, got {activation!r}")
+    if H < 1 or D < 1:
+        raise ValueError("x must be [..., H, D] with H and D at least 1")
+    tokens = x.numel() // (H * D)
+    args = (_ptr(x), _ptr(gate), _ptr(weight), _ptr(residual), _ptr(residual_scale),
+            _ACTIVATIONS[activation], float(eps), tokens, H, D)
+    return dev, tokens, H, D, args, ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+
+
+def gated_norm_fwd(x, gate, weight, activation="sigmoid", eps=1e-6, residual=None,
+                   residual_scale=None, out=None):
+    """The norm behind an attention block, on rows x [..., H, D] bf16:
+    u = x + residual_scale[h] residual (if given), y = u / sqrt(mean(u^2) + eps) weight
+    act(gate).  gate and residual as x (gate None: no gate); weight [D], residual_scale [H]
+    fp32; activation "sigmoid" or "silu"; D a multiple of 8 up to 512.  ``out`` may be
+    ``x`` or ``gate``.  Returns y [..., H, D] bf16."""
+    torch = _torch()
+    dev, _, _, _, args, stream = _norm_prepare(x, gate, weight, activation, eps, residual,
+                                               residual_scale)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need(out, "out", torch.bfloat16, x.shape, dev)
+    with _on(dev):
+        _check(load().gated_norm_fwd(*args, _ptr(out), stream))
+    return out
+
+
+def gated_norm_bwd(x, gate, weight, dy, activation="sigmoid", eps=1e-6, residual=None,
+                   residual_scale=None, workspace=None):
+    """Gradients of gated_norm_fwd for dL/dy = ``dy``: a dict with dx, dgate, dresidual
+    (bf16, as x; None without that input), dweight [D] and dresidual_scale [H] (fp32)."""
+    torch = _torch()
+    dev, tokens, H, D, args, stream = _norm_prepare(x, gate, weight, activation, eps, residual,
+                                                    residual_scale)
+    _need(dy, "dy", torch.bfloat16, x.shape, dev)
+    need = int(load().gated_norm_bwd_workspace_size(tokens, H, D))
+    if need == 0:
+        raise LibKdaError(2, status_str(2))
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif _nbytes(workspace) < need or workspace.device != dev:
+        raise LibKdaError(3, status_str(3))
+    r = {"dx": torch.empty_like(x), "dgate": None if gate is None else torch.empty_like(gate),
+         "dweight": torch.empty_like(weight),
+         "dresidual": None if residual is None else torch.empty_like(residual),
+         "dresidual_scale": None if residual is None else torch.empty_like(residual_scale)}
+    with _on(dev):
+        _check(load().gated_norm_bwd(*args, _ptr(dy), _ptr(r["dx"]), _ptr(r["dgate"]),
+                                     _ptr(r["dweight"]), _ptr(r["dresidual"]),
+                                     _ptr(r["dresidual_scale"]), _ptr(workspace),
+                                     _nbytes(workspace), stream))
+    return r

@@ -14,6 +14,11 @@ by rounding only.
 This module only checks and forwards arguments (no arithmetic of the method
 runs outside the library).
 
+``chunk_la`` (linear attention with a decay for each head) and ``gated_norm``
+(the norm behind an attention block) are the same over la_fwd / la_bwd and
+gated_norm_fwd / gated_norm_bwd; their backward passes need nothing of the
+forward call, so they keep the inputs only.
+
 The kernels fix the variant the pages describe as the fast path: q and k are
 L2-normalised inside, the KDA gate is formed inside from g, A_log and dt_bias
 (clamped at ``lower_bound``), KDA beta arrives as logits and goes through the
@@ -170,3 +175,89 @@ def chunk_gdn(q, k, v, g, beta, scale=None, initial_state=None, output_final_sta
     out = _GDN.get().apply(q, k, v, g, beta, initial_state, float(scale), cu_seqlens,
                            bool(output_final_state))
     return out if output_final_state else (out, None)
+
+
+class _LA:
+    fn = None
+
+    @classmethod
+    def get(cls):
+        if cls.fn is None:
+            torch = _torch()
+
+            class LAFunction(torch.autograd.Function):
+                @staticmethod
+                def forward(ctx, q, k, v, log_decay, initial_state, scale, cu_seqlens,
+                            output_final_state):
+                    o, final = _b.la_fwd(q, k, v, log_decay, scale, initial_state,
+                                         output_final_state, cu_seqlens)
+                    ctx.save_for_backward(q, k, v, log_decay, initial_state, cu_seqlens)
+                    ctx.scale = scale
+                    if final is None:
+                        return o
+                    return o, final
+
+                @staticmethod
+                def backward(ctx, do, dfinal=None):
+                    q, k, v, log_decay, h0, cu = ctx.saved_tensors
+                    r = _b.la_bwd(q, k, v, log_decay, do.contiguous(), ctx.scale, h0,
+                                  None if dfinal is None else dfinal.contiguous(), cu,
+                                  need_dh0=h0 is not None and ctx.needs_input_grad[4])
+                    return r["dq"], r["dk"], r["dv"], None, r["dh0"], None, None, None
+
+            cls.fn = LAFunction
+        return cls.fn
+
+
+class _GatedNorm:
+    fn = None
+
+    @classmethod
+    def get(cls):
+        if cls.fn is None:
+            torch = _torch()
+
+            class GatedNormFunction(torch.autograd.Function):
+                @staticmethod
+                def forward(ctx, x, gate, weight, residual, residual_scale, activation, eps):
+                    ctx.save_for_backward(x, gate, weight, residual, residual_scale)
+                    ctx.activation, ctx.eps = activation, eps
+                    return _b.gated_norm_fwd(x, gate, weight, activation, eps, residual,
+                                             residual_scale)
+
+                @staticmethod
+                def backward(ctx, dy):
+                    x, gate, weight, residual, residual_scale = ctx.saved_tensors
+                    r = _b.gated_norm_bwd(x, gate, weight, dy.contiguous(), ctx.activation,
+                                          ctx.eps, residual, residual_scale)
+                    return (r["dx"], r["dgate"], r["dweight"], r["dresidual"],
+                            r["dresidual_scale"], None, None)
+
+            cls.fn = GatedNormFunction
+        return cls.fn
+
+
+def chunk_la(q, k, v, log_decay, scale=None, initial_state=None, output_final_state=False,
+             cu_seqlens=None):
+    """Differentiable linear attention with a decay for each head.  q, k [B,T,H,K], v
+    [B,T,H,V] bf16, used as given; log_decay [H] fp32 (<= 0); initial_state [N,H,K,V] fp32
+    or None; cu_seqlens int32 [N+1] or None (B = 1).  Returns (o, final_state);
+    final_state is None unless ``output_final_state``.  Gradients reach q, k, v and
+    initial_state; the decays are fixed, so a log_decay that asks for one is refused."""
+    torch = _torch()
+    if torch.is_grad_enabled() and log_decay.requires_grad:
+        raise NotImplementedError("log_decay.requires_grad is not supported: the decays are "
+                                  "fixed and get no gradient")
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    out = _LA.get().apply(q, k, v, log_decay, initial_state, float(scale), cu_seqlens,
+                          bool(output_final_state))
+    return out if output_final_state else (out, None)
+
+
+def gated_norm(x, gate, weight, activation="sigmoid", eps=1e-6, residual=None,
+               residual_scale=None):
+    """Differentiable gated norm on rows x [..., H, D] (see gated_norm_fwd).  Gradients
+    reach x, gate, weight, residual and residual_scale."""
+    return _GatedNorm.get().apply(x, gate, weight, residual, residual_scale, activation,
+                                  float(eps))

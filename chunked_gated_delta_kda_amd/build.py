@@ -17,7 +17,8 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 LIB = PKG / "libkda.so"
 SOURCES = ["kda_api.hip", "kda_prep.hip", "kda_recur.hip", "kda_fused.hip", "kda_decode.hip",
-           "kda_split.hip", "kda_bwd.hip"]
+           "kda_split.hip", "kda_bwd.hip", "la_api.hip", "la_chunk.hip", "la_decode.hip",
+           "gated_norm.hip"]
 ARCH = "gfx950"
 
 
@@ -32,7 +33,7 @@ def hipcc() -> str:
 # backward gradient kernel is left to the compiler's default: its register
 # demand exceeds the VGPR file, and the VGPR-form rewrite crashes on it.
 VGPR_FORM = {"kda_api.hip", "kda_prep.hip", "kda_recur.hip", "kda_fused.hip", "kda_decode.hip",
-             "kda_split.hip"}
+             "kda_split.hip", "la_chunk.hip"}
 
 
 # Sources scheduled with the compiler's iterative ILP strategy instead of the

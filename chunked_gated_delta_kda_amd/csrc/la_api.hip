@@ -1,0 +1,369 @@
+// la_api.hip -- the C ABI of linear attention with a decay for each head and
+// of the gated norm (declared in include/kda.h): host-side argument checks,
+// workspace layout and the launches on the caller's stream.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "kda.h"
+#include "la_launch.h"
+
+namespace {
+
+constexpr size_t ALIGN = 256;
+constexpr int64_t I31 = (int64_t)1 << 31;
+
+size_t align_up(size_t x) { return (x + ALIGN - 1) / ALIGN * ALIGN; }
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+bool supported_dim(int32_t d) { return d == 64 || d == 128; }
+
+struct LaCall {
+    const int32_t* cu;
+    bool packed;
+    int32_t num_seqs, B, T, H, K, V;
+    int32_t segments;  // the caller's request: chunks per segment, 0 automatic, < 0 whole
+};
+
+// Segments of a batch (see LaSeqs); dirs: passes with a state pass of their own.
+kda::LaSeqs plan(const LaCall& c) {
+    kda::LaSeqs s{};
+    s.cu = c.cu;
+    s.n_seqs = c.packed ? c.num_seqs : c.B;
+    s.T = c.T;
+    s.H = c.H;
+    const int64_t tokens = c.packed ? c.T : (int64_t)c.B * c.T;
+    const int64_t chunks = (tokens / s.n_seqs + kda::LA_CHUNK - 1) / kda::LA_CHUNK;  // of an average sequence
+    int64_t per = c.segments;
+    if (c.segments == 0) {
+        const int64_t groups = (int64_t)s.n_seqs * c.H * (c.V / kda::LA_COLS);
+        per = -1;
+        if (groups < 256 && chunks >= 32) {
+            const int64_t segs = std::min<int64_t>((512 + groups - 1) / groups, chunks / 16);
+            if (segs > 1) per = (chunks + segs - 1) / segs;
+        }
+    }
+    s.seg_per_seq = 1;
+    s.n_slots = s.n_seqs;
+    // (a segment that holds every token is the whole sequence)
+    if (per > 0 && per * kda::LA_CHUNK < c.T) {
+        s.seg_tokens = (int32_t)(per * kda::LA_CHUNK);
+        if (c.packed) {
+            const int64_t n = (int64_t)c.T / s.seg_tokens + s.n_seqs;
+            s.n_slots = (int32_t)std::min<int64_t>(n, INT32_MAX);
+        } else {
+            s.seg_per_seq = (c.T + s.seg_tokens - 1) / s.seg_tokens;
+            s.n_slots = (int32_t)std::min<int64_t>((int64_t)s.seg_per_seq * s.n_seqs, INT32_MAX);
+        }
+    }
+    return s;
+}
+
+size_t la_states_bytes(const LaCall& c, const kda::LaSeqs& s) {
+    return s.seg_tokens ? align_up((size_t)s.n_slots * c.H * c.K * c.V * sizeof(float)) : 0;
+}
+
+bool valid_sizes(const LaCall& c) {
+    return c.B >= 1 && c.T >= 0 && c.H >= 1 && c.num_seqs >= 1 && supported_dim(c.K) && supported_dim(c.V) &&
+           (int64_t)c.B * c.T < I31;
+}
+
+// workspace bytes (dirs: 1 forward, 2 backward); 0: sizes that are not supported
+size_t la_workspace(const LaCall& c, int dirs) {
+    if (!valid_sizes(c)) return 0;
+    const kda::LaSeqs s = plan(c);
+    return std::max(ALIGN, (size_t)dirs * la_states_bytes(c, s));
+}
+
+// Checks of every pass; fills the plan.
+int check_la(const LaCall& c, float scale, const float* log_decay, const void* ws, size_t ws_bytes, int dirs,
+             kda::LaSeqs& s) {
+    if (c.B < 1 || c.T < 0 || c.H < 1) return KDA_ERR_INVALID_ARG;
+    if (!supported_dim(c.K) || !supported_dim(c.V)) return KDA_ERR_UNSUPPORTED;
+    if ((int64_t)c.B * c.T >= I31 || !std::isfinite(scale) || !log_decay || !aligned(log_decay, 4))
+        return KDA_ERR_INVALID_ARG;
+    if (c.packed && (c.B != 1 || c.num_seqs < 1 || !aligned(c.cu, 4))) return KDA_ERR_INVALID_ARG;
+    s = plan(c);
+    // one grid over (slot, head, column block), and over (sequence, head, piece of a state)
+    if ((int64_t)s.n_slots * c.H >= I31 / 64) return KDA_ERR_INVALID_ARG;
+    const size_t need = (size_t)dirs * la_states_bytes(c, s);
+    if (need && (!ws || !aligned(ws, ALIGN) || ws_bytes < need)) return KDA_ERR_WORKSPACE;
+    return KDA_OK;
+}
+
+kda::LaPass make_pass(const uint16_t* x, const uint16_t* y, const uint16_t* z, uint16_t* o, int32_t D2, int32_t row,
+                      int32_t col, bool reverse, float scale) {
+    kda::LaPass p{};
+    p.x = x;
+    p.y = y;
+    p.z = z;
+    p.o = o;
+    p.D2 = D2;
+    p.row = row;
+    p.col = col;
+    p.reverse = reverse;
+    p.in_scale = scale;
+    p.x_scale = reverse ? 1.f : scale;
+    p.z_scale = reverse ? scale : 1.f;
+    return p;
+}
+
+// what each segment adds to the state, for a pass with the states' own [K, V] layout
+void launch_states(const kda::LaSeqs& s, const float* log_decay, const kda::LaPass* p, float* const* out, int n,
+                   int32_t K, hipStream_t stream) {
+    kda::LaArgs a{};
+    a.s = s;
+    a.log_decay = log_decay;
+    for (int i = 0; i < n; ++i) {
+        a.pass[i] = p[i];
+        a.pass[i].x = nullptr;
+        a.pass[i].o = nullptr;
+        a.pass[i].s_in = nullptr;
+        a.pass[i].s_out = out[i];
+        a.pass[i].s_out_slots = 1;
+    }
+    kda::launch_la_chunk(a, n, K, true, stream);
+}
+
+int status() { return hipGetLastError() == hipSuccess ? KDA_OK : KDA_ERR_LAUNCH; }
+
+}  // namespace
+
+extern "C" {
+
+size_t la_fwd_workspace_size(int32_t B, int32_t T, int32_t H, int32_t K, int32_t V, int32_t num_seqs,
+                             int32_t segment_chunks) {
+    // (packed and fixed-length batches of these sizes plan alike but for the
+    // slots: the larger of the two)
+    const LaCall f{nullptr, false, num_seqs, B, T, H, K, V, segment_chunks};
+    LaCall p = f;
+    p.packed = true;
+    const size_t a = la_workspace(f, 1);
+    return B == 1 && a ? std::max(a, la_workspace(p, 1)) : a;
+}
+
+size_t la_bwd_workspace_size(int32_t B, int32_t T, int32_t H, int32_t K, int32_t V, int32_t num_seqs,
+                             int32_t segment_chunks) {
+    const LaCall f{nullptr, false, num_seqs, B, T, H, K, V, segment_chunks};
+    LaCall p = f;
+    p.packed = true;
+    const size_t a = la_workspace(f, 2);
+    return B == 1 && a ? std::max(a, la_workspace(p, 2)) : a;
+}
+
+int la_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float* log_decay, float scale,
+           const float* initial_state, float* final_state, const int32_t* cu_seqlens, int32_t num_seqs, int32_t B,
+           int32_t T, int32_t H, int32_t K, int32_t V, uint16_t* o, void* workspace, size_t workspace_bytes,
+           int32_t segment_chunks, void* stream) {
+    const LaCall c{cu_seqlens, cu_seqlens != nullptr, num_seqs, B, T, H, K, V, segment_chunks};
+    kda::LaSeqs s;
+    const int st = check_la(c, scale, log_decay, workspace, workspace_bytes, 1, s);
+    if (st != KDA_OK) return st;
+    if (T > 0 && (!q || !k || !v || !o)) return KDA_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)q, (const void*)k, (const void*)v, (const void*)o, (const void*)initial_state,
+                          (const void*)final_state})
+        if (!aligned(p, 16)) return KDA_ERR_INVALID_ARG;
+    const hipStream_t str = static_cast<hipStream_t>(stream);
+    (void)hipGetLastError();  // clear a stale error from unrelated work
+    kda::LaArgs a{};
+    a.s = s;
+    a.log_decay = log_decay;
+    kda::LaPass& p = a.pass[0];
+    p = make_pass(q, k, v, o, V, V, 1, false, scale);
+    p.s_in = initial_state;
+    p.s_out = final_state;
+    if (s.seg_tokens) {
+        float* states = static_cast<float*>(workspace);
+        launch_states(s, log_decay, &p, &states, 1, K, str);
+        kda::LaScanArgs sc{};
+        sc.s = s;
+        sc.log_decay = log_decay;
+        sc.init[0] = initial_state;
+        sc.state[0] = states;
+        sc.elems = K * V;
+        sc.n_dirs = 1;
+        kda::launch_la_scan(sc, str);
+        p.s_in = states;
+        p.s_in_slots = 1;
+    }
+    kda::launch_la_chunk(a, 1, K, false, str);
+    return status();
+}
+
+int la_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float* log_decay, float scale,
+           const float* initial_state, const int32_t* cu_seqlens, int32_t num_seqs, int32_t B, int32_t T, int32_t H,
+           int32_t K, int32_t V, const uint16_t* d_o, const float* d_final, uint16_t* dq, uint16_t* dk, uint16_t* dv,
+           float* dh0, void* workspace, size_t workspace_bytes, int32_t segment_chunks, void* stream) {
+    const LaCall c{cu_seqlens, cu_seqlens != nullptr, num_seqs, B, T, H, K, V, segment_chunks};
+    kda::LaSeqs s;
+    const int st = check_la(c, scale, log_decay, workspace, workspace_bytes, 2, s);
+    if (st != KDA_OK) return st;
+    if (T > 0 && (!q || !k || !v || !d_o || !dq || !dk || !dv)) return KDA_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)q, (const void*)k, (const void*)v, (const void*)d_o, (const void*)dq,
+                          (const void*)dk, (const void*)dv, (const void*)initial_state, (const void*)d_final,
+                          (const void*)dh0})
+        if (!aligned(p, 16)) return KDA_ERR_INVALID_ARG;
+    const hipStream_t str = static_cast<hipStream_t>(stream);
+    (void)hipGetLastError();
+    kda::LaPass pq = make_pass(d_o, v, k, dq, K, 1, V, false, scale);
+    kda::LaPass pk = make_pass(v, d_o, q, dk, K, 1, V, true, scale);
+    kda::LaPass pv = make_pass(k, q, d_o, dv, V, V, 1, true, scale);
+    pq.s_in = initial_state;
+    pk.s_in = pv.s_in = d_final;
+    pv.s_out = dh0;
+    if (s.seg_tokens) {
+        float* states[2] = {static_cast<float*>(workspace),
+                            static_cast<float*>(workspace) + la_states_bytes(c, s) / sizeof(float)};
+        const kda::LaPass p[2] = {make_pass(q, k, v, nullptr, V, V, 1, false, scale), pv};
+        launch_states(s, log_decay, p, states, 2, K, str);
+        kda::LaScanArgs sc{};
+        sc.s = s;
+        sc.log_decay = log_decay;
+        sc.init[0] = initial_state;
+        sc.init[1] = d_final;
+        sc.state[0] = states[0];
+        sc.state[1] = states[1];
+        sc.elems = K * V;
+        sc.n_dirs = 2;
+        kda::launch_la_scan(sc, str);
+        pq.s_in = states[0];
+        pk.s_in = pv.s_in = states[1];
+        pq.s_in_slots = pk.s_in_slots = pv.s_in_slots = 1;
+    }
+    kda::LaArgs a{};
+    a.s = s;
+    a.log_decay = log_decay;
+    if (K == V) {
+        a.pass[0] = pk;
+        a.pass[1] = pv;
+        a.pass[2] = pq;
+        kda::launch_la_chunk(a, 3, K, false, str);
+    } else {
+        a.pass[0] = pk;
+        a.pass[1] = pq;
+        kda::launch_la_chunk(a, 2, V, false, str);
+        a.pass[0] = pv;
+        kda::launch_la_chunk(a, 1, K, false, str);
+    }
+    return status();
+}
+
+int la_decode(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float* log_decay, float scale,
+              const float* state_in, float* state_out, int32_t N, int32_t H, int32_t K, int32_t V, uint16_t* o,
+              void* stream) {
+    if (N < 1 || H < 1) return KDA_ERR_INVALID_ARG;
+    if (!q || !k || !v || !log_decay || !state_out || !o) return KDA_ERR_INVALID_ARG;
+    if (!supported_dim(K) || !supported_dim(V)) return KDA_ERR_UNSUPPORTED;
+    if (!std::isfinite(scale) || (int64_t)N * H * (V / 64) >= I31) return KDA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 8) || !aligned(o, 8) || !aligned(log_decay, 4) ||
+        !aligned(state_in, 16) || !aligned(state_out, 16))
+        return KDA_ERR_INVALID_ARG;
+    kda::LaDecodeArgs d{};
+    d.q = q;
+    d.k = k;
+    d.v = v;
+    d.log_decay = log_decay;
+    d.state_in = state_in;
+    d.state_out = state_out;
+    d.o = o;
+    d.scale = scale;
+    d.H = H;
+    d.V = V;
+    d.n_pairs = N * H;
+    (void)hipGetLastError();
+    kda::launch_la_decode(d, K, static_cast<hipStream_t>(stream));
+    return status();
+}
+
+}  // extern "C"
+
+namespace {
+
+int check_norm(const uint16_t* x, const uint16_t* gate, const float* weight, const uint16_t* residual,
+               const float* residual_scale, int32_t activation, float eps, int64_t tokens, int32_t H, int32_t D) {
+    if (tokens < 0 || H < 1 || D < 1) return KDA_ERR_INVALID_ARG;
+    if (D % 8 || D > 512) return KDA_ERR_UNSUPPORTED;
+    if (tokens * (double)H >= (double)I31) return KDA_ERR_INVALID_ARG;
+    if (activation != KDA_GATE_SIGMOID && activation != KDA_GATE_SILU) return KDA_ERR_INVALID_ARG;
+    if (!(eps >= 0.f) || !std::isfinite(eps) || !weight) return KDA_ERR_INVALID_ARG;
+    // (the scale says that there is a residual: it is never empty)
+    if (residual && !residual_scale) return KDA_ERR_INVALID_ARG;
+    if (tokens > 0 && (!x || (residual_scale && !residual))) return KDA_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(gate, 16) || !aligned(residual, 16) || !aligned(weight, 4) ||
+        !aligned(residual_scale, 4))
+        return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+
+kda::GatedNormArgs norm_args(const uint16_t* x, const uint16_t* gate, const float* weight, const uint16_t* residual,
+                             const float* residual_scale, int32_t activation, float eps, int64_t tokens, int32_t H,
+                             int32_t D) {
+    kda::GatedNormArgs a{};
+    a.x = x;
+    a.gate = gate;
+    a.weight = weight;
+    a.res = residual;
+    a.res_scale = residual_scale;
+    a.silu = activation == KDA_GATE_SILU;
+    a.eps = eps;
+    a.H = H;
+    a.D = D;
+    a.rows = tokens * H;
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gated_norm_fwd(const uint16_t* x, const uint16_t* gate, const float* weight, const uint16_t* residual,
+                   const float* residual_scale, int32_t activation, float eps, int64_t tokens, int32_t H, int32_t D,
+                   uint16_t* y, void* stream) {
+    const int st = check_norm(x, gate, weight, residual, residual_scale, activation, eps, tokens, H, D);
+    if (st != KDA_OK) return st;
+    if (!aligned(y, 16) || (tokens > 0 && !y)) return KDA_ERR_INVALID_ARG;
+    if (tokens == 0) return KDA_OK;
+    kda::GatedNormArgs a = norm_args(x, gate, weight, residual, residual_scale, activation, eps, tokens, H, D);
+    a.y = y;
+    (void)hipGetLastError();
+    kda::launch_gated_norm_fwd(a, static_cast<hipStream_t>(stream));
+    return status();
+}
+
+size_t gated_norm_bwd_workspace_size(int64_t tokens, int32_t H, int32_t D) {
+    if (tokens < 0 || H < 1 || D < 1 || D % 8 || D > 512 || tokens * (double)H >= (double)I31) return 0;
+    const int64_t rows = tokens * H;
+    return align_up((size_t)kda::gated_norm_groups(rows, D) * D * sizeof(float)) +
+           align_up((size_t)rows * sizeof(float));
+}
+
+int gated_norm_bwd(const uint16_t* x, const uint16_t* gate, const float* weight, const uint16_t* residual,
+                   const float* residual_scale, int32_t activation, float eps, int64_t tokens, int32_t H, int32_t D,
+                   const uint16_t* dy, uint16_t* dx, uint16_t* dgate, float* dweight, uint16_t* dresidual,
+                   float* dresidual_scale, void* workspace, size_t workspace_bytes, void* stream) {
+    const int st = check_norm(x, gate, weight, residual, residual_scale, activation, eps, tokens, H, D);
+    if (st != KDA_OK) return st;
+    if (!dweight || (tokens > 0 && (!dy || !dx))) return KDA_ERR_INVALID_ARG;
+    if ((gate && !dgate) || (residual && !dresidual) || (residual_scale && !dresidual_scale))
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned(dy, 16) || !aligned(dx, 16) || !aligned(dgate, 16) || !aligned(dresidual, 16) ||
+        !aligned(dweight, 4) || !aligned(dresidual_scale, 4))
+        return KDA_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, ALIGN) || workspace_bytes < gated_norm_bwd_workspace_size(tokens, H, D))
+        return KDA_ERR_WORKSPACE;
+    kda::GatedNormArgs a = norm_args(x, gate, weight, residual, residual_scale, activation, eps, tokens, H, D);
+    a.dy = dy;
+    a.dx = dx;
+    a.dgate = dgate;
+    a.dres = dresidual;
+    a.dweight = dweight;
+    a.dres_scale = dresidual_scale;
+    a.groups = kda::gated_norm_groups(a.rows, D);
+    a.part_w = static_cast<float*>(workspace);
+    a.row_ds = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
+                                        align_up((size_t)a.groups * D * sizeof(float)));
+    (void)hipGetLastError();
+    kda::launch_gated_norm_bwd(a, static_cast<hipStream_t>(stream));
+    return status();
+}
+
+}  // extern "C"

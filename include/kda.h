@@ -2,7 +2,8 @@
  * kda.h -- C ABI of libkda: the chunkwise forward pass of gated delta-rule
  * linear attention on AMD Instinct MI355X (gfx950).
  *
- * Two operations:
+ * Two operations (and, at the end, linear attention with a decay for each
+ * head, la_*, and the gated norm behind any of them):
  *   kda_fwd  Kimi Delta Attention: per-channel decay computed from a
  *            pre-activation gate, beta given as logits.
  *   gdn_fwd  Gated DeltaNet: one scalar log decay per (token, head), beta
@@ -402,6 +403,103 @@ int gdn_bwd_saved(const uint16_t* q, const uint16_t* k, const uint16_t* v, const
                   int32_t K, int32_t V, const uint16_t* d_o, const float* d_final, uint16_t* dq,
                   uint16_t* dk, uint16_t* dv, float* dg, uint16_t* dbeta, float* dh0,
                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the member of this family
+ * without the delta correction.  For every sequence and head, with the state
+ * S in [K, V] layout and a = exp(log_decay[h]):
+ *   S_t = a S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t.
+ * q and k enter as they are (no norm; a feature map is the caller's).
+ * log_decay [H] fp32 holds natural logs, <= 0 (not checked); -infinity makes
+ * every token forget all before it.  No gradient is formed for it.
+ *
+ * Layouts, cu_seqlens, ownership, streams and errors are those of kda_fwd,
+ * with these additions:
+ *  - Every row of o (and of dq, dk, dv) is written: rows outside every
+ *    sequence of a packed batch (before cu_seqlens[0], from
+ *    cu_seqlens[num_seqs] on) get zeros.
+ *  - Inputs are finite.  A NaN or an infinity in a row of k or v makes the
+ *    outputs of its 64-token chunk, and all later ones of its sequence, what
+ *    they happen to be; it never leaves its sequence and head.
+ *  - Alignment: q, k, v, o, states and all gradients 16 bytes; log_decay 4.
+ *  - segment_chunks: 0 automatic, < 0 whole sequences, > 0 segments of that
+ *    many 64-token chunks.  A sequence is one chain of chunks; where the
+ *    (sequence, head) pairs are too few to fill the GPU, it is cut into
+ *    segments: a first pass forms what each adds to a zero state, a scan
+ *    gives each its entering state, and a second pass computes them all at
+ *    once.  The result is the unsplit one up to fp32 rounding.
+ *
+ * la_fwd_workspace_size / la_bwd_workspace_size: bytes of device workspace
+ * (num_seqs: packed sequences when cu_seqlens will be passed, else B), 0 for
+ * sizes that are not supported.  Only segments need it (their states, fp32
+ * [segments, H, K, V], for the backward pass twice): a call that makes none
+ * accepts NULL. */
+size_t la_fwd_workspace_size(int32_t B, int32_t T, int32_t H, int32_t K, int32_t V,
+                             int32_t num_seqs, int32_t segment_chunks);
+
+int la_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float* log_decay,
+           float scale, const float* initial_state, float* final_state,
+           const int32_t* cu_seqlens, int32_t num_seqs, int32_t B, int32_t T, int32_t H,
+           int32_t K, int32_t V, uint16_t* o, void* workspace, size_t workspace_bytes,
+           int32_t segment_chunks, void* stream);
+
+/* Gradients of la_fwd for dL/do = d_o [B, T, H, V] bf16 and dL/d(final state)
+ * = d_final [N, H, K, V] fp32 (NULL: zero).  With E_t = dL/dS_t from later
+ * tokens and R_t = E_t + scale q_t do_t^T:
+ *   dq_t = scale S_t do_t,  dv_t = R_t^T k_t,  dk_t = R_t v_t,
+ *   E_{t-1} = a R_t,  dh0 = E_{-1}
+ * dq, dk [B, T, H, K] and dv [B, T, H, V] bf16; dh0 [N, H, K, V] fp32 or NULL
+ * (not written).  No result of the forward call is needed. */
+size_t la_bwd_workspace_size(int32_t B, int32_t T, int32_t H, int32_t K, int32_t V,
+                             int32_t num_seqs, int32_t segment_chunks);
+
+int la_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float* log_decay,
+           float scale, const float* initial_state, const int32_t* cu_seqlens, int32_t num_seqs,
+           int32_t B, int32_t T, int32_t H, int32_t K, int32_t V, const uint16_t* d_o,
+           const float* d_final, uint16_t* dq, uint16_t* dk, uint16_t* dv, float* dh0,
+           void* workspace, size_t workspace_bytes, int32_t segment_chunks, void* stream);
+
+/* One token for each of N sequences (see kda_decode for the layouts): q, k
+ * [N, H, K], v, o [N, H, V] bf16; state_in (NULL: zeros), state_out
+ * [N, H, K, V] fp32, which may be the same array (update in place).  T steps
+ * equal the forward pass over T tokens up to rounding.  Alignment: q, k,
+ * states 16 bytes; v, o 8. */
+int la_decode(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float* log_decay,
+              float scale, const float* state_in, float* state_out, int32_t N, int32_t H,
+              int32_t K, int32_t V, uint16_t* o, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Gated norm: what follows an attention block of this family, for every token
+ * and head on its row of D channels:
+ *   u = x + residual_scale[h] * residual
+ *   y = u / sqrt(mean(u^2) + eps) * weight * act(gate)
+ * x, gate, residual, y [tokens, H, D] bf16; weight [D], residual_scale [H]
+ * fp32.  gate NULL: no gate.  residual_scale NULL (and residual NULL): u = x.
+ * activation: KDA_GATE_SIGMOID or KDA_GATE_SILU (also checked without a gate).
+ * D is a multiple of 8 from 8 to 512, else KDA_ERR_UNSUPPORTED; eps >= 0;
+ * tokens * H < 2^31.  tokens = 0 is allowed (row tensors may then be NULL).
+ * y may be x or gate (each row is read before it is written).  Arithmetic is
+ * fp32, each output is rounded once; a NaN or infinity in a row stays in it.  Alignment: row tensors 16 bytes.
+ *
+ * gated_norm_bwd: dL/dy = dy -> dx, dgate, dresidual [tokens, H, D] bf16 and
+ * dweight [D], dresidual_scale [H] fp32 (sums over all rows in a fixed order:
+ * reproducible).  dgate may be NULL only without a gate, dresidual and
+ * dresidual_scale only without a residual.  No result of the forward call is
+ * needed.  Outputs must not alias inputs. */
+enum kda_gate_activation { KDA_GATE_SIGMOID = 0, KDA_GATE_SILU = 1 };
+
+int gated_norm_fwd(const uint16_t* x, const uint16_t* gate, const float* weight,
+                   const uint16_t* residual, const float* residual_scale, int32_t activation,
+                   float eps, int64_t tokens, int32_t H, int32_t D, uint16_t* y, void* stream);
+
+size_t gated_norm_bwd_workspace_size(int64_t tokens, int32_t H, int32_t D);
+
+int gated_norm_bwd(const uint16_t* x, const uint16_t* gate, const float* weight,
+                   const uint16_t* residual, const float* residual_scale, int32_t activation,
+                   float eps, int64_t tokens, int32_t H, int32_t D, const uint16_t* dy,
+                   uint16_t* dx, uint16_t* dgate, float* dweight, uint16_t* dresidual,
+                   float* dresidual_scale, void* workspace, size_t workspace_bytes,
+                   void* stream);
 
 /* Static description of a status code (never NULL). */
 const char* kda_status_str(int status);
