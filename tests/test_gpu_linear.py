@@ -265,6 +265,21 @@ def test_autograd_is_la_bwd():
     assert torch.equal(gq, r["dq"])
 
 
+@pytest.mark.parametrize("K,V", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("T", [64, 130, 448])
+def test_same_results_every_time(K, V, T):
+    """No result depends on when a wave gets there."""
+    d = dev(make(4, T, 8, K, V, seed=625))
+    o, S = fwd(d)
+    r = bwd(d)
+    for _ in range(20):
+        o2, S2 = fwd(d)
+        r2 = bwd(d)
+        assert torch.equal(o, o2) and torch.equal(S, S2)
+        for n in r:
+            assert torch.equal(r[n], r2[n]), n
+
+
 def test_same_results_twice_and_on_another_stream():
     d = dev(make(1, 700, 3, 128, 128, seed=630))
     o, S = fwd(d, segment_chunks=2)
