@@ -17,7 +17,7 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 LIB = PKG / "libkda.so"
 SOURCES = ["kda_api.hip", "kda_prep.hip", "kda_recur.hip", "kda_fused.hip", "kda_decode.hip",
-           "kda_split.hip", "kda_bwd.hip", "la_api.hip", "la_chunk.hip", "la_decode.hip",
+           "kda_split.hip", "kda_bwd.hip", "la_api.hip", "la_chunk.hip", "la_narrow.hip", "la_decode.hip",
            "gated_norm.hip"]
 ARCH = "gfx950"
 

@@ -24,26 +24,52 @@ struct LaCall {
     int32_t segments;  // the caller's request: chunks per segment, 0 automatic, < 0 whole
 };
 
-// Segments of a batch (see LaSeqs); dirs: passes with a state pass of their own.
-kda::LaSeqs plan(const LaCall& c) {
-    kda::LaSeqs s{};
+struct LaPlan {
+    kda::LaSeqs s;
+    bool narrow;  // whole sequences in workgroups of a few columns (la_narrow.hip)
+};
+
+// Kernel and segments (see LaSeqs) for `passes` passes over a batch side by side.
+//
+// A workgroup of la_chunk.hip has a (segment, head)'s whole rows, and a CU to itself:
+// with fewer (sequence, head) pairs than CUs a sequence is cut into segments, which
+// costs a second reading of y and z and a wait between two launches.  la_narrow.hip
+// cuts the state's columns instead, which costs nothing but reads x and y once per 32
+// columns and z in 64-byte pieces; its chunk takes 1.2 us, so it wins where the CUs
+// hold all of its workgroups and the sequences are short.  Forward (and backward) of
+// H (sequence, head) pairs, 128 x 128, us:
+//             T = 512     2048        4096          8192
+//   H = 16    14 (16)     43 (45)     81 (83)       155 (158)   narrow
+//             28 (40)     37 (69)     50 (97)        65 (144)   rows, in segments
+//   H = 32    15 (24)     44 (65)     82 (121)      157 (262)   narrow
+//             28 (42)     45 (89)     61 (150)       95 (273)   rows
+//   H = 64    17 (35)     46 (112)    84 (233)      180 (476)   narrow
+//             32 (35)     57 (90)     93 (171)      174 (346)   rows
+// The rule: 512 workgroups of la_narrow.hip are in flight at once, and with s segments
+// to a sequence the other kernel takes about 20 us and 4 us for every s chunks.
+LaPlan plan(const LaCall& c, int passes) {
+    LaPlan p{};
+    kda::LaSeqs& s = p.s;
     s.cu = c.cu;
     s.n_seqs = c.packed ? c.num_seqs : c.B;
     s.T = c.T;
     s.H = c.H;
-    const int64_t tokens = c.packed ? c.T : (int64_t)c.B * c.T;
-    const int64_t chunks = (tokens / s.n_seqs + kda::LA_CHUNK - 1) / kda::LA_CHUNK;  // of an average sequence
-    int64_t per = c.segments;
-    if (c.segments == 0) {
-        const int64_t groups = (int64_t)s.n_seqs * c.H * (c.V / kda::LA_COLS);
-        per = -1;
-        if (groups < 256 && chunks >= 32) {
-            const int64_t segs = std::min<int64_t>((512 + groups - 1) / groups, chunks / 16);
-            if (segs > 1) per = (chunks + segs - 1) / segs;
-        }
-    }
     s.seg_per_seq = 1;
     s.n_slots = s.n_seqs;
+    const int64_t tokens = c.packed ? c.T : (int64_t)c.B * c.T;
+    const int64_t chunks = (tokens / s.n_seqs + kda::LA_CHUNK - 1) / kda::LA_CHUNK;  // of an average sequence
+    const int64_t pairs = (int64_t)s.n_seqs * c.H;
+    const int64_t segs = 256 / (pairs * passes);
+    const int64_t narrow_groups = kda::la_narrow_groups(pairs, std::max(c.K, c.V)) * passes;
+    p.narrow = c.segments <= 0 && narrow_groups <= 512 &&
+               (c.segments < 0 || segs <= 3 || chunks * (6 * segs - 20) <= 100 * segs);
+    if (p.narrow) return p;
+    int64_t per = c.segments;
+    if (c.segments == 0) {
+        per = -1;
+        const int64_t n = std::min<int64_t>(segs, chunks / 3);
+        if (n > 1) per = (chunks + n - 1) / n;
+    }
     // (a segment that holds every token is the whole sequence)
     if (per > 0 && per * kda::LA_CHUNK < c.T) {
         s.seg_tokens = (int32_t)(per * kda::LA_CHUNK);
@@ -54,9 +80,17 @@ kda::LaSeqs plan(const LaCall& c) {
             s.seg_per_seq = (c.T + s.seg_tokens - 1) / s.seg_tokens;
             s.n_slots = (int32_t)std::min<int64_t>((int64_t)s.seg_per_seq * s.n_seqs, INT32_MAX);
         }
+    } else if (c.packed && s.n_seqs <= 64 && pairs * passes > 256) {
+        s.by_length = 1;
     }
-    return s;
+    return p;
 }
+
+// A segment forms its entering state itself where those before it are few, which
+// reads them once more for each segment behind; a scan over many in a launch of its
+// own takes 10 us.  (2 x 2048 tokens, 32 heads, 4 segments: 72 us with the scan, 61
+// without.)
+bool self_entering(const kda::LaSeqs& s) { return (s.T + s.seg_tokens - 1) / s.seg_tokens <= 8; }
 
 size_t la_states_bytes(const LaCall& c, const kda::LaSeqs& s) {
     return s.seg_tokens ? align_up((size_t)s.n_slots * c.H * c.K * c.V * sizeof(float)) : 0;
@@ -70,19 +104,21 @@ bool valid_sizes(const LaCall& c) {
 // workspace bytes (dirs: 1 forward, 2 backward); 0: sizes that are not supported
 size_t la_workspace(const LaCall& c, int dirs) {
     if (!valid_sizes(c)) return 0;
-    const kda::LaSeqs s = plan(c);
+    const kda::LaSeqs s = plan(c, dirs == 2 ? 3 : 1).s;
     return std::max(ALIGN, (size_t)dirs * la_states_bytes(c, s));
 }
 
 // Checks of every pass; fills the plan.
 int check_la(const LaCall& c, float scale, const float* log_decay, const void* ws, size_t ws_bytes, int dirs,
-             kda::LaSeqs& s) {
+             LaPlan& plan_out) {
     if (c.B < 1 || c.T < 0 || c.H < 1) return KDA_ERR_INVALID_ARG;
     if (!supported_dim(c.K) || !supported_dim(c.V)) return KDA_ERR_UNSUPPORTED;
     if ((int64_t)c.B * c.T >= I31 || !std::isfinite(scale) || !log_decay || !aligned(log_decay, 4))
         return KDA_ERR_INVALID_ARG;
+    if (c.H > 65536) return KDA_ERR_INVALID_ARG;  // 32-bit byte offsets within a chunk
     if (c.packed && (c.B != 1 || c.num_seqs < 1 || !aligned(c.cu, 4))) return KDA_ERR_INVALID_ARG;
-    s = plan(c);
+    plan_out = plan(c, dirs == 2 ? 3 : 1);
+    const kda::LaSeqs& s = plan_out.s;
     // one grid over (slot, head, column block), and over (sequence, head, piece of a state)
     if ((int64_t)s.n_slots * c.H >= I31 / 64) return KDA_ERR_INVALID_ARG;
     const size_t need = (size_t)dirs * la_states_bytes(c, s);
@@ -90,14 +126,13 @@ int check_la(const LaCall& c, float scale, const float* log_decay, const void* w
     return KDA_OK;
 }
 
-kda::LaPass make_pass(const uint16_t* x, const uint16_t* y, const uint16_t* z, uint16_t* o, int32_t D2, int32_t row,
-                      int32_t col, bool reverse, float scale) {
+kda::LaPass make_pass(const uint16_t* x, const uint16_t* y, const uint16_t* z, uint16_t* o, int32_t row, int32_t col,
+                      bool reverse, float scale) {
     kda::LaPass p{};
     p.x = x;
     p.y = y;
     p.z = z;
     p.o = o;
-    p.D2 = D2;
     p.row = row;
     p.col = col;
     p.reverse = reverse;
@@ -109,7 +144,7 @@ kda::LaPass make_pass(const uint16_t* x, const uint16_t* y, const uint16_t* z, u
 
 // what each segment adds to the state, for a pass with the states' own [K, V] layout
 void launch_states(const kda::LaSeqs& s, const float* log_decay, const kda::LaPass* p, float* const* out, int n,
-                   int32_t K, hipStream_t stream) {
+                   int32_t K, int32_t V, hipStream_t stream) {
     kda::LaArgs a{};
     a.s = s;
     a.log_decay = log_decay;
@@ -121,7 +156,13 @@ void launch_states(const kda::LaSeqs& s, const float* log_decay, const kda::LaPa
         a.pass[i].s_out = out[i];
         a.pass[i].s_out_slots = 1;
     }
+    a.cols = V;
     kda::launch_la_chunk(a, n, K, true, stream);
+}
+
+void launch(const LaPlan& p, const kda::LaArgs& a, int n, int D1, hipStream_t stream) {
+    if (p.narrow) kda::launch_la_narrow(a, n, D1, stream);
+    else kda::launch_la_chunk(a, n, D1, false, stream);
 }
 
 int status() { return hipGetLastError() == hipSuccess ? KDA_OK : KDA_ERR_LAUNCH; }
@@ -155,9 +196,10 @@ int la_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float*
            int32_t T, int32_t H, int32_t K, int32_t V, uint16_t* o, void* workspace, size_t workspace_bytes,
            int32_t segment_chunks, void* stream) {
     const LaCall c{cu_seqlens, cu_seqlens != nullptr, num_seqs, B, T, H, K, V, segment_chunks};
-    kda::LaSeqs s;
-    const int st = check_la(c, scale, log_decay, workspace, workspace_bytes, 1, s);
+    LaPlan pl;
+    const int st = check_la(c, scale, log_decay, workspace, workspace_bytes, 1, pl);
     if (st != KDA_OK) return st;
+    const kda::LaSeqs& s = pl.s;
     if (T > 0 && (!q || !k || !v || !o)) return KDA_ERR_INVALID_ARG;
     for (const void* p : {(const void*)q, (const void*)k, (const void*)v, (const void*)o, (const void*)initial_state,
                           (const void*)final_state})
@@ -168,24 +210,29 @@ int la_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float*
     a.s = s;
     a.log_decay = log_decay;
     kda::LaPass& p = a.pass[0];
-    p = make_pass(q, k, v, o, V, V, 1, false, scale);
+    p = make_pass(q, k, v, o, V, 1, false, scale);
     p.s_in = initial_state;
     p.s_out = final_state;
     if (s.seg_tokens) {
         float* states = static_cast<float*>(workspace);
-        launch_states(s, log_decay, &p, &states, 1, K, str);
-        kda::LaScanArgs sc{};
-        sc.s = s;
-        sc.log_decay = log_decay;
-        sc.init[0] = initial_state;
-        sc.state[0] = states;
-        sc.elems = K * V;
-        sc.n_dirs = 1;
-        kda::launch_la_scan(sc, str);
-        p.s_in = states;
-        p.s_in_slots = 1;
+        launch_states(s, log_decay, &p, &states, 1, K, V, str);
+        if (self_entering(s)) {
+            p.seg_states = states;
+        } else {
+            kda::LaScanArgs sc{};
+            sc.s = s;
+            sc.log_decay = log_decay;
+            sc.init[0] = initial_state;
+            sc.state[0] = states;
+            sc.elems = K * V;
+            sc.n_dirs = 1;
+            kda::launch_la_scan(sc, str);
+            p.s_in = states;
+            p.s_in_slots = 1;
+        }
     }
-    kda::launch_la_chunk(a, 1, K, false, str);
+    a.cols = V;
+    launch(pl, a, 1, K, str);
     return status();
 }
 
@@ -194,9 +241,10 @@ int la_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float*
            int32_t K, int32_t V, const uint16_t* d_o, const float* d_final, uint16_t* dq, uint16_t* dk, uint16_t* dv,
            float* dh0, void* workspace, size_t workspace_bytes, int32_t segment_chunks, void* stream) {
     const LaCall c{cu_seqlens, cu_seqlens != nullptr, num_seqs, B, T, H, K, V, segment_chunks};
-    kda::LaSeqs s;
-    const int st = check_la(c, scale, log_decay, workspace, workspace_bytes, 2, s);
+    LaPlan pl;
+    const int st = check_la(c, scale, log_decay, workspace, workspace_bytes, 2, pl);
     if (st != KDA_OK) return st;
+    const kda::LaSeqs& s = pl.s;
     if (T > 0 && (!q || !k || !v || !d_o || !dq || !dk || !dv)) return KDA_ERR_INVALID_ARG;
     for (const void* p : {(const void*)q, (const void*)k, (const void*)v, (const void*)d_o, (const void*)dq,
                           (const void*)dk, (const void*)dv, (const void*)initial_state, (const void*)d_final,
@@ -204,30 +252,35 @@ int la_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float*
         if (!aligned(p, 16)) return KDA_ERR_INVALID_ARG;
     const hipStream_t str = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
-    kda::LaPass pq = make_pass(d_o, v, k, dq, K, 1, V, false, scale);
-    kda::LaPass pk = make_pass(v, d_o, q, dk, K, 1, V, true, scale);
-    kda::LaPass pv = make_pass(k, q, d_o, dv, V, V, 1, true, scale);
+    kda::LaPass pq = make_pass(d_o, v, k, dq, 1, V, false, scale);
+    kda::LaPass pk = make_pass(v, d_o, q, dk, 1, V, true, scale);
+    kda::LaPass pv = make_pass(k, q, d_o, dv, V, 1, true, scale);
     pq.s_in = initial_state;
     pk.s_in = pv.s_in = d_final;
     pv.s_out = dh0;
     if (s.seg_tokens) {
         float* states[2] = {static_cast<float*>(workspace),
                             static_cast<float*>(workspace) + la_states_bytes(c, s) / sizeof(float)};
-        const kda::LaPass p[2] = {make_pass(q, k, v, nullptr, V, V, 1, false, scale), pv};
-        launch_states(s, log_decay, p, states, 2, K, str);
-        kda::LaScanArgs sc{};
-        sc.s = s;
-        sc.log_decay = log_decay;
-        sc.init[0] = initial_state;
-        sc.init[1] = d_final;
-        sc.state[0] = states[0];
-        sc.state[1] = states[1];
-        sc.elems = K * V;
-        sc.n_dirs = 2;
-        kda::launch_la_scan(sc, str);
-        pq.s_in = states[0];
-        pk.s_in = pv.s_in = states[1];
-        pq.s_in_slots = pk.s_in_slots = pv.s_in_slots = 1;
+        const kda::LaPass p[2] = {make_pass(q, k, v, nullptr, V, 1, false, scale), pv};
+        launch_states(s, log_decay, p, states, 2, K, V, str);
+        if (self_entering(s)) {
+            pq.seg_states = states[0];
+            pk.seg_states = pv.seg_states = states[1];
+        } else {
+            kda::LaScanArgs sc{};
+            sc.s = s;
+            sc.log_decay = log_decay;
+            sc.init[0] = initial_state;
+            sc.init[1] = d_final;
+            sc.state[0] = states[0];
+            sc.state[1] = states[1];
+            sc.elems = K * V;
+            sc.n_dirs = 2;
+            kda::launch_la_scan(sc, str);
+            pq.s_in = states[0];
+            pk.s_in = pv.s_in = states[1];
+            pq.s_in_slots = pk.s_in_slots = pv.s_in_slots = 1;
+        }
     }
     kda::LaArgs a{};
     a.s = s;
@@ -236,13 +289,16 @@ int la_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float*
         a.pass[0] = pk;
         a.pass[1] = pv;
         a.pass[2] = pq;
-        kda::launch_la_chunk(a, 3, K, false, str);
+        a.cols = V;
+        launch(pl, a, 3, K, str);
     } else {
         a.pass[0] = pk;
         a.pass[1] = pq;
-        kda::launch_la_chunk(a, 2, V, false, str);
+        a.cols = K;
+        launch(pl, a, 2, V, str);
         a.pass[0] = pv;
-        kda::launch_la_chunk(a, 1, K, false, str);
+        a.cols = V;
+        launch(pl, a, 1, K, str);
     }
     return status();
 }

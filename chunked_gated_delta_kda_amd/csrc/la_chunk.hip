@@ -15,432 +15,485 @@
 //   E_(t-1) = a R_t         (the reversed passes' state; E_(-1) = dh0),
 // so one kernel serves all four.
 //
-// One workgroup of four waves per (segment, head, 32 state columns); the
-// column blocks of one head are neighbours on one XCD, whose L2 serves the
-// rows of x and y to all of them.  Per chunk, wave w
-//  - forms P^T for its 16 queries (key tiles 0..w; 16x16x32 MFMAs on the raw
-//    bf16 rows), whose D layout is the operand of the product with z, so P
-//    stays in registers; decays are a table of 16 values a lane;
-//  - adds S^T x from the bf16 copy of S that the waves left in LDS;
-//  - updates its quarter of S (half of the D1 rows, 16 columns) in fp32
-//    accumulators, and leaves its bf16 copy for the next chunk.
-// One barrier a chunk: the y and z tiles and the copy of S are double-buffered.
+// One workgroup of eight waves per (segment, head), alone on its CU (160 KB of LDS):
+//  - four waves move rows: every chunk, x and y two chunks ahead and z one ahead from
+//    memory into LDS (loaded two chunks before that), the outputs from LDS to memory,
+//    whole rows at a time; and they form P^T = in_scale a^(i-j) (x_i . y_j) of the
+//    next chunk (16x16x32 MFMAs on the raw bf16 rows), left in LDS as operands;
+//  - four waves keep the state, D2 / 4 columns each, in fp32 accumulators.  Rounded,
+//    they are the operand of S^T x as they are, so the state never leaves its wave;
+//    y and z are read by transposing reads as operands that contract over tokens.
+// One barrier a chunk.
 //
-// Precision: raw bf16 operands; P and the copy of S are rounded to bf16 once
-// each (outputs are bf16).  The state itself is fp32 to its last bits, since
-// it is returned: a token's decayed z is split into three bf16 terms (24
-// bits), so every product of the update is exact, and the decay of a chunk is
-// applied as S + (a^n - 1) S where a^n is near one, or the rounding of a^n
-// would add up over thousands of chunks.
-#include "kda_common.h"
-#include "la_launch.h"
+// What bounds it: of 256 workgroups in flight each chunk costs a SIMD 152 products of 16
+// cycles and about 700 other vector instructions, which overlap for a fifth only: 5200
+// cycles, 2.3 us, in which the CUs move 64 KB each, 7 TB/s if all were equal.  So long
+// batches are bound by instruction issue and by their last workgroups, not by memory:
+// 16 sequences of 256 to 8192 tokens, 32 heads of 128 x 128, take 595 us (2.55 GB,
+// 4.3 TB/s; the bytes alone take 520 us).  Measured on the way there (the same batch):
+// 32 columns a workgroup in waves that read z in 64-byte pieces 820 us; eight state
+// waves of 16 columns, which read x and y from LDS twice as often, 615; products and
+// conversions in the compiler's own order 616; one state wave per SIMD with the order
+// written out 595.
+//
+// Precision: raw bf16 operands; P and the copy of S are rounded to bf16 once each
+// (outputs are bf16).  The state itself is fp32 to its last bits where it is returned:
+// a token's decayed z is split into three bf16 terms (24 bits), so every product of
+// the update is exact, and the decays of the chunks do not drift from a's powers
+// (ChunkDecay).  Where no state is returned two terms (16 bits) are enough, since
+// the state is then only read through its rounding to 8 bits: 11% of a backward pass.
+#include "la_device.h"
 
 namespace kda {
 
-namespace {
+template <int D1, int D2, int TERMS, bool STATES>
+__global__ __launch_bounds__(512, 2) void la_chunk_kernel(LaArgs a) {
+    constexpr int NC = D2 / 64;            // 16-column tiles of each of the four state waves
+    constexpr int KS = D1 / 32;            // 16x16x32 steps over D1
+    constexpr int NT = D1 / 16;            // state tiles of a wave
+    // the four waves that move rows: 16-byte pieces of an x or y tile (of a z tile)
+    // per thread, threads per row, rows that they cover at once
+    constexpr int RV = D1 / 32, RT = D1 / 8, RROWS = 256 / RT;
+    constexpr int ZV = D2 / 32, ZT = D2 / 8, ZROWS = 256 / ZT;
+    constexpr int PT = 3;                  // tiles of P per wave, at most
+    __shared__ __align__(16) bf16 xtile[STATES ? 1 : 3][STATES ? 8 : LC * D1];
+    __shared__ __align__(16) bf16 ytile[3][LC * D1];
+    __shared__ __align__(16) bf16 ztile[3][LC * D2];
+    __shared__ bf16x8 pfrag[STATES ? 1 : 2][6][STATES ? 1 : 64];
 
-constexpr int LC = LA_CHUNK;
-
-// the type's lowest log decay that matters: exp(-200) is zero in fp32 twice over
-constexpr float LOG_DECAY_FLOOR = -200.f;
-
-__device__ __forceinline__ float head_log_decay(const float* p, int h) {
-    const float v = p[h];
-    return v < LOG_DECAY_FLOOR ? LOG_DECAY_FLOOR : v;  // keeps a NaN
-}
-
-// a segment: tokens t0 .. t0 + len of sequence n, positions p0 .. p1
-struct Seg {
-    int n;
-    int t0, len;
-    int p0, p1;
-};
-
-__device__ __forceinline__ int clamp_tok(const LaSeqs& s, int v) { return min(max(v, 0), s.T); }
-
-// The segment of a slot; false if the slot holds none.  Offsets are clamped
-// to the batch, so an array that is not what it should be gives wrong
-// results, never an access out of bounds.
-__device__ __forceinline__ bool find_seg(const LaSeqs& s, int slot, Seg& g) {
-    int seg;
-    if (!s.cu) {
-        g.n = slot / s.seg_per_seq;
-        seg = slot % s.seg_per_seq;
-        g.t0 = g.n * s.T;
-        g.len = s.T;
-    } else {
-        int n = slot;
-        seg = 0;
-        if (s.seg_tokens) {
-            // the last sequence whose first slot is not behind this one: 64
-            // candidates at a time
-            const int lane = threadIdx.x & 63;
-            int lo = 0, cnt = s.n_seqs;
-            for (;;) {
-                const int step = (cnt + 63) / 64;
-                const int i = lo + lane * step;
-                const bool le = lane * step < cnt &&
-                                clamp_tok(s, s.cu[min(i, s.n_seqs)]) / s.seg_tokens + i <= slot;
-                const int k = __popcll(__ballot(le)) - 1;
-                if (k < 0) return false;
-                lo += k * step;
-                if (step == 1) break;
-                cnt = min(step, cnt - k * step);
-            }
-            n = lo;
-            seg = slot - (clamp_tok(s, s.cu[n]) / s.seg_tokens + n);
-        }
-        g.n = n;
-        g.t0 = clamp_tok(s, s.cu[n]);
-        g.len = max(clamp_tok(s, s.cu[n + 1]) - g.t0, 0);
-    }
-    if (!s.seg_tokens) {
-        g.p0 = 0;
-        g.p1 = g.len;
-        return true;
-    }
-    if (seg > 0 && (int64_t)seg * s.seg_tokens >= g.len) return false;
-    g.p0 = seg * s.seg_tokens;
-    g.p1 = g.p0 + min(g.len - g.p0, s.seg_tokens);
-    return true;
-}
-
-// Row r of tile t of the state (and of an operand that contracts over the
-// chunk's tokens): channel 32 (t / 2) + 8 (r / 4) + 4 (t % 2) + r % 4, so the
-// accumulators of tiles 2j and 2j+1 are the eight channels 32 j + 8 g + e of
-// the operand of a product that contracts over them.
-
-// Operand that contracts over tokens: lane (r, g) receives rows 4 g .. 4 g + 3,
-// column channel(t, r) of 16 rows of an LDS tile, by one transposing read
-// (ds_read_b64_tr_b16): in each group of 16 lanes, lane r fetches four
-// consecutive columns of row 4 g + r / 4, those that lanes 4 (r % 4) .. + 3
-// receive.
-__device__ __forceinline__ bf16x4 read_t(const bf16* p) {
-    typedef __attribute__((address_space(3))) short4_t* lds_short4;
-    return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4)p));
-}
-
-__device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-
-// The y tile holds its rows without padding (two workgroups of 80 KB share a
-// CU's LDS); 16-byte unit u of row m sits at unit u ^ swizzle(m).  Sixteen rows
-// of one unit (the P products) then lie in sixteen different units, and the
-// four rows of a transposing read in four different 64-byte blocks.
-template <int D1>
-__device__ __forceinline__ int swizzle(int m) {
-    return D1 == 128 ? 4 * (m & 3) + ((m >> 2) & 3) : 4 * ((m >> 1) & 1) + ((m >> 2) & 3);
-}
-
-}  // namespace
-
-template <int D1, bool STATES>
-__global__ __launch_bounds__(STATES ? 256 : 512, STATES ? 2 : 4) void la_chunk_kernel(LaArgs a) {
-    constexpr int KS = D1 / 32;       // 16x16x32 steps over D1
-    constexpr int NT = D1 / 32;       // state tiles of a wave (half of D1 / 16)
-    constexpr int YV = D1 / 32;       // 16-byte pieces of the y tile per thread of its four waves
-    constexpr int TPR = D1 / 8;       // threads per row of the y tile
-    constexpr int YROWS = 256 / TPR;  // rows they cover at once
-    __shared__ __align__(16) bf16 ytile[2][LC * D1];
-    __shared__ __align__(16) bf16 ztile[STATES ? 1 : 2][LC * LA_COLS];
-    __shared__ __align__(16) bf16 zterm[2][3][LC * LA_COLS];
-    __shared__ u32x4 scopy[STATES ? 1 : 2][2][STATES ? 1 : KS][64];
-
-    const LaPass& p = a.pass[blockIdx.y];
+    const LaPass p = a.pass[blockIdx.y];
     const int H = a.s.H;
-    const int ncb = p.D2 / LA_COLS;
-    // workgroups are dealt to the eight XCDs in turn: the column blocks of one
-    // (segment, head) follow each other on one of them
-    const int64_t b = blockIdx.x;
-    const int64_t group = (b / 8 / ncb) * 8 + b % 8;
-    const int cb = (int)(b / 8 % ncb);
-    if (group >= (int64_t)a.s.n_slots * H) return;
-    const int slot = (int)(group / H), h = (int)(group % H);
+    const int slot = (int)(blockIdx.x / H), h = (int)(blockIdx.x % H);
     Seg sg;
     if (!find_seg(a.s, slot, sg)) return;
-    if (STATES && sg.p1 == sg.len) return;  // nobody enters from a sequence's last segment
+    const float ld = head_log_decay(a.log_decay, h);
+    const float l2 = ld * LOG2E;
+    if constexpr (STATES) {
+        if (sg.p1 == sg.len) return;  // nobody enters from a sequence's last segment
+    }
 
-    const int tid = threadIdx.x & 255;  // within the four waves of a role
-    const int lane = tid & 63, r = lane & 15, g = lane >> 4;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const bool out_role = !STATES && __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) == 0;
-    const int D2 = p.D2, c0 = cb * LA_COLS;
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const bool mover = wave < 4;
     const int late = p.reverse ? 1 : 0;
 
     if (!STATES && a.s.cu && sg.p0 == 0 && (sg.n == 0 || sg.n == a.s.n_seqs - 1)) {
         // rows outside every sequence: zeros
         auto zero_rows = [&](int lo, int hi) {
-            for (int t = lo + ((int)threadIdx.x >> 2); t < hi; t += 128)
-                *reinterpret_cast<u32x4*>(p.o + ((int64_t)t * H + h) * D2 + c0 + 8 * (tid & 3)) = u32x4{0, 0, 0, 0};
+            for (int t = lo + (int)threadIdx.x / ZT; t < hi; t += 512 / ZT)
+                *reinterpret_cast<u32x4*>(p.o + ((int64_t)t * H + h) * D2 + 8 * (threadIdx.x % ZT)) = u32x4{0, 0, 0, 0};
         };
         if (sg.n == 0) zero_rows(0, sg.t0);
         if (sg.n == a.s.n_seqs - 1) zero_rows(sg.t0 + sg.len, a.s.T);
     }
 
-    const float ld = head_log_decay(a.log_decay, h);
-    const float l2 = ld * LOG2E;
-
-    // ---- rows of x, y, z at a position.  Positions behind the segment's end
-    // read its last row, whose weight in the state is then zero and whose
-    // output is not stored: every load is unconditional.
+    // ---- rows of x, y, z of a chunk: a uniform base and a 32-bit byte offset
+    // per row.  Positions behind the segment's end read its last row, whose
+    // weight in the state is then zero and whose output is not stored, and
+    // chunks behind the last one read that one: every load is unconditional.
+    // (In reverse the base is the chunk's last position, the lowest address.)
     const int np = sg.p1 - sg.p0, nc = (np + LC - 1) / LC;
-    const int64_t step = p.reverse ? -1 : 1;
-    const int64_t tok0 = p.reverse ? (int64_t)sg.t0 + sg.len - 1 - sg.p0 : (int64_t)sg.t0 + sg.p0;
-    const int64_t ystep = step * H * D1, zstep = step * H * D2;
-    auto at = [&](int c, int row) { return (int64_t)min(c * LC + row, np - 1); };
+    const int64_t first = p.reverse ? (int64_t)sg.t0 + sg.len - LC - sg.p0 : (int64_t)sg.t0 + sg.p0;
+    const int64_t x_first = (first * H + h) * (D1 * 2), z_first = (first * H + h) * (D2 * 2);
+    const int64_t x_step = (p.reverse ? -1 : 1) * (int64_t)LC * H * (D1 * 2);
+    const int64_t z_step = (p.reverse ? -1 : 1) * (int64_t)LC * H * (D2 * 2);
+    const uint32_t x_row = (uint32_t)H * (D1 * 2), z_row = (uint32_t)H * (D2 * 2);
+    auto offset = [&](int row, uint32_t bytes) { return (uint32_t)(p.reverse ? LC - 1 - row : row) * bytes; };
+    auto load16 = [](const char* base, uint32_t o) { return *reinterpret_cast<const u32x4*>(base + o); };
+    const char* const x_ptr = reinterpret_cast<const char*>(p.x) + x_first;
+    const char* const y_ptr = reinterpret_cast<const char*>(p.y) + x_first;
+    const char* const z_ptr = reinterpret_cast<const char*>(p.z) + z_first;
+    char* const o_ptr = reinterpret_cast<char*>(p.o) + z_first;
 
-    // z of a chunk: one 16-byte piece a thread, left in LDS as it is and, decayed
-    // to the chunk's end, as three bf16 terms
-    const uint16_t* const zrow = p.z + (tok0 * H + h) * D2 + c0 + 8 * (tid & 3);
-    auto load_z = [&](int c) { return *reinterpret_cast<const u32x4*>(zrow + at(c, tid >> 2) * zstep); };
-    const float z_full = exp2_hw((LC - 1 - (tid >> 2) + late) * l2) * p.z_scale;
-    auto put_z = [&](int c, u32x4 raw) {
-        const int n = np - c * LC, row = tid >> 2;
-        float wt = z_full;
-        if (n < LC) wt = row < n ? exp2_hw((n - 1 - row + late) * l2) * p.z_scale : 0.f;
-        const bf16x8 z = __builtin_bit_cast(bf16x8, raw);
-        bf16x8 term[3];
+    // LDS reads of a tile's rows 16 t + r, channels 32 j + 8 g (an operand that
+    // contracts over channels)
+    int row_off[KS];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float v = (float)z[e] * wt;
-#pragma unroll
-            for (int q = 0; q < 3; ++q) {
-                term[q][e] = (bf16)v;
-                v -= (float)term[q][e];
-            }
-        }
-        if constexpr (!STATES) *reinterpret_cast<u32x4*>(&ztile[c & 1][8 * tid]) = raw;
-#pragma unroll
-        for (int q = 0; q < 3; ++q) *reinterpret_cast<bf16x8*>(&zterm[c & 1][q][8 * tid]) = term[q];
+    for (int j = 0; j < KS; ++j) row_off[j] = r * D1 + 8 * ((4 * j + g) ^ swizzle<D1>(r));
+    auto row_frag = [&](const bf16* tile, int t, int j) __attribute__((always_inline)) {
+        return *reinterpret_cast<const bf16x8*>(tile + 16 * t * D1 + row_off[j]);
     };
-    // where a transposing read of a z tile starts (tile ct of 16 columns: + 4 ct)
-    const int zt_off = (4 * g + (r >> 2)) * LA_COLS + 8 * (r & 3);
 
-    if (out_role) {
+    if (mover) {
         if (nc == 0) return;
-        // ================= outputs: wave w owns the chunk's queries 16 w + r
-        auto outputs = [&](auto wc) __attribute__((always_inline)) {
-            constexpr int W = decltype(wc)::value;
-            const int i0 = 16 * W + r;
-            const uint16_t* const xrow = p.x + (tok0 * H + h) * D1 + 8 * g;
-            uint16_t* const orow = p.o + (tok0 * H + h) * D2 + c0 + 8 * g;
-            const float up = exp2_hw((i0 + 1 - late) * l2) * p.x_scale;
-            float dec[W + 1][4];  // decay from key 16 (W - d) + 4 g + i
+        // ================= rows and P.  In interval c these waves leave x and y of
+        // chunk c + 2, z of c + 1 and P of c + 1 in LDS, and store the outputs of
+        // chunk c - 1, which the state waves left in place of its z.
+        const int tid = threadIdx.x;
+        const int r_row = tid / RT, r_unit = tid % RT, z_trow = tid / ZT, z_unit = tid % ZT;
+        auto load_rows = [&](const char* ptr, int c, u32x4 (&v)[RV]) __attribute__((always_inline)) {
+            c = min(c, nc - 1);
+            const int last = np - 1 - c * LC;
+            uint32_t o[RV];
 #pragma unroll
-            for (int d = 0; d <= W; ++d)
+            for (int i = 0; i < RV; ++i) o[i] = offset(r_row + i * RROWS, x_row);
+            if (last < LC - 1) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) dec[d][i] = exp2_hw(max(16 * d + r - 4 * g - i, 0) * l2) * p.in_scale;
-            int koff[KS];
-#pragma unroll
-            for (int j = 0; j < KS; ++j) koff[j] = r * D1 + 8 * ((4 * j + g) ^ swizzle<D1>(r));
-
-            u32x4 xs[2][KS], zs[2];
-            auto load_x = [&](int c, u32x4 (&x)[KS]) __attribute__((always_inline)) {
-                const uint16_t* q = xrow + at(c, i0) * ystep;
-#pragma unroll
-                for (int j = 0; j < KS; ++j) x[j] = *reinterpret_cast<const u32x4*>(q + 32 * j);
-            };
-            {
-                const u32x4 z0 = load_z(0);
-                load_x(0, xs[0]);
-                zs[1] = load_z(1);
-                load_x(1, xs[1]);
-                zs[0] = load_z(2);
-                put_z(0, z0);
+                for (int i = 0; i < RV; ++i) o[i] = offset(min(r_row + i * RROWS, last), x_row);
             }
-            __syncthreads();
-            // chunk c from x; z holds chunk c + 1, and takes chunk c + 3
-            auto chunk = [&](int c, u32x4 (&x)[KS], u32x4& z, auto full) __attribute__((always_inline)) {
-                const int buf = c & 1;
-                const bf16* yt = ytile[buf];
-                const bf16* zt = ztile[buf] + zt_off;
-                if (c + 1 < nc) put_z(c + 1, z);
-                z = load_z(c + 3);
-                // S^T x: D rows are the columns channel(ct, .), D columns the queries
-                floatx4 acc[2];
 #pragma unroll
-                for (int ct = 0; ct < 2; ++ct) {
-                    acc[ct] = floatx4{0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < RV; ++i) v[i] = load16(ptr + c * x_step, o[i] + 16 * r_unit);
+        };
+        auto load_z = [&](int c, u32x4 (&v)[ZV]) __attribute__((always_inline)) {
+            c = min(c, nc - 1);
+            const int last = np - 1 - c * LC;
+            uint32_t o[ZV];
 #pragma unroll
-                    for (int j = 0; j < KS; ++j)
-                        acc[ct] = mfma32(__builtin_bit_cast(bf16x8, scopy[buf][ct][j][lane]), __builtin_bit_cast(bf16x8, x[j]), acc[ct]);
-                }
-                // P^T of the key tiles W, W - 1, ...
-                floatx4 pt[W + 1];
+            for (int i = 0; i < ZV; ++i) o[i] = offset(z_trow + i * ZROWS, z_row);
+            if (last < LC - 1) {
 #pragma unroll
-                for (int d = 0; d <= W; ++d) {
-                    pt[d] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int j = 0; j < KS; ++j)
-                        pt[d] = mfma32(*reinterpret_cast<const bf16x8*>(yt + 16 * (W - d) * D1 + koff[j]), __builtin_bit_cast(bf16x8, x[j]), pt[d]);
-                }
-                load_x(c + 2, x);
-                acc[0] *= up;
-                acc[1] *= up;
-                bf16x4 pf[W + 1];
-#pragma unroll
-                for (int d = 0; d <= W; ++d) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        pt[d][i] *= dec[d][i];
-                        if (d == 0 && r < 4 * g + i) pt[d][i] = 0.f;
-                    }
-                    pf[d] = to_bf16x4(pt[d]);
-                }
-                // (P z), two key tiles at a time; a last odd one is padded with zeros.
-                // (Not by a 16x16x16 product: issued right behind the 16x16x32 one
-                // whose result it adds to, it read two stale accumulators now and then.)
-                const bf16x4 none = {};
-#pragma unroll
-                for (int d = 0; d <= W; d += 2)
-#pragma unroll
-                    for (int ct = 0; ct < 2; ++ct) {
-                        const bf16* z0 = zt + 16 * (W - d) * LA_COLS + 4 * ct;
-                        acc[ct] = mfma32(join(read_t(z0), d < W ? read_t(z0 - 16 * LA_COLS) : none),
-                                         join(pf[d], d < W ? pf[d < W ? d + 1 : d] : none), acc[ct]);
-                    }
-                const u32x4 ov = __builtin_bit_cast(u32x4, join(to_bf16x4(acc[0]), to_bf16x4(acc[1])));
-                uint16_t* o = orow + at(c, i0) * zstep;
-                if (decltype(full)::value || c * LC + i0 < np) *reinterpret_cast<u32x4*>(o) = ov;
-                if (c + 1 < nc) __syncthreads();
-            };
-            const int nf = np / LC;  // full chunks
-            int c = 0;
-            for (; c + 1 < nf; c += 2) {
-                chunk(c, xs[0], zs[1], std::true_type{});
-                chunk(c + 1, xs[1], zs[0], std::true_type{});
+                for (int i = 0; i < ZV; ++i) o[i] = offset(min(z_trow + i * ZROWS, last), z_row);
             }
-            if (c < nf) {
-                chunk(c, xs[0], zs[1], std::true_type{});
-                if (nf < nc) chunk(c + 1, xs[1], zs[0], std::false_type{});
-            } else if (nf < nc) {
-                chunk(c, xs[0], zs[1], std::false_type{});
+#pragma unroll
+            for (int i = 0; i < ZV; ++i) v[i] = load16(z_ptr + c * z_step, o[i] + 16 * z_unit);
+        };
+        auto put_rows = [&](bf16* tile, const u32x4 (&v)[RV]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < RV; ++i) {
+                const int row = r_row + i * RROWS;
+                *reinterpret_cast<u32x4*>(tile + row * D1 + 8 * (r_unit ^ swizzle<D1>(row))) = v[i];
             }
         };
-        if (w == 0) outputs(std::integral_constant<int, 0>{});
-        else if (w == 1) outputs(std::integral_constant<int, 1>{});
-        else if (w == 2) outputs(std::integral_constant<int, 2>{});
-        else outputs(std::integral_constant<int, 3>{});
+        auto z_piece = [&](int c, int i) __attribute__((always_inline)) {
+            const int row = z_trow + i * ZROWS;
+            return reinterpret_cast<u32x4*>(&ztile[c % 3][row * D2 + 8 * (z_unit ^ swizzle<D2>(row))]);
+        };
+        auto put_z = [&](int c, const u32x4 (&v)[ZV]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < ZV; ++i) *z_piece(c, i) = v[i];
+        };
+        auto store_rows = [&](int c, auto full) __attribute__((always_inline)) {
+            u32x4 v[ZV];
+#pragma unroll
+            for (int i = 0; i < ZV; ++i) v[i] = *z_piece(c, i);
+#pragma unroll
+            for (int i = 0; i < ZV; ++i) {
+                const int row = z_trow + i * ZROWS;
+                if (decltype(full)::value || c * LC + row < np)
+                    *reinterpret_cast<u32x4*>(o_ptr + c * z_step + (offset(row, z_row) + 16 * z_unit)) = v[i];
+            }
+        };
+        // P^T of chunk c, by tiles (key tile k, query tile q), left as halves of the
+        // operands of P z: (q, key tiles 0 and 1), and for q = 2, 3 (q, key tiles 2 and 3)
+        int pk[PT], pq[PT];
+        float dec[PT][4];
+#pragma unroll
+        for (int i = 0; i < PT; ++i) {
+            const int t = wave + 4 * i;  // 0..3: the first row of keys, then 4..6, 7..8, 9
+            pk[i] = t < 4 ? 0 : t < 7 ? 1 : t < 9 ? 2 : 3;
+            pq[i] = t < 4 ? t : t < 7 ? t - 3 : t < 9 ? t - 5 : 3;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                dec[i][e] = exp2_hw(max(16 * (pq[i] - pk[i]) + r - 4 * g - e, 0) * l2) * p.in_scale;
+        }
+        auto scores = [&](int c) __attribute__((always_inline)) {
+            const bf16* xt = xtile[c % 3];
+            const bf16* yt = ytile[c % 3];
+#pragma unroll
+            for (int i = 0; i < PT; ++i) {
+                if (i == 2 && wave >= 2) continue;
+                floatx4 t;
+#pragma unroll
+                for (int j = 0; j < KS; ++j)
+                    t = mfma32(row_frag(yt, pk[i], j), row_frag(xt, pq[i], j), j ? t : floatx4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    t[e] *= dec[i][e];
+                    if (pk[i] == pq[i] && r < 4 * g + e) t[e] = 0.f;
+                }
+                const int f = pk[i] < 2 ? pq[i] : pq[i] + 2;
+                reinterpret_cast<bf16x4*>(&pfrag[c & 1][f][lane])[pk[i] & 1] = to_bf16x4(t);
+            }
+        };
+
+        // one or two chunks ahead in registers, what they have room for
+        constexpr int SETS = 2;
+        u32x4 xr[SETS][RV], yr[SETS][RV], zr[SETS][ZV];
+        {
+            u32x4 x0[RV], y0[RV], z0[ZV], x1[RV], y1[RV];
+            if constexpr (!STATES) load_rows(x_ptr, 0, x0);
+            load_rows(y_ptr, 0, y0);
+            load_z(0, z0);
+            if constexpr (!STATES) load_rows(x_ptr, 1, x1);
+            load_rows(y_ptr, 1, y1);
+#pragma unroll
+            for (int k = 0; k < SETS; ++k) {
+                load_z(1 + k, zr[k]);
+                if constexpr (!STATES) load_rows(x_ptr, 2 + k, xr[k]);
+                load_rows(y_ptr, 2 + k, yr[k]);
+            }
+            if constexpr (!STATES) put_rows(xtile[0], x0);
+            put_rows(ytile[0], y0);
+            put_z(0, z0);
+            if constexpr (!STATES) put_rows(xtile[1], x1);
+            put_rows(ytile[1], y1);
+            // the halves that no tile of P fills
+            if (!STATES && wave < 2) {
+                reinterpret_cast<bf16x4*>(&pfrag[wave][0][lane])[1] = bf16x4{};
+                reinterpret_cast<bf16x4*>(&pfrag[wave][4][lane])[1] = bf16x4{};
+            }
+        }
+        __syncthreads();
+        if constexpr (!STATES) {
+            scores(0);
+            __syncthreads();
+        }
+        auto interval = [&](int c, u32x4 (&x)[RV], u32x4 (&y)[RV], u32x4 (&z)[ZV]) __attribute__((always_inline)) {
+            if constexpr (!STATES) {
+                if (c > 0) store_rows(c - 1, std::true_type{});
+                scores(c + 1);
+                put_rows(xtile[(c + 2) % 3], x);
+            }
+            put_rows(ytile[(c + 2) % 3], y);
+            put_z(c + 1, z);
+            if constexpr (!STATES) load_rows(x_ptr, c + 2 + SETS, x);
+            load_rows(y_ptr, c + 2 + SETS, y);
+            load_z(c + 1 + SETS, z);
+            __syncthreads();
+        };
+        int c = 0;
+        for (; c + SETS < nc; c += SETS) {
+            interval(c, xr[0], yr[0], zr[0]);
+            if constexpr (SETS == 2) interval(c + 1, xr[1], yr[1], zr[1]);
+        }
+        if (c + 1 < nc) interval(c, xr[0], yr[0], zr[0]);
+        if (!STATES && nc > 1) store_rows(nc - 2, std::true_type{});
+        __syncthreads();
+        if constexpr (!STATES) store_rows(nc - 1, std::false_type{});
         return;
     }
 
-    // ================= the state: wave w owns half the D1 rows and 16 columns.
-    // Accumulator element i of tile kt is row channel(kh NT + kt, 4 g + i),
-    // column c0 + channel(vh, r).
-    const int kh = w >> 1, vh = w & 1;
-    floatx4 S[NT];
-    const int64_t sz = (int64_t)D1 * D2;
-    const int scol = c0 + tile_channel(vh, r);
-    if (p.s_in) {
-        const float* s = p.s_in + ((int64_t)(p.s_in_slots ? slot : sg.n) * H + h) * sz + (int64_t)scol * p.col;
+    // ================= the state.  Wave w owns columns 16 NC w .. over all rows:
+    // accumulator element i of tile (n, kt) is row channel(kt, 4 g + i), column
+    // 16 (NC w + n) + r; so S, rounded, is the operand of S^T x without leaving its wave.
+    const int w = wave - 4;
+    floatx4 S[NC][NT];
+    const int64_t state_at = (int64_t)(16 * NC * w + r) * p.col;
 #pragma unroll
-        for (int kt = 0; kt < NT; ++kt)
+    for (int n = 0; n < NC; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) S[kt][i] = s[tile_channel(kh * NT + kt, 4 * g + i) * p.row];
-    } else {
+        for (int kt = 0; kt < NT; ++kt) S[n][kt] = floatx4{0.f, 0.f, 0.f, 0.f};
+    auto add_state = [&](const float* t, int64_t at) __attribute__((always_inline)) {
+        t += (at * H + h) * (D1 * D2) + state_at;
 #pragma unroll
-        for (int kt = 0; kt < NT; ++kt) S[kt] = floatx4{0.f, 0.f, 0.f, 0.f};
-    }
-    if (nc > 0) {
-        float c_s0, c_s1;  // a chunk's decay, as c_s0 S + c_s1 S
-        auto set_decay = [&](int n) {
-            const float x = n * ld;
-            const bool near = x > -0.6f;
-            c_s0 = near ? 1.f : 0.f;
-            c_s1 = near ? expm1f(x) : exp2_hw(n * l2);
-        };
-        const uint16_t* const yrow = p.y + (tok0 * H + h) * D1 + 8 * (tid % TPR);
-        bf16* const yput = &ytile[0][(tid / TPR) * D1 + 8 * ((tid % TPR) ^ swizzle<D1>(tid / TPR))];
-        auto load_y = [&](int c, u32x4 (&y)[YV]) __attribute__((always_inline)) {
-#pragma unroll
-            for (int i = 0; i < YV; ++i) y[i] = *reinterpret_cast<const u32x4*>(yrow + at(c, tid / TPR + i * YROWS) * ystep);
-        };
-        auto put_y = [&](int c, const u32x4 (&y)[YV]) __attribute__((always_inline)) {
-#pragma unroll
-            for (int i = 0; i < YV; ++i) *reinterpret_cast<u32x4*>(yput + (c & 1) * LC * D1 + i * YROWS * D1) = y[i];
-        };
-        auto put_s = [&](int buf) __attribute__((always_inline)) {
-            if constexpr (!STATES) {
-#pragma unroll
-                for (int j = 0; j < NT / 2; ++j) {
-                    const bf16x8 f = join(to_bf16x4(S[2 * j]), to_bf16x4(S[2 * j + 1]));
-                    scopy[buf][vh][kh * (NT / 2) + j][lane] = __builtin_bit_cast(u32x4, f);
-                }
-            }
-        };
-        int yt_off[NT / 2];  // transposing reads of y, tiles 2 T and 2 T + 1 of this wave
-#pragma unroll
-        for (int j = 0; j < NT / 2; ++j)
-            yt_off[j] = (4 * g + (r >> 2)) * D1 + 8 * ((4 * (kh * (NT / 2) + j) + (r & 3)) ^ swizzle<D1>(4 * g + (r >> 2)));
-
-        u32x4 ys[2][YV], zs[2];
-        {
-            u32x4 y0[YV];
-            load_y(0, y0);
-            u32x4 z0;
-            if constexpr (STATES) z0 = load_z(0);
-            load_y(1, ys[1]);
-            if constexpr (STATES) zs[1] = load_z(1);
-            load_y(2, ys[0]);
-            if constexpr (STATES) zs[0] = load_z(2);
-            set_decay(min(np, LC));
-            put_y(0, y0);
-            if constexpr (STATES) put_z(0, z0);
-            put_s(0);
-        }
-        __syncthreads();
-        // chunk c; y (and z) hold chunk c + 1, and take chunk c + 3
-        auto chunk = [&](int c, u32x4 (&y)[YV], u32x4& z) __attribute__((always_inline)) {
-            const int buf = c & 1;
-            if (c + 1 < nc) {
-                put_y(c + 1, y);
-                if constexpr (STATES) put_z(c + 1, z);
-            }
-            load_y(c + 3, y);
-            if constexpr (STATES) z = load_z(c + 3);
-            const int n = np - c * LC;
-            if (n < LC && c > 0) set_decay(n);
+        for (int n = 0; n < NC; ++n) {
+            floatx4 u[NT];  // (all loads before the first sum)
 #pragma unroll
             for (int kt = 0; kt < NT; ++kt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) S[kt][i] = fmaf(S[kt][i], c_s1, S[kt][i] * c_s0);
-            const bf16* yt = ytile[buf];
+                for (int i = 0; i < 4; ++i) u[kt][i] = t[tile_channel(kt, 4 * g + i) * p.row + 16 * n * p.col];
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                bf16x8 z3[3];
+            for (int kt = 0; kt < NT; ++kt) S[n][kt] += u[kt];
+        }
+    };
+    if constexpr (!STATES) {
+        if (p.s_in) add_state(p.s_in, p.s_in_slots ? slot : sg.n);
+        if (p.seg_states && sg.p0 > 0) {
+            // the segments before: E <- a^seg_tokens E + what each adds
+            const int before = sg.p0 / a.s.seg_tokens;
+            const float x = ld * (float)a.s.seg_tokens;
+            const bool near = x > -0.6f;
+            const float m0 = near ? 1.f : 0.f, m1 = near ? expm1f(x) : exp2_hw(l2 * (float)a.s.seg_tokens);
+            for (int i = 0; i < before; ++i) {
 #pragma unroll
-                for (int q = 0; q < 3; ++q) {
-                    const bf16* z0 = zterm[buf][q] + 32 * m * LA_COLS + zt_off + 4 * vh;
-                    z3[q] = join(read_t(z0), read_t(z0 + 16 * LA_COLS));
-                }
+                for (int n = 0; n < NC; ++n)
 #pragma unroll
-                for (int kt = 0; kt < NT; ++kt) {
-                    const bf16* y0 = yt + 32 * m * D1 + yt_off[kt / 2] + 4 * (kt & 1);
-                    const bf16x8 yf = join(read_t(y0), read_t(y0 + 16 * D1));
+                    for (int kt = 0; kt < NT; ++kt)
 #pragma unroll
-                    for (int q = 2; q >= 0; --q) S[kt] = mfma32(yf, z3[q], S[kt]);
-                }
+                        for (int e = 0; e < 4; ++e) S[n][kt][e] = fmaf(S[n][kt][e], m1, S[n][kt][e] * m0);
+                add_state(p.seg_states, slot - before + i);
             }
-            if (c + 1 < nc) {
-                put_s(buf ^ 1);
-                __syncthreads();
+        }
+    }
+    if (nc > 0) {
+        ChunkDecay chunk_decay(ld);
+        float decay, wt[2][8];
+        // (a chunk's decay and its tokens' weights)
+        auto set_chunk = [&](int n) __attribute__((always_inline)) {
+            if (n < LC) decay = exp2_hw(n * l2);
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int t = 32 * m + 16 * (e >> 2) + 4 * g + (e & 3);
+                    wt[m][e] = t < n ? exp2_hw((n - 1 - t + late) * l2) * p.z_scale : 0.f;
+                }
+        };
+        set_chunk(LC);
+        float up[4];  // decay of the entering state at query 16 q + r
+#pragma unroll
+        for (int q = 0; q < 4; ++q) up[q] = exp2_hw((16 * q + r + 1 - late) * l2) * p.x_scale;
+        // transposing reads of y (tiles 2 T and 2 T + 1) and of the wave's z columns
+        const int t_row = 4 * g + (r >> 2);
+        int y_off[NT / 2], z_off[NC], o_off[NC];
+#pragma unroll
+        for (int T = 0; T < NT / 2; ++T) y_off[T] = t_row * D1 + 8 * ((4 * T + (r & 3)) ^ swizzle<D1>(t_row));
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+            z_off[n] = t_row * D2 + 8 * ((2 * (NC * w + n) + ((r & 3) >> 1)) ^ swizzle<D2>(t_row)) + 4 * (r & 1);
+            o_off[n] = r * D2 + 8 * ((2 * (NC * w + n) + (g >> 1)) ^ swizzle<D2>(r)) + 4 * (g & 1);
+        }
+
+        __syncthreads();
+        if constexpr (!STATES) __syncthreads();
+        // S, rounded: the operands of S^T x
+        bf16x8 sf[NC][KS];
+        auto round_state = [&](int n, int j) __attribute__((always_inline)) {
+            if constexpr (!STATES) {
+                sf[n][j] = join(to_bf16x4(S[n][2 * j]), to_bf16x4(S[n][2 * j + 1]));
+                pin(sf[n][j]);
             }
         };
-        int c = 0;
-        for (; c + 1 < nc; c += 2) {
-            chunk(c, ys[1], zs[1]);
-            chunk(c + 1, ys[0], zs[0]);
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+#pragma unroll
+            for (int j = 0; j < KS; ++j) round_state(n, j);
+        auto decay_tile = [&](int n, int kt) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) S[n][kt][i] *= decay;
+            pin(S[n][kt]);
+        };
+
+        // One chunk.  A wave is alone with one mover on its SIMD, so the order of its
+        // instructions has to keep the matrix pipe busy: a product issues in a quarter
+        // of the cycles that it takes, and each is followed by the few conversions
+        // that fill the rest (FENCE keeps the compiler from gathering them); operands
+        // are read from LDS a step ahead.
+        for (int c = 0; c < nc; ++c) {
+            bf16* zt = ztile[c % 3];
+            const bf16* yt = ytile[c % 3];
+            bf16x8 zf[NC][2], yf[3];
+            floatx4 acc[NC][4];
+            u32x4 term[2][NC][TERMS];
+            decay = chunk_decay.step();
+            if (c == nc - 1 && np - c * LC < LC) set_chunk(np - c * LC);
+            auto read_y = [&](int i) __attribute__((always_inline)) {
+                const bf16* y0 = yt + 32 * (i / NT) * D1 + y_off[i % NT / 2] + 4 * (i & 1);
+                yf[i % 3] = join(read_t(y0), read_t(y0 + 16 * D1));
+            };
+            // z of half a chunk, decayed to the chunk's end, as bf16 terms, in 16 NC steps
+            float v0, v1;
+            auto split = [&](int m, int step) __attribute__((always_inline)) {
+                const int n = step / 16, e = step / 4 % 4, q = step % 4;
+                if (q == 0) {
+                    const uint32_t raw = __builtin_bit_cast(u32x4, zf[n][m])[e];
+                    v0 = decayed(bf_lo(raw), wt[m][2 * e]);
+                    v1 = decayed(bf_hi(raw), wt[m][2 * e + 1]);
+                } else if (q <= TERMS) {
+                    uint32_t two = take_term(v0, v1);
+                    pin(two);
+                    term[m][n][q - 1][e] = two;
+                }
+            };
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int n = 0; n < NC; ++n)
+                    zf[n][m] = join(read_t(zt + z_off[n] + 32 * m * D2), read_t(zt + z_off[n] + (32 * m + 16) * D2));
+            // S^T x (D rows are the wave's columns, D columns the queries), and the first split
+            if constexpr (!STATES) {
+                const bf16* xt = xtile[c % 3];
+                bf16x8 xf[2][4], pf[6];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) xf[0][q] = row_frag(xt, q, 0);
+                FENCE;
+#pragma unroll
+                for (int j = 0; j < KS; ++j) {
+                    if (j + 1 < KS) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) xf[(j + 1) & 1][q] = row_frag(xt, q, j + 1);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 6; ++q) pf[q] = pfrag[c & 1][q][lane];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4 * NC; ++i) {
+                        const int q = i / NC, n = i % NC, k = j * 4 * NC + i;
+                        acc[n][q] = mfma32(sf[n][j], xf[j & 1][q], j ? acc[n][q] : floatx4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                        for (int u = 0; u < 4 / KS; ++u) split(0, 4 / KS * k + u);
+                        FENCE;
+                    }
+                }
+                // P z, and the state's decay
+                read_y(0);
+                read_y(1);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int n = 0; n < NC; ++n) acc[n][q] *= up[q];
+                FENCE;
+#pragma unroll
+                for (int i = 0; i < 6 * NC; ++i) {
+                    const int q = i / NC < 4 ? i / NC : i / NC - 2, n = i % NC;
+                    acc[n][q] = mfma32(zf[n][i / NC < 4 ? 0 : 1], pf[i / NC], acc[n][q]);
+#pragma unroll
+                    for (int t = 0; t < NC * NT; ++t)
+                        if (t * 6 / NT == i) decay_tile(t % NC, t / NC);
+                    FENCE;
+                }
+            } else {
+                read_y(0);
+                read_y(1);
+#pragma unroll
+                for (int k = 0; k < 16 * NC; ++k) split(0, k);
+#pragma unroll
+                for (int t = 0; t < NC * NT; ++t) decay_tile(t % NC, t / NC);
+                FENCE;
+            }
+            auto update = [&](int i, int k) __attribute__((always_inline)) {
+                const int q = TERMS - 1 - k / NC, n = k % NC;
+                S[n][i % NT] = mfma32(yf[i % 3], __builtin_bit_cast(bf16x8, term[i / NT][n][q]), S[n][i % NT]);
+            };
+            // the first half's update, with the second split; the outputs take the place
+            // of the wave's columns of z
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                read_y(i + 2);
+#pragma unroll
+                for (int k = 0; k < TERMS * NC; ++k) {
+                    update(i, k);
+                    const int at = i * TERMS * NC + k;  // of TERMS NC NT
+                    if (!STATES && at >= 2 * NC && at < 6 * NC) {
+                        const int q = (at - 2 * NC) / NC, n = at % NC;
+                        *reinterpret_cast<bf16x4*>(zt + o_off[n] + 16 * q * D2) = to_bf16x4(acc[n][q]);
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < 16 * NC; ++u)
+                            if (!STATES ? at >= 6 * NC && u * (TERMS * NT - 6) / 16 == at - 6 * NC : u * TERMS * NT / 16 == at)
+                                split(1, u);
+                    }
+                    FENCE;
+                }
+            }
+            // the second, with the rounding of the state for the next chunk
+#pragma unroll
+            for (int i = NT; i < 2 * NT; ++i) {
+                if (i + 2 < 2 * NT) read_y(i + 2);
+#pragma unroll
+                for (int k = 0; k < TERMS * NC; ++k) {
+                    update(i, k);
+                    const int done = (i - NT) / 2 - 1;  // tiles 2 done and 2 done + 1 are final
+                    if (i % 2 == 1 && done >= 0 && k < NC) round_state(k, done);
+                    FENCE;
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NC; ++n) round_state(n, KS - 1);
+            settle();
+            __syncthreads();
         }
-        if (c < nc) chunk(c, ys[1], zs[1]);
     }
 
     if (p.s_out && (p.s_out_slots || sg.p1 == sg.len)) {
-        float* s = p.s_out + ((int64_t)(p.s_out_slots ? slot : sg.n) * H + h) * sz + (int64_t)scol * p.col;
+        float* s = p.s_out + ((int64_t)(p.s_out_slots ? slot : sg.n) * H + h) * (D1 * D2) + state_at;
 #pragma unroll
-        for (int kt = 0; kt < NT; ++kt)
+        for (int n = 0; n < NC; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[tile_channel(kh * NT + kt, 4 * g + i) * p.row] = S[kt][i];
+            for (int kt = 0; kt < NT; ++kt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[tile_channel(kt, 4 * g + i) * p.row + 16 * n * p.col] = S[n][kt][i];
     }
 }
 
@@ -478,17 +531,22 @@ __global__ __launch_bounds__(256) void la_scan_kernel(LaScanArgs a) {
 }
 
 void launch_la_chunk(const LaArgs& a, int n, int D1, bool states, hipStream_t stream) {
-    const int64_t groups = (int64_t)a.s.n_slots * a.s.H;
-    int ncb = 0;
-    for (int i = 0; i < n; ++i) ncb = max(ncb, a.pass[i].D2 / LA_COLS);
-    const dim3 grid((unsigned)((groups + 7) / 8 * 8 * ncb), (unsigned)n);
-    if (D1 == 128) {
-        if (states) hipLaunchKernelGGL((la_chunk_kernel<128, true>), grid, dim3(256), 0, stream, a);
-        else hipLaunchKernelGGL((la_chunk_kernel<128, false>), grid, dim3(512), 0, stream, a);
-    } else {
-        if (states) hipLaunchKernelGGL((la_chunk_kernel<64, true>), grid, dim3(256), 0, stream, a);
-        else hipLaunchKernelGGL((la_chunk_kernel<64, false>), grid, dim3(512), 0, stream, a);
-    }
+    int terms = 2;
+    for (int i = 0; i < n; ++i)
+        if (a.pass[i].s_out) terms = 3;
+    const dim3 grid((unsigned)((int64_t)a.s.n_slots * a.s.H), (unsigned)n);
+    auto go = [&](auto d1, auto d2) {
+        constexpr int X = decltype(d1)::value, Z = decltype(d2)::value;
+        if (states) hipLaunchKernelGGL((la_chunk_kernel<X, Z, 3, true>), grid, dim3(512), 0, stream, a);
+        else if (terms == 3) hipLaunchKernelGGL((la_chunk_kernel<X, Z, 3, false>), grid, dim3(512), 0, stream, a);
+        else hipLaunchKernelGGL((la_chunk_kernel<X, Z, 2, false>), grid, dim3(512), 0, stream, a);
+    };
+    const std::integral_constant<int, 64> s{};
+    const std::integral_constant<int, 128> l{};
+    if (D1 == 128 && a.cols == 128) go(l, l);
+    else if (D1 == 128) go(l, s);
+    else if (a.cols == 128) go(s, l);
+    else go(s, s);
 }
 
 void launch_la_scan(const LaScanArgs& a, hipStream_t stream) {

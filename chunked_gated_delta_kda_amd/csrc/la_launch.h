@@ -10,7 +10,6 @@
 namespace kda {
 
 constexpr int LA_CHUNK = 64;  // tokens per chunk
-constexpr int LA_COLS = 32;   // state columns per workgroup
 
 // One chunked pass over the tokens of a batch (la_chunk.hip):
 //   O_p = x_scale a^(p+1-late) S_in^T x_p + in_scale sum_{j<=p} a^(p-j) (x_p . y_j) z_j
@@ -26,9 +25,11 @@ struct LaPass {
     const float* s_in;     // entering states, fp32, or null (zeros)
     float* s_out;          // states left behind, fp32, or null (not written)
     int32_t s_in_slots;    // s_in holds one state per segment slot (else per sequence)
+    const float* seg_states;  // what each segment adds to a zero state, by slot, or null:
+                           // a segment then forms its entering state from s_in and the
+                           // segments before it
     int32_t s_out_slots;   // s_out: one per slot, of all segments but a sequence's last
                            // (else one per sequence, of its last segment)
-    int32_t D2;            // 64 or 128
     int32_t row, col;      // element (d1, d2) of a state sits at row * d1 + col * d2
     int32_t reverse;       // positions run from the last token to the first, late = 1
     float in_scale, x_scale, z_scale;
@@ -47,12 +48,14 @@ struct LaSeqs {
     int32_t seg_tokens;    // positions per segment (a multiple of LA_CHUNK), 0: whole
     int32_t seg_per_seq;   // fixed length only
     int32_t n_slots;
+    int32_t by_length;     // packed whole sequences: slot i is the i-th longest
 };
 
 struct LaArgs {
     LaPass pass[3];
     LaSeqs s;
     const float* log_decay;  // [H] fp32
+    int32_t cols;            // D2
 };
 
 struct LaScanArgs {
@@ -103,8 +106,12 @@ struct GatedNormArgs {
     int32_t groups;
 };
 
-// passes [0, n) of a share D1; states: no outputs (x and o null)
+// Passes [0, n) of a share D1 and D2 (cols); states: no outputs (x and o null).
 void launch_la_chunk(const LaArgs& a, int n, int D1, bool states, hipStream_t stream);
+// The same for whole sequences, in workgroups of a few columns (la_narrow.hip).
+void launch_la_narrow(const LaArgs& a, int n, int D1, hipStream_t stream);
+// workgroups of that launch
+int64_t la_narrow_groups(int64_t pairs, int cols);
 void launch_la_scan(const LaScanArgs& a, hipStream_t stream);
 void launch_la_decode(const LaDecodeArgs& a, int K, hipStream_t stream);
 void launch_gated_norm_fwd(const GatedNormArgs& a, hipStream_t stream);

@@ -345,3 +345,72 @@ def test_rows_past_32_bit_offsets():
     for n in ("dq", "dk", "dv"):
         assert torch.equal(r[n][:, -last:], r1[n]), n
     assert torch.equal(r["dh0"][1], r1["dh0"][0])
+
+
+# more (sequence, head) pairs than one round of narrow workgroups holds
+MANY = 130
+
+
+@pytest.mark.parametrize("K,V", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("T", [1, 64, 100, 193])
+def test_many_heads(T, K, V):
+    check(make(1, T, 2 * MANY if V == 64 else MANY, K, V, seed=700 + T + K + 2 * V), whole=T > 16)
+
+
+@pytest.mark.parametrize("decay", ["none", "all", "fast", "slow"])
+def test_many_heads_decays(decay):
+    check(make(1, 150, MANY, 128, 128, seed=710, decay=decay), gradients=True)
+
+
+@pytest.mark.parametrize("lens,lead,tail", [([0, 5, 0, 130, 1, 0], 0, 0), ([70, 0, 3], 9, 41), ([33] * 63, 0, 1),
+                                            ([33, 7, 90] * 22, 2, 0)])
+def test_many_heads_packed(lens, lead, tail):
+    """Longest first up to 64 sequences, in order beyond."""
+    w = make(0, 0, 90, 64, 128, seed=720, lens=lens, lead=lead, tail=tail)
+    check(w, whole=sum(lens) > 100)
+    d = dev(w)
+    o, _ = fwd(d, out=torch.full_like(d["v"], float("nan")))
+    assert not o[:, :lead].any() and not o[:, lead + sum(lens):].any()
+
+
+def test_a_head_is_the_same_beside_few_and_many():
+    w = make(2, 300, MANY, 128, 128, seed=730)
+    d = dev(w)
+    o, S = fwd(d)
+    r = bwd(d)
+    one = {n: (t[:, :, 7:8].contiguous() if n in ("q", "k", "v", "do") else t) for n, t in d.items()}
+    one.update(ld=d["ld"][7:8].contiguous(), h0=d["h0"][:, 7:8].contiguous(), dfin=d["dfin"][:, 7:8].contiguous())
+    o1, S1 = fwd(one, segment_chunks=-1)
+    r1 = bwd(one, segment_chunks=-1)
+    assert torch.equal(o[:, :, 7:8], o1) and torch.equal(S[:, 7:8], S1)
+    for n in ("dq", "dk", "dv"):
+        assert torch.equal(r[n][:, :, 7:8], r1[n]), n
+    assert torch.equal(r["dh0"][:, 7:8], r1["dh0"])
+
+
+def test_gradients_without_the_states():
+    """Nobody reads the last state: two terms of a decayed value are enough then."""
+    w = make(1, 190, MANY, 128, 128, seed=740)
+    d = dev(w)
+    r = kda.la_bwd(d["q"], d["k"], d["v"], d["ld"], d["do"], d["scale"], d["h0"], d["dfin"], need_dh0=False)
+    assert r["dh0"] is None
+    rr = ref.la_bwd(w["q"], w["k"], w["v"], w["ld"], w["scale"], w["do"], w["h0"], w["dfin"], None)
+    mr = magnitude(w)[2]
+    for n in ("dq", "dk", "dv"):
+        # (what two terms of eight bits cut off is below 2^-14 of the value: inside the
+        # bound's 0.02 * 2^-8, beside 2^-16 for the second order)
+        near_bf16(n, r[n], rr[n], mr[n])
+
+
+def test_long_state_of_many_heads_keeps_its_last_bits():
+    w = make(1, 2100, MANY, 64, 64, seed=750, decay="slow")
+    d = dev(w)
+    assert kda.la_workspace_size(1, 2100, 2 * MANY, 64, 64) <= 256
+    o, S = kda.la_fwd(*(torch.cat([d[n]] * 2, 2) for n in ("q", "k", "v")), torch.cat([d["ld"]] * 2), d["scale"],
+                      torch.cat([d["h0"]] * 2, 1))
+    ro, rS = ref.la_fwd(*(w[n][:, :, :3] for n in ("q", "k", "v")), w["ld"][:3], w["scale"], w["h0"][:, :3], None)
+    a = {n: w[n][:, :, :3].abs() for n in ("q", "k", "v")}
+    mo, mS = ref.la_fwd(a["q"], a["k"], a["v"], w["ld"][:3], w["scale"], w["h0"][:, :3].abs(), None)
+    near_bf16("o", o[:, :, :3], ro, mo)
+    near_state("state", S[:, :3], rS, mS)
+    assert torch.equal(S[:, :MANY], S[:, MANY:]) and torch.equal(o[:, :, :MANY], o[:, :, MANY:])

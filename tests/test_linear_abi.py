@@ -139,3 +139,9 @@ def test_wrappers_refuse():
         kda.la_fwd(q.float(), q, q, ld)
     with pytest.raises(ValueError, match="GPU"):
         kda.gated_norm(q, q, torch.ones(64))
+
+
+def test_la_refuses_rows_that_32_bit_offsets_do_not_reach(lib):
+    """A chunk's rows are addressed by 32-bit byte offsets: at most 65536 heads."""
+    assert la_fwd(lib, H=65537) == 1
+    assert la_bwd(lib, H=65537) == 1
