@@ -181,6 +181,10 @@ def _ptr(t):
 
 def _need(t, name, dtype, shape=None, device=None):
     torch = _torch()
+    if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.is_cuda
+            and (device is None or t.device == device) and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -650,10 +654,31 @@ def gdn_bwd(q, k, v, g, beta, do, scale=None, initial_state=None, dfinal=None, c
 
 
 # ------------------------------------------ linear attention, a decay for each head
+class _Current:
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_CURRENT = _Current()
+
+
 def _on(dev):
     """The device made current for the launches (they go to its current stream)."""
-    torch = _torch()
-    return torch.cuda.device(dev)
+    cuda = _torch().cuda
+    return _CURRENT if cuda.current_device() == dev.index else cuda.device(dev)
+
+
+def _stream(dev):
+    """The device's current stream, as a handle (a Stream object around it costs as
+    much as half a launch)."""
+    return _torch()._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def la_workspace_size(B, T, H, K, V, num_seqs=None, segment_chunks=0, backward=False) -> int:
@@ -697,7 +722,7 @@ def _la_prepare(q, k, v, log_decay, scale, initial_state, cu_seqlens, workspace,
         raise LibKdaError(3, status_str(3))
     return (dev, B, T, H, K, V, N, float(K ** -0.5 if scale is None else scale), workspace,
             0 if workspace is None else _nbytes(workspace),
-            ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream))
+            _stream(dev))
 
 
 def la_fwd(q, k, v, log_decay, scale=None, initial_state=None, output_final_state=True,
@@ -714,7 +739,7 @@ def la_fwd(q, k, v, log_decay, scale=None, initial_state=None, output_final_stat
     dev, B, T, H, K, V, N, sc, ws, wsb, stream = _la_prepare(
         q, k, v, log_decay, scale, initial_state, cu_seqlens, workspace, segment_chunks, False)
     if out is None:
-        out = torch.empty((B, T, H, V), dtype=torch.bfloat16, device=dev)
+        out = torch.empty_like(v)
     else:
         _need(out, "out", torch.bfloat16, (B, T, H, V), dev)
     final = None
@@ -725,8 +750,8 @@ def la_fwd(q, k, v, log_decay, scale=None, initial_state=None, output_final_stat
             _need(final_out, "final_out", torch.float32, (N, H, K, V), dev)
         final = final_out
     with _on(dev):
-        _check(load().la_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), sc, _ptr(initial_state),
-                             _ptr(final), _ptr(cu_seqlens), N, B, T, H, K, V, _ptr(out), _ptr(ws),
+        _check(load().la_fwd(_addr(q), _addr(k), _addr(v), _addr(log_decay), sc, _addr(initial_state),
+                             _addr(final), _addr(cu_seqlens), N, B, T, H, K, V, _addr(out), _addr(ws),
                              wsb, int(segment_chunks), stream))
     return out, final
 
@@ -746,10 +771,10 @@ def la_bwd(q, k, v, log_decay, do, scale=None, initial_state=None, dfinal=None, 
     r = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
          "dh0": torch.empty((N, H, K, V), dtype=torch.float32, device=dev) if need_dh0 else None}
     with _on(dev):
-        _check(load().la_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), sc, _ptr(initial_state),
-                             _ptr(cu_seqlens), N, B, T, H, K, V, _ptr(do), _ptr(dfinal),
-                             _ptr(r["dq"]), _ptr(r["dk"]), _ptr(r["dv"]), _ptr(r["dh0"]),
-                             _ptr(ws), wsb, int(segment_chunks), stream))
+        _check(load().la_bwd(_addr(q), _addr(k), _addr(v), _addr(log_decay), sc, _addr(initial_state),
+                             _addr(cu_seqlens), N, B, T, H, K, V, _addr(do), _addr(dfinal),
+                             _addr(r["dq"]), _addr(r["dk"]), _addr(r["dv"]), _addr(r["dh0"]),
+                             _addr(ws), wsb, int(segment_chunks), stream))
     return r
 
 
@@ -777,14 +802,14 @@ def la_decode(q, k, v, log_decay, scale=None, state=None, state_out=None, out=No
     else:
         _need(state_out, "state_out", torch.float32, (N, H, K, V), dev)
     if out is None:
-        out = torch.empty((N, H, V), dtype=torch.bfloat16, device=dev)
+        out = torch.empty_like(v)
     else:
         _need(out, "out", torch.bfloat16, (N, H, V), dev)
-    stream = ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    stream = _stream(dev)
     with _on(dev):
-        _check(load().la_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
-                                float(K ** -0.5 if scale is None else scale), _ptr(state),
-                                _ptr(state_out), N, H, K, V, _ptr(out), stream))
+        _check(load().la_decode(_addr(q), _addr(k), _addr(v), _addr(log_decay),
+                                float(K ** -0.5 if scale is None else scale), _addr(state),
+                                _addr(state_out), N, H, K, V, _addr(out), stream))
     return out, state_out
 
 
@@ -812,9 +837,9 @@ def _norm_prepare(x, gate, weight, activation, eps, residual, residual_scale):
     if H < 1 or D < 1:
         raise ValueError("x must be [..., H, D] with H and D at least 1")
     tokens = x.numel() // (H * D)
-    args = (_ptr(x), _ptr(gate), _ptr(weight), _ptr(residual), _ptr(residual_scale),
+    args = (_addr(x), _addr(gate), _addr(weight), _addr(residual), _addr(residual_scale),
             _ACTIVATIONS[activation], float(eps), tokens, H, D)
-    return dev, tokens, H, D, args, ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    return dev, tokens, H, D, args, _stream(dev)
 
 
 def gated_norm_fwd(x, gate, weight, activation="sigmoid", eps=1e-6, residual=None,
@@ -832,7 +857,7 @@ def gated_norm_fwd(x, gate, weight, activation="sigmoid", eps=1e-6, residual=Non
     else:
         _need(out, "out", torch.bfloat16, x.shape, dev)
     with _on(dev):
-        _check(load().gated_norm_fwd(*args, _ptr(out), stream))
+        _check(load().gated_norm_fwd(*args, _addr(out), stream))
     return out
 
 
@@ -856,8 +881,8 @@ def gated_norm_bwd(x, gate, weight, dy, activation="sigmoid", eps=1e-6, residual
          "dresidual": None if residual is None else torch.empty_like(residual),
          "dresidual_scale": None if residual is None else torch.empty_like(residual_scale)}
     with _on(dev):
-        _check(load().gated_norm_bwd(*args, _ptr(dy), _ptr(r["dx"]), _ptr(r["dgate"]),
-                                     _ptr(r["dweight"]), _ptr(r["dresidual"]),
-                                     _ptr(r["dresidual_scale"]), _ptr(workspace),
+        _check(load().gated_norm_bwd(*args, _addr(dy), _addr(r["dx"]), _addr(r["dgate"]),
+                                     _addr(r["dweight"]), _addr(r["dresidual"]),
+                                     _addr(r["dresidual_scale"]), _addr(workspace),
                                      _nbytes(workspace), stream))
     return r
