@@ -126,13 +126,15 @@ int check_la(const LaCall& c, float scale, const float* log_decay, const void* w
     return KDA_OK;
 }
 
-kda::LaPass make_pass(const uint16_t* x, const uint16_t* y, const uint16_t* z, uint16_t* o, int32_t row, int32_t col,
-                      bool reverse, float scale) {
+kda::LaPass make_pass(const uint16_t* x, const uint16_t* y, const uint16_t* z, uint16_t* o, int32_t D1, int32_t D2,
+                      int32_t row, int32_t col, bool reverse, float scale) {
     kda::LaPass p{};
     p.x = x;
     p.y = y;
     p.z = z;
     p.o = o;
+    p.D1 = D1;
+    p.D2 = D2;
     p.row = row;
     p.col = col;
     p.reverse = reverse;
@@ -144,7 +146,7 @@ kda::LaPass make_pass(const uint16_t* x, const uint16_t* y, const uint16_t* z, u
 
 // what each segment adds to the state, for a pass with the states' own [K, V] layout
 void launch_states(const kda::LaSeqs& s, const float* log_decay, const kda::LaPass* p, float* const* out, int n,
-                   int32_t K, int32_t V, hipStream_t stream) {
+                   hipStream_t stream) {
     kda::LaArgs a{};
     a.s = s;
     a.log_decay = log_decay;
@@ -156,13 +158,12 @@ void launch_states(const kda::LaSeqs& s, const float* log_decay, const kda::LaPa
         a.pass[i].s_out = out[i];
         a.pass[i].s_out_slots = 1;
     }
-    a.cols = V;
-    kda::launch_la_chunk(a, n, K, true, stream);
+    kda::launch_la_chunk(a, n, true, stream);
 }
 
-void launch(const LaPlan& p, const kda::LaArgs& a, int n, int D1, hipStream_t stream) {
-    if (p.narrow) kda::launch_la_narrow(a, n, D1, stream);
-    else kda::launch_la_chunk(a, n, D1, false, stream);
+void launch(const LaPlan& p, const kda::LaArgs& a, int n, hipStream_t stream) {
+    if (p.narrow) kda::launch_la_narrow(a, n, stream);
+    else kda::launch_la_chunk(a, n, false, stream);
 }
 
 int status() { return hipGetLastError() == hipSuccess ? KDA_OK : KDA_ERR_LAUNCH; }
@@ -210,12 +211,12 @@ int la_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float*
     a.s = s;
     a.log_decay = log_decay;
     kda::LaPass& p = a.pass[0];
-    p = make_pass(q, k, v, o, V, 1, false, scale);
+    p = make_pass(q, k, v, o, K, V, V, 1, false, scale);
     p.s_in = initial_state;
     p.s_out = final_state;
     if (s.seg_tokens) {
         float* states = static_cast<float*>(workspace);
-        launch_states(s, log_decay, &p, &states, 1, K, V, str);
+        launch_states(s, log_decay, &p, &states, 1, str);
         if (self_entering(s)) {
             p.seg_states = states;
         } else {
@@ -231,8 +232,7 @@ int la_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float*
             p.s_in_slots = 1;
         }
     }
-    a.cols = V;
-    launch(pl, a, 1, K, str);
+    launch(pl, a, 1, str);
     return status();
 }
 
@@ -252,17 +252,17 @@ int la_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float*
         if (!aligned(p, 16)) return KDA_ERR_INVALID_ARG;
     const hipStream_t str = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
-    kda::LaPass pq = make_pass(d_o, v, k, dq, 1, V, false, scale);
-    kda::LaPass pk = make_pass(v, d_o, q, dk, 1, V, true, scale);
-    kda::LaPass pv = make_pass(k, q, d_o, dv, V, 1, true, scale);
+    kda::LaPass pq = make_pass(d_o, v, k, dq, V, K, 1, V, false, scale);
+    kda::LaPass pk = make_pass(v, d_o, q, dk, V, K, 1, V, true, scale);
+    kda::LaPass pv = make_pass(k, q, d_o, dv, K, V, V, 1, true, scale);
     pq.s_in = initial_state;
     pk.s_in = pv.s_in = d_final;
     pv.s_out = dh0;
     if (s.seg_tokens) {
         float* states[2] = {static_cast<float*>(workspace),
                             static_cast<float*>(workspace) + la_states_bytes(c, s) / sizeof(float)};
-        const kda::LaPass p[2] = {make_pass(q, k, v, nullptr, V, 1, false, scale), pv};
-        launch_states(s, log_decay, p, states, 2, K, V, str);
+        const kda::LaPass p[2] = {make_pass(q, k, v, nullptr, K, V, V, 1, false, scale), pv};
+        launch_states(s, log_decay, p, states, 2, str);
         if (self_entering(s)) {
             pq.seg_states = states[0];
             pk.seg_states = pv.seg_states = states[1];
@@ -285,21 +285,10 @@ int la_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float*
     kda::LaArgs a{};
     a.s = s;
     a.log_decay = log_decay;
-    if (K == V) {
-        a.pass[0] = pk;
-        a.pass[1] = pv;
-        a.pass[2] = pq;
-        a.cols = V;
-        launch(pl, a, 3, K, str);
-    } else {
-        a.pass[0] = pk;
-        a.pass[1] = pq;
-        a.cols = K;
-        launch(pl, a, 2, V, str);
-        a.pass[0] = pv;
-        a.cols = V;
-        launch(pl, a, 1, K, str);
-    }
+    a.pass[0] = pk;
+    a.pass[1] = pv;
+    a.pass[2] = pq;
+    launch(pl, a, 3, str);
     return status();
 }
 

@@ -46,8 +46,14 @@
 
 namespace kda {
 
+// LDS of a workgroup: three tiles each of x, y, z and two sets of P
+template <int D1, int D2, bool STATES>
+constexpr int lds_bytes() {
+    return 3 * LC * (STATES ? D1 + D2 : 2 * D1 + D2) * 2 + (STATES ? 0 : 2 * 6 * 64 * 16);
+}
+
 template <int D1, int D2, int TERMS, bool STATES>
-__global__ __launch_bounds__(512, 2) void la_chunk_kernel(LaArgs a) {
+__device__ __forceinline__ void chunk_pass(const LaArgs& a, const LaPass& p, unsigned char* lds) {
     constexpr int NC = D2 / 64;            // 16-column tiles of each of the four state waves
     constexpr int KS = D1 / 32;            // 16x16x32 steps over D1
     constexpr int NT = D1 / 16;            // state tiles of a wave
@@ -56,12 +62,11 @@ __global__ __launch_bounds__(512, 2) void la_chunk_kernel(LaArgs a) {
     constexpr int RV = D1 / 32, RT = D1 / 8, RROWS = 256 / RT;
     constexpr int ZV = D2 / 32, ZT = D2 / 8, ZROWS = 256 / ZT;
     constexpr int PT = 3;                  // tiles of P per wave, at most
-    __shared__ __align__(16) bf16 xtile[STATES ? 1 : 3][STATES ? 8 : LC * D1];
-    __shared__ __align__(16) bf16 ytile[3][LC * D1];
-    __shared__ __align__(16) bf16 ztile[3][LC * D2];
-    __shared__ bf16x8 pfrag[STATES ? 1 : 2][6][STATES ? 1 : 64];
+    bf16(*const ytile)[LC * D1] = reinterpret_cast<bf16(*)[LC * D1]>(lds);
+    bf16(*const ztile)[LC * D2] = reinterpret_cast<bf16(*)[LC * D2]>(ytile + 3);
+    bf16(*const xtile)[LC * D1] = reinterpret_cast<bf16(*)[LC * D1]>(ztile + 3);
+    bf16x8(*const pfrag)[6][64] = reinterpret_cast<bf16x8(*)[6][64]>(xtile + 3);
 
-    const LaPass p = a.pass[blockIdx.y];
     const int H = a.s.H;
     const int slot = (int)(blockIdx.x / H), h = (int)(blockIdx.x % H);
     Seg sg;
@@ -497,6 +502,22 @@ __global__ __launch_bounds__(512, 2) void la_chunk_kernel(LaArgs a) {
     }
 }
 
+template <int D1, int D2, int TERMS, bool STATES>
+__global__ __launch_bounds__(512, 2) void la_chunk_kernel(LaArgs a) {
+    __shared__ __align__(16) unsigned char lds[lds_bytes<D1, D2, STATES>()];
+    chunk_pass<D1, D2, TERMS, STATES>(a, a.pass[blockIdx.y], lds);
+}
+
+// passes over 64 x 128 and 128 x 64 states side by side
+template <int TERMS>
+__global__ __launch_bounds__(512, 2) void la_chunk_mixed_kernel(LaArgs a) {
+    constexpr int A = lds_bytes<64, 128, false>(), B = lds_bytes<128, 64, false>();
+    __shared__ __align__(16) unsigned char lds[A > B ? A : B];
+    const LaPass& p = a.pass[blockIdx.y];
+    if (p.D2 == 128) chunk_pass<64, 128, TERMS, false>(a, p, lds);
+    else chunk_pass<128, 64, TERMS, false>(a, p, lds);
+}
+
 // Entering states of the segments: for a sequence's segments in order,
 // E_0 = the sequence's own entering state, E_(s+1) = a^seg_tokens E_s + U_s,
 // written over U.  One thread per four elements of a (sequence, head)'s state.
@@ -530,11 +551,19 @@ __global__ __launch_bounds__(256) void la_scan_kernel(LaScanArgs a) {
     }
 }
 
-void launch_la_chunk(const LaArgs& a, int n, int D1, bool states, hipStream_t stream) {
+void launch_la_chunk(const LaArgs& a, int n, bool states, hipStream_t stream) {
     int terms = 2;
-    for (int i = 0; i < n; ++i)
+    bool mixed = false;
+    for (int i = 0; i < n; ++i) {
         if (a.pass[i].s_out) terms = 3;
+        mixed |= a.pass[i].D1 != a.pass[0].D1;
+    }
     const dim3 grid((unsigned)((int64_t)a.s.n_slots * a.s.H), (unsigned)n);
+    if (mixed) {
+        if (terms == 3) hipLaunchKernelGGL((la_chunk_mixed_kernel<3>), grid, dim3(512), 0, stream, a);
+        else hipLaunchKernelGGL((la_chunk_mixed_kernel<2>), grid, dim3(512), 0, stream, a);
+        return;
+    }
     auto go = [&](auto d1, auto d2) {
         constexpr int X = decltype(d1)::value, Z = decltype(d2)::value;
         if (states) hipLaunchKernelGGL((la_chunk_kernel<X, Z, 3, true>), grid, dim3(512), 0, stream, a);
@@ -543,9 +572,10 @@ void launch_la_chunk(const LaArgs& a, int n, int D1, bool states, hipStream_t st
     };
     const std::integral_constant<int, 64> s{};
     const std::integral_constant<int, 128> l{};
-    if (D1 == 128 && a.cols == 128) go(l, l);
+    const int D1 = a.pass[0].D1, D2 = a.pass[0].D2;
+    if (D1 == 128 && D2 == 128) go(l, l);
     else if (D1 == 128) go(l, s);
-    else if (a.cols == 128) go(s, l);
+    else if (D2 == 128) go(s, l);
     else go(s, s);
 }
 

@@ -30,6 +30,7 @@ struct LaPass {
                            // segments before it
     int32_t s_out_slots;   // s_out: one per slot, of all segments but a sequence's last
                            // (else one per sequence, of its last segment)
+    int32_t D1, D2;        // 64 or 128 each
     int32_t row, col;      // element (d1, d2) of a state sits at row * d1 + col * d2
     int32_t reverse;       // positions run from the last token to the first, late = 1
     float in_scale, x_scale, z_scale;
@@ -55,7 +56,6 @@ struct LaArgs {
     LaPass pass[3];
     LaSeqs s;
     const float* log_decay;  // [H] fp32
-    int32_t cols;            // D2
 };
 
 struct LaScanArgs {
@@ -106,11 +106,12 @@ struct GatedNormArgs {
     int32_t groups;
 };
 
-// Passes [0, n) of a share D1 and D2 (cols); states: no outputs (x and o null).
-void launch_la_chunk(const LaArgs& a, int n, int D1, bool states, hipStream_t stream);
+// Passes [0, n) of a, of one D1 x D2, or of both 64 x 128 and 128 x 64; states: no
+// outputs (x and o null), one D1 x D2.
+void launch_la_chunk(const LaArgs& a, int n, bool states, hipStream_t stream);
 // The same for whole sequences, in workgroups of a few columns (la_narrow.hip).
-void launch_la_narrow(const LaArgs& a, int n, int D1, hipStream_t stream);
-// workgroups of that launch
+void launch_la_narrow(const LaArgs& a, int n, hipStream_t stream);
+// workgroups of a pass there
 int64_t la_narrow_groups(int64_t pairs, int cols);
 void launch_la_scan(const LaScanArgs& a, hipStream_t stream);
 void launch_la_decode(const LaDecodeArgs& a, int K, hipStream_t stream);

@@ -25,21 +25,22 @@ namespace kda {
 
 constexpr int LA_COLS = 32;  // state columns per workgroup
 
+constexpr int narrow_lds_bytes(int D1) { return 2 * LC * D1 * 2 + 2 * 4 * LC * LA_COLS * 2 + 2 * 2 * (D1 / 32) * 64 * 16; }
+
 template <int D1>
-__global__ __launch_bounds__(512, 4) void la_narrow_kernel(LaArgs a) {
+__device__ __forceinline__ void narrow_pass(const LaArgs& a, const LaPass& p, unsigned char* lds) {
     constexpr int KS = D1 / 32;       // 16x16x32 steps over D1
     constexpr int NT = D1 / 32;       // state tiles of a wave (half of D1 / 16)
     constexpr int YV = D1 / 32;       // 16-byte pieces of the y tile per thread of its four waves
     constexpr int TPR = D1 / 8;       // threads per row of the y tile
     constexpr int YROWS = 256 / TPR;  // rows they cover at once
-    __shared__ __align__(16) bf16 ytile[2][LC * D1];
-    __shared__ __align__(16) bf16 ztile[2][LC * LA_COLS];
-    __shared__ __align__(16) bf16 zterm[2][3][LC * LA_COLS];
-    __shared__ u32x4 scopy[2][2][KS][64];
+    bf16(*const ytile)[LC * D1] = reinterpret_cast<bf16(*)[LC * D1]>(lds);
+    bf16(*const ztile)[LC * LA_COLS] = reinterpret_cast<bf16(*)[LC * LA_COLS]>(ytile + 2);
+    bf16(*const zterm)[3][LC * LA_COLS] = reinterpret_cast<bf16(*)[3][LC * LA_COLS]>(ztile + 2);
+    u32x4(*const scopy)[2][KS][64] = reinterpret_cast<u32x4(*)[2][KS][64]>(zterm + 2);
 
-    const LaPass& p = a.pass[blockIdx.y];
     const int H = a.s.H;
-    const int ncb = a.cols / LA_COLS;
+    const int ncb = p.D2 / LA_COLS;
     // workgroups are dealt to the eight XCDs in turn: the column blocks of one
     // (segment, head) follow each other on one of them
     const int64_t b = blockIdx.x;
@@ -54,7 +55,7 @@ __global__ __launch_bounds__(512, 4) void la_narrow_kernel(LaArgs a) {
     const int lane = tid & 63, r = lane & 15, g = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const bool out_role = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) == 0;
-    const int D2 = a.cols, c0 = cb * LA_COLS;
+    const int D2 = p.D2, c0 = cb * LA_COLS;
     const int late = p.reverse ? 1 : 0;
 
     if (a.s.cu && (sg.n == 0 || sg.n == a.s.n_seqs - 1)) {
@@ -311,12 +312,28 @@ __global__ __launch_bounds__(512, 4) void la_narrow_kernel(LaArgs a) {
     }
 }
 
+// (128-row and 64-row states, side by side where a batch has both)
+template <bool MIXED, int D1>
+__global__ __launch_bounds__(512, 4) void la_narrow_kernel(LaArgs a) {
+    __shared__ __align__(16) unsigned char lds[narrow_lds_bytes(MIXED ? 128 : D1)];
+    const LaPass& p = a.pass[blockIdx.y];
+    if (MIXED && p.D1 == 64) narrow_pass<64>(a, p, lds);
+    else narrow_pass<D1>(a, p, lds);
+}
+
 int64_t la_narrow_groups(int64_t pairs, int cols) { return (pairs + 7) / 8 * 8 * (cols / LA_COLS); }
 
-void launch_la_narrow(const LaArgs& a, int n, int D1, hipStream_t stream) {
-    const dim3 grid((unsigned)la_narrow_groups((int64_t)a.s.n_seqs * a.s.H, a.cols), (unsigned)n);
-    if (D1 == 128) hipLaunchKernelGGL((la_narrow_kernel<128>), grid, dim3(512), 0, stream, a);
-    else hipLaunchKernelGGL((la_narrow_kernel<64>), grid, dim3(512), 0, stream, a);
+void launch_la_narrow(const LaArgs& a, int n, hipStream_t stream) {
+    int cols = 64;
+    bool mixed = false;
+    for (int i = 0; i < n; ++i) {
+        cols = a.pass[i].D2 > cols ? a.pass[i].D2 : cols;
+        mixed |= a.pass[i].D1 != a.pass[0].D1;
+    }
+    const dim3 grid((unsigned)la_narrow_groups((int64_t)a.s.n_seqs * a.s.H, cols), (unsigned)n);
+    if (mixed) hipLaunchKernelGGL((la_narrow_kernel<true, 128>), grid, dim3(512), 0, stream, a);
+    else if (a.pass[0].D1 == 128) hipLaunchKernelGGL((la_narrow_kernel<false, 128>), grid, dim3(512), 0, stream, a);
+    else hipLaunchKernelGGL((la_narrow_kernel<false, 64>), grid, dim3(512), 0, stream, a);
 }
 
 }  // namespace kda

@@ -414,3 +414,13 @@ def test_long_state_of_many_heads_keeps_its_last_bits():
     near_bf16("o", o[:, :, :3], ro, mo)
     near_state("state", S[:, :3], rS, mS)
     assert torch.equal(S[:, :MANY], S[:, MANY:]) and torch.equal(o[:, :, :MANY], o[:, :, MANY:])
+
+
+@pytest.mark.parametrize("K,V", [(64, 128), (128, 64), (64, 64), (128, 128)])
+@pytest.mark.parametrize("H", [2, MANY])
+def test_outputs_without_the_last_state(H, K, V):
+    w = make(1, 130, H, K, V, seed=760)
+    d = dev(w)
+    o, S = kda.la_fwd(d["q"], d["k"], d["v"], d["ld"], d["scale"], d["h0"], output_final_state=False)
+    assert S is None
+    near_bf16("o", o, ref.la_fwd(w["q"], w["k"], w["v"], w["ld"], w["scale"], w["h0"])[0], magnitude(w)[0])
