@@ -53,7 +53,7 @@ constexpr int lds_bytes() {
 }
 
 template <int D1, int D2, int TERMS, bool STATES>
-__device__ __forceinline__ void chunk_pass(const LaArgs& a, const LaPass& p, unsigned char* lds) {
+__device__ __forceinline__ void chunk_pass(const LaArgs& a, const LaPass& p, int slot, int h, unsigned char* lds) {
     constexpr int NC = D2 / 64;            // 16-column tiles of each of the four state waves
     constexpr int KS = D1 / 32;            // 16x16x32 steps over D1
     constexpr int NT = D1 / 16;            // state tiles of a wave
@@ -68,7 +68,6 @@ __device__ __forceinline__ void chunk_pass(const LaArgs& a, const LaPass& p, uns
     bf16x8(*const pfrag)[6][64] = reinterpret_cast<bf16x8(*)[6][64]>(xtile + 3);
 
     const int H = a.s.H;
-    const int slot = (int)(blockIdx.x / H), h = (int)(blockIdx.x % H);
     Seg sg;
     if (!find_seg(a.s, slot, sg)) return;
     const float ld = head_log_decay(a.log_decay, h);
@@ -502,10 +501,23 @@ __device__ __forceinline__ void chunk_pass(const LaArgs& a, const LaPass& p, uns
     }
 }
 
+// A workgroup's part of a launch of (heads of a slot x slots, passes): heads fastest,
+// then the passes, which read the same rows, then the slots.
+struct Work {
+    int pass, slot, h;
+    __device__ __forceinline__ explicit Work(int H) {
+        const uint32_t id = blockIdx.y * gridDim.x + blockIdx.x;
+        h = id % H;
+        pass = id / H % gridDim.y;
+        slot = id / H / gridDim.y;
+    }
+};
+
 template <int D1, int D2, int TERMS, bool STATES>
 __global__ __launch_bounds__(512, 2) void la_chunk_kernel(LaArgs a) {
     __shared__ __align__(16) unsigned char lds[lds_bytes<D1, D2, STATES>()];
-    chunk_pass<D1, D2, TERMS, STATES>(a, a.pass[blockIdx.y], lds);
+    const Work w(a.s.H);
+    chunk_pass<D1, D2, TERMS, STATES>(a, a.pass[w.pass], w.slot, w.h, lds);
 }
 
 // passes over 64 x 128 and 128 x 64 states side by side
@@ -513,9 +525,10 @@ template <int TERMS>
 __global__ __launch_bounds__(512, 2) void la_chunk_mixed_kernel(LaArgs a) {
     constexpr int A = lds_bytes<64, 128, false>(), B = lds_bytes<128, 64, false>();
     __shared__ __align__(16) unsigned char lds[A > B ? A : B];
-    const LaPass& p = a.pass[blockIdx.y];
-    if (p.D2 == 128) chunk_pass<64, 128, TERMS, false>(a, p, lds);
-    else chunk_pass<128, 64, TERMS, false>(a, p, lds);
+    const Work w(a.s.H);
+    const LaPass& p = a.pass[w.pass];
+    if (p.D2 == 128) chunk_pass<64, 128, TERMS, false>(a, p, w.slot, w.h, lds);
+    else chunk_pass<128, 64, TERMS, false>(a, p, w.slot, w.h, lds);
 }
 
 // Entering states of the segments: for a sequence's segments in order,
