@@ -33,20 +33,19 @@ struct LaPlan {
 //
 // A workgroup of la_chunk.hip has a (segment, head)'s whole rows, and a CU to itself:
 // with fewer (sequence, head) pairs than CUs a sequence is cut into segments, which
-// costs a second reading of y and z and a wait between two launches.  la_narrow.hip
-// cuts the state's columns instead, which costs nothing but reads x and y once per 32
-// columns and z in 64-byte pieces; its chunk takes 1.2 us, so it wins where the CUs
-// hold all of its workgroups and the sequences are short.  Forward (and backward) of
-// H (sequence, head) pairs, 128 x 128, us:
-//             T = 512     2048        4096          8192
-//   H = 16    14 (16)     43 (45)     81 (83)       155 (158)   narrow
-//             28 (40)     37 (69)     50 (97)        65 (144)   rows, in segments
-//   H = 32    15 (24)     44 (65)     82 (121)      157 (262)   narrow
-//             28 (42)     45 (89)     61 (150)       95 (273)   rows
-//   H = 64    17 (35)     46 (112)    84 (233)      180 (476)   narrow
-//             32 (35)     57 (90)     93 (171)      174 (346)   rows
-// The rule: 512 workgroups of la_narrow.hip are in flight at once, and with s segments
-// to a sequence the other kernel takes about 20 us and 4 us for every s chunks.
+// costs a second reading of y and z and two more launches: about 27 us and 4 us for
+// every s chunks of 128 x 128, where s segments of every sequence are in flight.
+// la_narrow.hip cuts the state's columns instead, which costs nothing but reads x and y
+// once per 32 columns and z in 64-byte pieces: 1.25 us a chunk (0.85 with 64 rows), half
+// as much again where more of its workgroups than CUs are in flight (512 are).  Forward
+// (and backward) of H pairs, 128 x 128, in us, measured:
+//             T = 1024     2048        4096          8192
+//   H = 16    24 (25)     43 (44)     79 (80)       150 (153)   narrow
+//             28 (51)     35 (54)     49 (78)        64 (127)   segments
+//   H = 32    25 (37)     43 (64)     78 (120)      151 (270)   narrow
+//             31 (56)     47 (89)     62 (126)       98 (222)   segments
+//   H = 64    26          44          81            170         narrow
+//             38 (53)     62 (89)     96 (169)      182 (338)   segments (backward: whole)
 LaPlan plan(const LaCall& c, int passes) {
     LaPlan p{};
     kda::LaSeqs& s = p.s;
@@ -59,15 +58,23 @@ LaPlan plan(const LaCall& c, int passes) {
     const int64_t tokens = c.packed ? c.T : (int64_t)c.B * c.T;
     const int64_t chunks = (tokens / s.n_seqs + kda::LA_CHUNK - 1) / kda::LA_CHUNK;  // of an average sequence
     const int64_t pairs = (int64_t)s.n_seqs * c.H;
-    const int64_t segs = 256 / (pairs * passes);
+    const int64_t beside = pairs * passes;
+    const int64_t most = std::max<int64_t>(1, chunks / 3);  // segments of three chunks or more
     const int64_t narrow_groups = kda::la_narrow_groups(pairs, std::max(c.K, c.V)) * passes;
-    p.narrow = c.segments <= 0 && narrow_groups <= 512 &&
-               (c.segments < 0 || segs <= 3 || chunks * (6 * segs - 20) <= 100 * segs);
-    if (p.narrow) return p;
+    if (c.segments <= 0 && narrow_groups <= 512) {
+        const double size = (c.K + c.V) / 256.0, s_flight = std::min<double>(256.0 / beside, (double)most);
+        const bool rows64 = c.K == 64 && (passes == 1 || c.V == 64);
+        const double narrow_us = chunks * (rows64 ? 0.85 : 1.25) * (narrow_groups > 256 ? 1.5 : 1.0);
+        p.narrow = c.segments < 0 || narrow_us <= size * (27.0 + 4.0 * chunks / s_flight);
+        if (p.narrow) return p;
+    }
     int64_t per = c.segments;
     if (c.segments == 0) {
         per = -1;
-        const int64_t n = std::min<int64_t>(segs, chunks / 3);
+        // one round of workgroups, or two where they leave fewer CUs idle
+        int64_t n = 256 / beside;
+        if (n >= 2 && 512 / beside > 2 * n) n = 512 / beside;
+        n = std::min(n, most);
         if (n > 1) per = (chunks + n - 1) / n;
     }
     // (a segment that holds every token is the whole sequence)
@@ -80,17 +87,11 @@ LaPlan plan(const LaCall& c, int passes) {
             s.seg_per_seq = (c.T + s.seg_tokens - 1) / s.seg_tokens;
             s.n_slots = (int32_t)std::min<int64_t>((int64_t)s.seg_per_seq * s.n_seqs, INT32_MAX);
         }
-    } else if (c.packed && s.n_seqs <= 64 && pairs * passes > 256) {
+    } else if (c.packed && s.n_seqs <= 64 && beside > 256) {
         s.by_length = 1;
     }
     return p;
 }
-
-// A segment forms its entering state itself where those before it are few, which
-// reads them once more for each segment behind; a scan over many in a launch of its
-// own takes 10 us.  (2 x 2048 tokens, 32 heads, 4 segments: 72 us with the scan, 61
-// without.)
-bool self_entering(const kda::LaSeqs& s) { return (s.T + s.seg_tokens - 1) / s.seg_tokens <= 8; }
 
 size_t la_states_bytes(const LaCall& c, const kda::LaSeqs& s) {
     return s.seg_tokens ? align_up((size_t)s.n_slots * c.H * c.K * c.V * sizeof(float)) : 0;
@@ -217,20 +218,16 @@ int la_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float*
     if (s.seg_tokens) {
         float* states = static_cast<float*>(workspace);
         launch_states(s, log_decay, &p, &states, 1, str);
-        if (self_entering(s)) {
-            p.seg_states = states;
-        } else {
-            kda::LaScanArgs sc{};
-            sc.s = s;
-            sc.log_decay = log_decay;
-            sc.init[0] = initial_state;
-            sc.state[0] = states;
-            sc.elems = K * V;
-            sc.n_dirs = 1;
-            kda::launch_la_scan(sc, str);
-            p.s_in = states;
-            p.s_in_slots = 1;
-        }
+        kda::LaScanArgs sc{};
+        sc.s = s;
+        sc.log_decay = log_decay;
+        sc.init[0] = initial_state;
+        sc.state[0] = states;
+        sc.elems = K * V;
+        sc.n_dirs = 1;
+        kda::launch_la_scan(sc, str);
+        p.s_in = states;
+        p.s_in_slots = 1;
     }
     launch(pl, a, 1, str);
     return status();
@@ -263,24 +260,19 @@ int la_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float*
                             static_cast<float*>(workspace) + la_states_bytes(c, s) / sizeof(float)};
         const kda::LaPass p[2] = {make_pass(q, k, v, nullptr, K, V, V, 1, false, scale), pv};
         launch_states(s, log_decay, p, states, 2, str);
-        if (self_entering(s)) {
-            pq.seg_states = states[0];
-            pk.seg_states = pv.seg_states = states[1];
-        } else {
-            kda::LaScanArgs sc{};
-            sc.s = s;
-            sc.log_decay = log_decay;
-            sc.init[0] = initial_state;
-            sc.init[1] = d_final;
-            sc.state[0] = states[0];
-            sc.state[1] = states[1];
-            sc.elems = K * V;
-            sc.n_dirs = 2;
-            kda::launch_la_scan(sc, str);
-            pq.s_in = states[0];
-            pk.s_in = pv.s_in = states[1];
-            pq.s_in_slots = pk.s_in_slots = pv.s_in_slots = 1;
-        }
+        kda::LaScanArgs sc{};
+        sc.s = s;
+        sc.log_decay = log_decay;
+        sc.init[0] = initial_state;
+        sc.init[1] = d_final;
+        sc.state[0] = states[0];
+        sc.state[1] = states[1];
+        sc.elems = K * V;
+        sc.n_dirs = 2;
+        kda::launch_la_scan(sc, str);
+        pq.s_in = states[0];
+        pk.s_in = pv.s_in = states[1];
+        pq.s_in_slots = pk.s_in_slots = pv.s_in_slots = 1;
     }
     kda::LaArgs a{};
     a.s = s;

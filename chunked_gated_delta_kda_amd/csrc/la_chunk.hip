@@ -210,8 +210,7 @@ __device__ __forceinline__ void chunk_pass(const LaArgs& a, const LaPass& p, int
             }
         };
 
-        // one or two chunks ahead in registers, what they have room for
-        constexpr int SETS = 2;
+        constexpr int SETS = 2;  // chunks ahead in registers
         u32x4 xr[SETS][RV], yr[SETS][RV], zr[SETS][ZV];
         {
             u32x4 x0[RV], y0[RV], z0[ZV], x1[RV], y1[RV];
@@ -277,38 +276,14 @@ __device__ __forceinline__ void chunk_pass(const LaArgs& a, const LaPass& p, int
     for (int n = 0; n < NC; ++n)
 #pragma unroll
         for (int kt = 0; kt < NT; ++kt) S[n][kt] = floatx4{0.f, 0.f, 0.f, 0.f};
-    auto add_state = [&](const float* t, int64_t at) __attribute__((always_inline)) {
-        t += (at * H + h) * (D1 * D2) + state_at;
+    if (!STATES && p.s_in) {
+        const float* t = p.s_in + ((int64_t)(p.s_in_slots ? slot : sg.n) * H + h) * (D1 * D2) + state_at;
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
-            floatx4 u[NT];  // (all loads before the first sum)
+        for (int n = 0; n < NC; ++n)
 #pragma unroll
             for (int kt = 0; kt < NT; ++kt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) u[kt][i] = t[tile_channel(kt, 4 * g + i) * p.row + 16 * n * p.col];
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int kt = 0; kt < NT; ++kt) S[n][kt] += u[kt];
-        }
-    };
-    if constexpr (!STATES) {
-        if (p.s_in) add_state(p.s_in, p.s_in_slots ? slot : sg.n);
-        if (p.seg_states && sg.p0 > 0) {
-            // the segments before: E <- a^seg_tokens E + what each adds
-            const int before = sg.p0 / a.s.seg_tokens;
-            const float x = ld * (float)a.s.seg_tokens;
-            const bool near = x > -0.6f;
-            const float m0 = near ? 1.f : 0.f, m1 = near ? expm1f(x) : exp2_hw(l2 * (float)a.s.seg_tokens);
-            for (int i = 0; i < before; ++i) {
-#pragma unroll
-                for (int n = 0; n < NC; ++n)
-#pragma unroll
-                    for (int kt = 0; kt < NT; ++kt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) S[n][kt][e] = fmaf(S[n][kt][e], m1, S[n][kt][e] * m0);
-                add_state(p.seg_states, slot - before + i);
-            }
-        }
+                for (int i = 0; i < 4; ++i) S[n][kt][i] = t[tile_channel(kt, 4 * g + i) * p.row + 16 * n * p.col];
     }
     if (nc > 0) {
         ChunkDecay chunk_decay(ld);

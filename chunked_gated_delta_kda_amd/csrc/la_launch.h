@@ -25,9 +25,6 @@ struct LaPass {
     const float* s_in;     // entering states, fp32, or null (zeros)
     float* s_out;          // states left behind, fp32, or null (not written)
     int32_t s_in_slots;    // s_in holds one state per segment slot (else per sequence)
-    const float* seg_states;  // what each segment adds to a zero state, by slot, or null:
-                           // a segment then forms its entering state from s_in and the
-                           // segments before it
     int32_t s_out_slots;   // s_out: one per slot, of all segments but a sequence's last
                            // (else one per sequence, of its last segment)
     int32_t D1, D2;        // 64 or 128 each
