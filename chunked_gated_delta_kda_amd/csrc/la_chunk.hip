@@ -25,23 +25,22 @@
 //    y and z are read by transposing reads as operands that contract over tokens.
 // One barrier a chunk.
 //
-// What bounds it: of 256 workgroups in flight each chunk costs a SIMD 152 products of 16
-// cycles and about 700 other vector instructions, which overlap for a fifth only: 5200
-// cycles, 2.3 us, in which the CUs move 64 KB each, 7 TB/s if all were equal.  So long
-// batches are bound by instruction issue and by their last workgroups, not by memory:
-// 16 sequences of 256 to 8192 tokens, 32 heads of 128 x 128, take 595 us (2.55 GB,
-// 4.3 TB/s; the bytes alone take 520 us).  Measured on the way there (the same batch):
-// 32 columns a workgroup in waves that read z in 64-byte pieces 820 us; eight state
-// waves of 16 columns, which read x and y from LDS twice as often, 615; products and
-// conversions in the compiler's own order 616; one state wave per SIMD with the order
-// written out 595.
+// What bounds it: with every CU busy, HBM: 16 sequences of 256 to 8192 tokens, 32 heads
+// of 128 x 128, take 590 us for 2.55 GB, 4.3 TB/s, where a copy reaches 4.9.  With 64
+// workgroups the issue of instructions: a chunk costs a SIMD 152 products of 16 cycles
+// and about 700 other vector instructions, which overlap for a fifth only, 2.6 us in
+// all.  Measured on the way there (the packed batch):
+// 32 columns a workgroup, z in 64-byte pieces, 820 us; eight state waves of 16 columns,
+// which read x and y from LDS twice as often, 615; products and conversions in the
+// compiler's own order 616.
 //
 // Precision: raw bf16 operands; P and the copy of S are rounded to bf16 once each
 // (outputs are bf16).  The state itself is fp32 to its last bits where it is returned:
 // a token's decayed z is split into three bf16 terms (24 bits), so every product of
 // the update is exact, and the decays of the chunks do not drift from a's powers
 // (ChunkDecay).  Where no state is returned two terms (16 bits) are enough, since
-// the state is then only read through its rounding to 8 bits: 11% of a backward pass.
+// the state is then only read through its rounding to 8 bits (gradients of 24 packed
+// sequences, 16 heads of 128 x 64: 166 -> 158 us).
 #include "la_device.h"
 
 namespace kda {

@@ -2,7 +2,8 @@
 // sequence (gfx950): the single-token form of la_chunk.hip's recurrence,
 //   S' = a S + k v^T,   o = scale S'^T q,   a = exp(log_decay[h]).
 //
-// Bound by HBM: the state is read and written once (8 K V bytes a pair).  One
+// Bound by HBM: the state is read and written once (8 K V bytes a pair): 64
+// sequences of 32 heads of 128 x 128 (268 MB) take 52 us, 5.1 TB/s.  One
 // workgroup per (sequence, head, 64 value columns); thread (rg, cq) owns rows
 // RPT rg .. RPT rg + RPT - 1 and columns 4 cq .. 4 cq + 3 of the block, so a
 // row of the block is 16 threads x 16 bytes.  The sum over rows for o goes
