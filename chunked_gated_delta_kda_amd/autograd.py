@@ -198,6 +198,7 @@ class _LA:
                     return o, final
 
                 @staticmethod
+                @torch.autograd.function.once_differentiable
                 def backward(ctx, do, dfinal=None):
                     q, k, v, log_decay, h0, cu = ctx.saved_tensors
                     r = _b.la_bwd(q, k, v, log_decay, do.contiguous(), ctx.scale, h0,
@@ -226,6 +227,7 @@ class _GatedNorm:
                                              residual_scale)
 
                 @staticmethod
+                @torch.autograd.function.once_differentiable
                 def backward(ctx, dy):
                     x, gate, weight, residual, residual_scale = ctx.saved_tensors
                     r = _b.gated_norm_bwd(x, gate, weight, dy.contiguous(), ctx.activation,

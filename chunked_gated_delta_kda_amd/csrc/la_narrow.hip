@@ -82,13 +82,13 @@ __device__ __forceinline__ void narrow_pass(const LaArgs& a, const LaPass& p, un
 
     // z of a chunk: one 16-byte piece a thread, left in LDS as it is and, decayed
     // to the chunk's end, as three bf16 terms
-    const uint16_t* const zrow = p.z + (tok0 * H + h) * D2 + c0 + 8 * (tid & 3);
-    auto load_z = [&](int c) { return *reinterpret_cast<const u32x4*>(zrow + at(c, tid >> 2) * zstep); };
-    const float z_full = exp2_hw((LC - 1 - (tid >> 2) + late) * l2) * p.z_scale;
-    auto put_z = [&](int c, u32x4 raw) {
-        const int n = np - c * LC, row = tid >> 2;
-        float wt = z_full;
-        if (n < LC) wt = row < n ? exp2_hw((n - 1 - row + late) * l2) * p.z_scale : 0.f;
+    const uint16_t* const zrow = p.z + (tok0 * H + h) * D2 + c0 + 8 * (lane & 3);
+    auto load_z = [&](int c, int row) { return *reinterpret_cast<const u32x4*>(zrow + at(c, row) * zstep); };
+    auto weight = [&](int n, int row) { return row < n ? exp2_hw((n - 1 - row + late) * l2) * p.z_scale : 0.f; };
+    auto put_z = [&](int c, int row, float full, u32x4 raw) __attribute__((always_inline)) {
+        const int n = np - c * LC;
+        float wt = full;
+        if (n < LC) wt = weight(n, row);
         u32x4 term[3];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -96,9 +96,10 @@ __device__ __forceinline__ void narrow_pass(const LaArgs& a, const LaPass& p, un
 #pragma unroll
             for (int q = 0; q < 3; ++q) term[q][e] = take_term(v0, v1);
         }
-        *reinterpret_cast<u32x4*>(&ztile[c & 1][8 * tid]) = raw;
+        const int at = row * LA_COLS + 8 * (lane & 3);
+        *reinterpret_cast<u32x4*>(&ztile[c & 1][at]) = raw;
 #pragma unroll
-        for (int q = 0; q < 3; ++q) *reinterpret_cast<u32x4*>(&zterm[c & 1][q][8 * tid]) = term[q];
+        for (int q = 0; q < 3; ++q) *reinterpret_cast<u32x4*>(&zterm[c & 1][q][at]) = term[q];
     };
     // where a transposing read of a z tile starts (tile ct of 16 columns: + 4 ct)
     const int zt_off = (4 * g + (r >> 2)) * LA_COLS + 8 * (r & 3);
@@ -121,28 +122,42 @@ __device__ __forceinline__ void narrow_pass(const LaArgs& a, const LaPass& p, un
 #pragma unroll
             for (int j = 0; j < KS; ++j) koff[j] = r * D1 + 8 * ((4 * j + g) ^ swizzle<D1>(r));
 
-            u32x4 xs[2][KS], zs[2];
+            // rows of z that this wave stages: 32, 16, 16 and none, since the waves have
+            // one, two, three and four tiles of P
+            constexpr int ZN = W == 0 ? 2 : W == 3 ? 0 : 1, Z0 = W == 0 ? 0 : 16 * (W + 1);
+            const int zr = Z0 + (lane >> 2);
+            const float z_full0 = weight(LC, zr), z_full1 = weight(LC, zr + 16);
+            u32x4 xs[2][KS], zs[2][ZN + (ZN == 0)];
+            auto load_zs = [&](int c, u32x4 (&z)[ZN + (ZN == 0)]) __attribute__((always_inline)) {
+#pragma unroll
+                for (int i = 0; i < ZN; ++i) z[i] = load_z(c, zr + 16 * i);
+            };
+            auto put_zs = [&](int c, const u32x4 (&z)[ZN + (ZN == 0)]) __attribute__((always_inline)) {
+#pragma unroll
+                for (int i = 0; i < ZN; ++i) put_z(c, zr + 16 * i, i ? z_full1 : z_full0, z[i]);
+            };
             auto load_x = [&](int c, u32x4 (&x)[KS]) __attribute__((always_inline)) {
                 const uint16_t* q = xrow + at(c, i0) * ystep;
 #pragma unroll
                 for (int j = 0; j < KS; ++j) x[j] = *reinterpret_cast<const u32x4*>(q + 32 * j);
             };
             {
-                const u32x4 z0 = load_z(0);
+                u32x4 z0[ZN + (ZN == 0)];
+                load_zs(0, z0);
                 load_x(0, xs[0]);
-                zs[1] = load_z(1);
+                load_zs(1, zs[1]);
                 load_x(1, xs[1]);
-                zs[0] = load_z(2);
-                put_z(0, z0);
+                load_zs(2, zs[0]);
+                put_zs(0, z0);
             }
             __syncthreads();
             // chunk c from x; z holds chunk c + 1, and takes chunk c + 3
-            auto chunk = [&](int c, u32x4 (&x)[KS], u32x4& z, auto full) __attribute__((always_inline)) {
+            auto chunk = [&](int c, u32x4 (&x)[KS], u32x4 (&z)[ZN + (ZN == 0)], auto full) __attribute__((always_inline)) {
                 const int buf = c & 1;
                 const bf16* yt = ytile[buf];
                 const bf16* zt = ztile[buf] + zt_off;
-                if (c + 1 < nc) put_z(c + 1, z);
-                z = load_z(c + 3);
+                if (c + 1 < nc) put_zs(c + 1, z);
+                load_zs(c + 3, z);
                 // S^T x: D rows are the columns channel(ct, .), D columns the queries
                 floatx4 acc[2];
 #pragma unroll

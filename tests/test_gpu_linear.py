@@ -424,3 +424,13 @@ def test_outputs_without_the_last_state(H, K, V):
     o, S = kda.la_fwd(d["q"], d["k"], d["v"], d["ld"], d["scale"], d["h0"], output_final_state=False)
     assert S is None
     near_bf16("o", o, ref.la_fwd(w["q"], w["k"], w["v"], w["ld"], w["scale"], w["h0"])[0], magnitude(w)[0])
+
+
+def test_no_second_derivative():
+    d = dev(make(1, 70, 2, 64, 64, seed=770))
+    leaf = {n: d[n].clone().requires_grad_() for n in ("q", "k", "v")}
+    o, _ = kda.chunk_la(leaf["q"], leaf["k"], leaf["v"], d["ld"])
+    y = kda.gated_norm(o, leaf["v"], torch.ones(64, device=DEV))
+    (g,) = torch.autograd.grad(y.float().square().sum(), leaf["q"], create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable|does not require grad"):
+        g.float().sum().backward()
