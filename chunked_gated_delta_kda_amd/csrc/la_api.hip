@@ -12,6 +12,7 @@ namespace {
 
 constexpr size_t ALIGN = 256;
 constexpr int64_t I31 = (int64_t)1 << 31;
+constexpr int32_t MAX_HEADS = 65536;  // 32-bit byte offsets within a chunk's rows
 
 size_t align_up(size_t x) { return (x + ALIGN - 1) / ALIGN * ALIGN; }
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -98,7 +99,7 @@ size_t la_states_bytes(const LaCall& c, const kda::LaSeqs& s) {
 }
 
 bool valid_sizes(const LaCall& c) {
-    return c.B >= 1 && c.T >= 0 && c.H >= 1 && c.num_seqs >= 1 && supported_dim(c.K) && supported_dim(c.V) &&
+    return c.B >= 1 && c.T >= 0 && c.H >= 1 && c.H <= MAX_HEADS && c.num_seqs >= 1 && supported_dim(c.K) && supported_dim(c.V) &&
            (int64_t)c.B * c.T < I31;
 }
 
@@ -116,7 +117,7 @@ int check_la(const LaCall& c, float scale, const float* log_decay, const void* w
     if (!supported_dim(c.K) || !supported_dim(c.V)) return KDA_ERR_UNSUPPORTED;
     if ((int64_t)c.B * c.T >= I31 || !std::isfinite(scale) || !log_decay || !aligned(log_decay, 4))
         return KDA_ERR_INVALID_ARG;
-    if (c.H > 65536) return KDA_ERR_INVALID_ARG;  // 32-bit byte offsets within a chunk
+    if (c.H > MAX_HEADS) return KDA_ERR_INVALID_ARG;
     if (c.packed && (c.B != 1 || c.num_seqs < 1 || !aligned(c.cu, 4))) return KDA_ERR_INVALID_ARG;
     plan_out = plan(c, dirs == 2 ? 3 : 1);
     const kda::LaSeqs& s = plan_out.s;

@@ -17,7 +17,7 @@
 // What bounds it: the way it reads.  A column block reads z in 64-byte pieces and x
 // and y once per block through L2: 2 x 2048 tokens, 32 heads of 128 x 128 (134 MB)
 // take 50 us with or without the products, 2.7 TB/s; the products alone 35 us.  With
-// few workgroups it is the chunk's chain of products, about 1.2 us a chunk: 256 tokens,
+// few workgroups it is the chain within a chunk, 1.0 to 1.3 us: 256 tokens,
 // 4 heads of 64 x 64, take 6.4 us where la_chunk.hip takes 8.5.
 #include "la_device.h"
 
@@ -80,8 +80,8 @@ __device__ __forceinline__ void narrow_pass(const LaArgs& a, const LaPass& p, un
     const int64_t ystep = step * H * D1, zstep = step * H * D2;
     auto at = [&](int c, int row) { return (int64_t)min(c * LC + row, np - 1); };
 
-    // z of a chunk: one 16-byte piece a thread, left in LDS as it is and, decayed
-    // to the chunk's end, as three bf16 terms
+    // z of a chunk, in 16-byte pieces, left in LDS as it is and, decayed to the
+    // chunk's end, as three bf16 terms
     const uint16_t* const zrow = p.z + (tok0 * H + h) * D2 + c0 + 8 * (lane & 3);
     auto load_z = [&](int c, int row) { return *reinterpret_cast<const u32x4*>(zrow + at(c, row) * zstep); };
     auto weight = [&](int n, int row) { return row < n ? exp2_hw((n - 1 - row + late) * l2) * p.z_scale : 0.f; };

@@ -422,7 +422,8 @@ int gdn_bwd_saved(const uint16_t* q, const uint16_t* k, const uint16_t* v, const
  *    outputs of its 64-token chunk, and all later ones of its sequence, what
  *    they happen to be; it never leaves its sequence and head.
  *  - Alignment: q, k, v, o, states and all gradients 16 bytes; log_decay 4.
- *    H is at most 65536.
+ *    H is at most 65536, and there are fewer than 2^25 pairs of a head and a
+ *    sequence (or segment).
  *  - segment_chunks: 0 automatic, < 0 whole sequences, > 0 segments of that
  *    many 64-token chunks.  A sequence is one chain of chunks; where the
  *    (sequence, head) pairs are too few to fill the GPU, it is cut into

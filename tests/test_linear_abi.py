@@ -145,3 +145,8 @@ def test_la_refuses_rows_that_32_bit_offsets_do_not_reach(lib):
     """A chunk's rows are addressed by 32-bit byte offsets: at most 65536 heads."""
     assert la_fwd(lib, H=65537) == 1
     assert la_bwd(lib, H=65537) == 1
+
+
+def test_la_workspace_of_unsupported_heads(lib):
+    assert kda.la_workspace_size(1, 16, 65537, 64, 64) == 0
+    assert kda.la_workspace_size(1, 16, 65537, 64, 64, backward=True) == 0
