@@ -277,12 +277,14 @@ __device__ __forceinline__ void chunk_pass(const LaArgs& a, const LaPass& p, int
         for (int kt = 0; kt < NT; ++kt) S[n][kt] = floatx4{0.f, 0.f, 0.f, 0.f};
     if (!STATES && p.s_in) {
         const float* t = p.s_in + ((int64_t)(p.s_in_slots ? slot : sg.n) * H + h) * (D1 * D2) + state_at;
+        auto load = [&](int row) __attribute__((always_inline)) {
 #pragma unroll
-        for (int n = 0; n < NC; ++n)
+            for (int n = 0; n < NC; ++n)
 #pragma unroll
-            for (int kt = 0; kt < NT; ++kt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) S[n][kt][i] = t[tile_channel(kt, 4 * g + i) * p.row + 16 * n * p.col];
+                for (int kt = 0; kt < NT; ++kt) S[n][kt] = load_state(t + 16 * n * p.col, tile_channel(kt, 4 * g), row);
+        };
+        if (p.row == 1) load(1);
+        else load(p.row);
     }
     if (nc > 0) {
         ChunkDecay chunk_decay(ld);

@@ -139,6 +139,16 @@ __device__ __forceinline__ int swizzle(int m) {
     return D == 128 ? 4 * (m & 3) + ((m >> 2) & 3) : 4 * ((m >> 1) & 1) + ((m >> 2) & 3);
 }
 
+// Rows channel .. channel + 3 of a column of a state that enters (`row` elements
+// apart; a transposed state's are neighbours).
+__device__ __forceinline__ floatx4 load_state(const float* column, int channel, int row) {
+    if (row == 1) return *reinterpret_cast<const floatx4*>(column + channel);
+    floatx4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = column[(channel + i) * row];
+    return v;
+}
+
 // The decay of a chunk, a^64, lies between two neighbouring floats: `below`, and the
 // next, which is taken in a part `above` of the chunks.  So the product of any number
 // of chunks' decays stays within a rounding of a power of a, where one float's own

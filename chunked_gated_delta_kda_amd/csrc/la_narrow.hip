@@ -235,10 +235,12 @@ __device__ __forceinline__ void narrow_pass(const LaArgs& a, const LaPass& p, un
     const int scol = c0 + tile_channel(vh, r);
     if (p.s_in) {
         const float* s = p.s_in + ((int64_t)sg.n * H + h) * sz + (int64_t)scol * p.col;
+        auto load = [&](int row) __attribute__((always_inline)) {
 #pragma unroll
-        for (int kt = 0; kt < NT; ++kt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) S[kt][i] = s[tile_channel(kh * NT + kt, 4 * g + i) * p.row];
+            for (int kt = 0; kt < NT; ++kt) S[kt] = load_state(s, tile_channel(kh * NT + kt, 4 * g), row);
+        };
+        if (p.row == 1) load(1);
+        else load(p.row);
     } else {
 #pragma unroll
         for (int kt = 0; kt < NT; ++kt) S[kt] = floatx4{0.f, 0.f, 0.f, 0.f};
