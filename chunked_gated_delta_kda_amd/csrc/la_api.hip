@@ -121,7 +121,8 @@ int check_la(const LaCall& c, float scale, const float* log_decay, const void* w
     if (c.packed && (c.B != 1 || c.num_seqs < 1 || !aligned(c.cu, 4))) return KDA_ERR_INVALID_ARG;
     plan_out = plan(c, dirs == 2 ? 3 : 1);
     const kda::LaSeqs& s = plan_out.s;
-    // one grid over (slot, head, column block), and over (sequence, head, piece of a state)
+    // (workgroups of a launch are counted in 32 bits: three passes over the slots and
+    // heads, sixteen pieces of a state)
     if ((int64_t)s.n_slots * c.H >= I31 / 64) return KDA_ERR_INVALID_ARG;
     const size_t need = (size_t)dirs * la_states_bytes(c, s);
     if (need && (!ws || !aligned(ws, ALIGN) || ws_bytes < need)) return KDA_ERR_WORKSPACE;

@@ -478,11 +478,11 @@ __device__ __forceinline__ void chunk_pass(const LaArgs& a, const LaPass& p, int
 }
 
 // A workgroup's part of a launch of (heads of a slot x slots, passes): heads fastest,
-// then the passes, which read the same rows, then the slots.
+// then the passes, which read the same rows, then the slots (see wide_grid).
 struct Work {
     int pass, slot, h;
     __device__ __forceinline__ explicit Work(int H) {
-        const uint32_t id = blockIdx.y * gridDim.x + blockIdx.x;
+        const uint32_t id = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
         h = id % H;
         pass = id / H % gridDim.y;
         slot = id / H / gridDim.y;
@@ -493,6 +493,7 @@ template <int D1, int D2, int TERMS, bool STATES>
 __global__ __launch_bounds__(512, 2) void la_chunk_kernel(LaArgs a) {
     __shared__ __align__(16) unsigned char lds[lds_bytes<D1, D2, STATES>()];
     const Work w(a.s.H);
+    if (w.slot >= a.s.n_slots) return;
     chunk_pass<D1, D2, TERMS, STATES>(a, a.pass[w.pass], w.slot, w.h, lds);
 }
 
@@ -502,6 +503,7 @@ __global__ __launch_bounds__(512, 2) void la_chunk_mixed_kernel(LaArgs a) {
     constexpr int A = lds_bytes<64, 128, false>(), B = lds_bytes<128, 64, false>();
     __shared__ __align__(16) unsigned char lds[A > B ? A : B];
     const Work w(a.s.H);
+    if (w.slot >= a.s.n_slots) return;
     const LaPass& p = a.pass[w.pass];
     if (p.D2 == 128) chunk_pass<64, 128, TERMS, false>(a, p, w.slot, w.h, lds);
     else chunk_pass<128, 64, TERMS, false>(a, p, w.slot, w.h, lds);
@@ -547,7 +549,7 @@ void launch_la_chunk(const LaArgs& a, int n, bool states, hipStream_t stream) {
         if (a.pass[i].s_out) terms = 3;
         mixed |= a.pass[i].D1 != a.pass[0].D1;
     }
-    const dim3 grid((unsigned)((int64_t)a.s.n_slots * a.s.H), (unsigned)n);
+    const dim3 grid = wide_grid((int64_t)a.s.n_slots * a.s.H, 512, (unsigned)n);
     if (mixed) {
         if (terms == 3) hipLaunchKernelGGL((la_chunk_mixed_kernel<3>), grid, dim3(512), 0, stream, a);
         else hipLaunchKernelGGL((la_chunk_mixed_kernel<2>), grid, dim3(512), 0, stream, a);

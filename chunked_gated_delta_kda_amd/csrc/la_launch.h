@@ -11,6 +11,16 @@ namespace kda {
 
 constexpr int LA_CHUNK = 64;  // tokens per chunk
 
+// A grid of at least `groups` workgroups of `threads` threads over x and z, y as given:
+// HIP launches fewer than 2^32 work items in a dimension, and a grid beyond that was
+// seen to wrap without an error.  Workgroup z * gridDim.x + x; those from `groups` on
+// have no work.
+inline dim3 wide_grid(int64_t groups, int threads, unsigned y = 1) {
+    const int64_t most = ((int64_t)1 << 31) / threads;
+    const int64_t z = (groups + most - 1) / most;
+    return dim3((unsigned)((groups + z - 1) / z), y, (unsigned)z);
+}
+
 // One chunked pass over the tokens of a batch (la_chunk.hip):
 //   O_p = x_scale a^(p+1-late) S_in^T x_p + in_scale sum_{j<=p} a^(p-j) (x_p . y_j) z_j
 //   S_out = a^n S_in + z_scale sum_j a^(n-1-j+late) y_j z_j^T
