@@ -515,8 +515,10 @@ __global__ __launch_bounds__(512, 2) void la_chunk_mixed_kernel(LaArgs a) {
 __global__ __launch_bounds__(256) void la_scan_kernel(LaScanArgs a) {
     const int dir = blockIdx.y;
     const int per = a.elems / 1024;  // workgroups per state (K V is a multiple of 4096)
-    const int pair = blockIdx.x / per, n = pair / a.s.H, h = pair % a.s.H;
-    const int e = (int)(blockIdx.x % per * 256 + threadIdx.x) * 4;
+    const uint32_t wg = blockIdx.z * gridDim.x + blockIdx.x;
+    const int pair = wg / per, n = pair / a.s.H, h = pair % a.s.H;
+    if (n >= a.s.n_seqs) return;
+    const int e = (int)(wg % per * 256 + threadIdx.x) * 4;
     int slot, len;
     if (!a.s.cu) {
         slot = n * a.s.seg_per_seq;
@@ -571,7 +573,7 @@ void launch_la_chunk(const LaArgs& a, int n, bool states, hipStream_t stream) {
 }
 
 void launch_la_scan(const LaScanArgs& a, hipStream_t stream) {
-    const dim3 grid((unsigned)((int64_t)a.s.n_seqs * a.s.H * (a.elems / 1024)), (unsigned)a.n_dirs);
+    const dim3 grid = wide_grid((int64_t)a.s.n_seqs * a.s.H * (a.elems / 1024), 256, (unsigned)a.n_dirs);
     hipLaunchKernelGGL(la_scan_kernel, grid, dim3(256), 0, stream, a);
 }
 

@@ -48,3 +48,25 @@ def test_linear_attention_of_2_to_the_23_pairs():
     near("dv", r["dv"], q, k, do)
     near("dk", r["dk"], do, v, q)
     near("dq", r["dq"], do, v, k)
+
+
+def test_segments_of_2_to_the_22_states():
+    """The scan over segments has a work item for every four elements of a state: here
+    2^32, nearly all of empty sequences."""
+    H, D, N = 64, 64, 1 << 16
+    lens = {5: 200, N - 1: 170}
+    T = sum(lens.values())
+    cu = torch.zeros(N + 1, dtype=torch.int32)
+    cu[6:] = 200
+    cu[N] = T
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    q, k, v = (normal(gen, 1, T, H, D) for _ in range(3))
+    ld = torch.full((H,), -0.02, device=DEV)
+    ws = torch.empty(kda.la_workspace_size(1, T, H, D, D, N, 1), dtype=torch.uint8, device=DEV)
+    say(f"[la] {N} sequences, {H} heads, {ws.numel() / 2 ** 30:.0f} GiB of segments' states")
+    ws.fill_(255)
+    o, _ = kda.la_fwd(q, k, v, ld, cu_seqlens=cu.to(DEV), output_final_state=False, workspace=ws,
+                      segment_chunks=1)
+    few = torch.tensor([0, 200, T], dtype=torch.int32, device=DEV)
+    want, _ = kda.la_fwd(q, k, v, ld, cu_seqlens=few, output_final_state=False, segment_chunks=1)
+    assert torch.equal(o, want)
