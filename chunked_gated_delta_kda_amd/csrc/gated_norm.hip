@@ -60,7 +60,7 @@ template <int L>
 __global__ __launch_bounds__(GN_THREADS) void gated_norm_fwd_kernel(GatedNormArgs a) {
     constexpr int RPW = GN_THREADS / L;  // rows per workgroup
     const int l = threadIdx.x % L, c = 8 * l;
-    const int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / L;
+    const int64_t row = ((int64_t)blockIdx.z * gridDim.x + blockIdx.x) * RPW + threadIdx.x / L;
     if (row >= a.rows) return;  // (all lanes of a row together)
     const bool in = c < a.D;
     const int64_t at = row * a.D + c;
@@ -250,8 +250,8 @@ void launch_gated_norm_fwd(const GatedNormArgs& a, hipStream_t stream) {
     by_lanes(row_lanes(a.D), [&](auto l) {
         constexpr int L = decltype(l)::value;
         constexpr int RPW = GN_THREADS / L;
-        hipLaunchKernelGGL((gated_norm_fwd_kernel<L>), dim3((unsigned)((a.rows + RPW - 1) / RPW)), dim3(GN_THREADS), 0,
-                           stream, a);
+        hipLaunchKernelGGL((gated_norm_fwd_kernel<L>), wide_grid((a.rows + RPW - 1) / RPW, GN_THREADS), dim3(GN_THREADS),
+                           0, stream, a);
     });
 }
 

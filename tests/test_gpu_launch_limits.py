@@ -70,3 +70,17 @@ def test_segments_of_2_to_the_22_states():
     few = torch.tensor([0, 200, T], dtype=torch.int32, device=DEV)
     want, _ = kda.la_fwd(q, k, v, ld, cu_seqlens=few, output_final_state=False, segment_chunks=1)
     assert torch.equal(o, want)
+
+
+def test_gated_norm_of_2_to_the_26_rows():
+    """64 lanes a row: 2^32 work items, in place."""
+    rows, D = (1 << 26) + 70, 264
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    x = normal(gen, rows, 1, D)
+    w = torch.randn(D, generator=gen, device=DEV)
+    at = [0, (1 << 25) - 3, (1 << 26) - 50, rows - 100]
+    say(f"[norm] {rows} rows of {D}")
+    want = [kda.gated_norm_fwd(x[i:i + 100].clone(), None, w) for i in at]
+    kda.gated_norm_fwd(x, None, w, out=x)
+    for i, y in zip(at, want):
+        assert torch.equal(x[i:i + 100], y), i
