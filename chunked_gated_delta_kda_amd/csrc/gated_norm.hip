@@ -193,12 +193,14 @@ __device__ __forceinline__ double sum_strided(const float* p, int64_t n, int64_t
 __global__ __launch_bounds__(GN_THREADS) void gated_norm_sum_kernel(GatedNormArgs a) {
     __shared__ double red[GN_THREADS];
     const int tid = threadIdx.x, wb = a.D / 8;
+    const int64_t wg = (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
+    if (wg >= (int64_t)wb + a.H) return;
     double s = 0.0;
-    const bool weight = (int)blockIdx.x < wb;
-    const int h = (int)blockIdx.x - wb;
+    const bool weight = wg < wb;
+    const int h = (int)(wg - wb);
     if (weight) {
         const int first = tid / 8, step = GN_THREADS / 8;
-        s = sum_strided(a.part_w + (int64_t)first * a.D + 8 * blockIdx.x + tid % 8,
+        s = sum_strided(a.part_w + (int64_t)first * a.D + 8 * wg + tid % 8,
                         ((int64_t)a.groups - first + step - 1) / step, (int64_t)step * a.D);
     } else {
         s = sum_strided(a.row_ds + (int64_t)tid * a.H + h, (a.rows / a.H - tid + GN_THREADS - 1) / GN_THREADS,
@@ -212,7 +214,7 @@ __global__ __launch_bounds__(GN_THREADS) void gated_norm_sum_kernel(GatedNormArg
         __syncthreads();
     }
     if (tid < keep) {
-        if (weight) a.dweight[8 * blockIdx.x + tid] = (float)red[tid];
+        if (weight) a.dweight[8 * wg + tid] = (float)red[tid];
         else a.dres_scale[h] = (float)red[0];
     }
 }
@@ -260,8 +262,8 @@ void launch_gated_norm_bwd(const GatedNormArgs& a, hipStream_t stream) {
         hipLaunchKernelGGL((gated_norm_bwd_kernel<decltype(l)::value>), dim3((unsigned)a.groups), dim3(GN_THREADS), 0,
                            stream, a);
     });
-    hipLaunchKernelGGL(gated_norm_sum_kernel, dim3((unsigned)(a.D / 8 + (a.res_scale ? a.H : 0))), dim3(GN_THREADS), 0, stream,
-                       a);
+    hipLaunchKernelGGL(gated_norm_sum_kernel, wide_grid(a.D / 8 + (a.res_scale ? (int64_t)a.H : 0), GN_THREADS),
+                       dim3(GN_THREADS), 0, stream, a);
 }
 
 }  // namespace kda

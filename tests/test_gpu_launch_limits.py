@@ -84,3 +84,20 @@ def test_gated_norm_of_2_to_the_26_rows():
     kda.gated_norm_fwd(x, None, w, out=x)
     for i, y in zip(at, want):
         assert torch.equal(x[i:i + 100], y), i
+
+
+def test_gated_norm_gradients_of_2_to_the_24_heads():
+    """A workgroup for each head's sum."""
+    H, D = (1 << 24) + 6, 8
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    x, gate, res, dy = (normal(gen, 1, H, D) for _ in range(4))
+    w, rs = torch.randn(D, generator=gen, device=DEV), torch.randn(H, generator=gen, device=DEV)
+    say(f"[norm] one token, {H} heads of {D}")
+    r = kda.gated_norm_bwd(x, gate, w, dy, "silu", residual=res, residual_scale=rs)
+    for s in (slice(0, H // 2), slice(H // 2, H)):
+        half = [t[:, s].contiguous() for t in (x, gate, dy, res)]
+        h = kda.gated_norm_bwd(half[0], half[1], w, half[2], "silu", residual=half[3],
+                               residual_scale=rs[s].contiguous())
+        for n in ("dx", "dgate", "dresidual"):
+            assert torch.equal(r[n][:, s], h[n]), n
+        assert torch.equal(r["dresidual_scale"][s], h["dresidual_scale"])
