@@ -28,9 +28,11 @@ __global__ __launch_bounds__(LD_THREADS) void la_decode_kernel(LaDecodeArgs a) {
     constexpr int RPT = K / LD_RG;
     __shared__ floatx4 red[LD_RG][LD_CQ];
     const int vb = a.V / LD_COLS;
-    const int pair = blockIdx.x / vb, h = pair % a.H;
+    const uint32_t wg = blockIdx.z * gridDim.x + blockIdx.x;
+    if (wg / vb >= (uint32_t)a.n_pairs) return;
+    const int pair = wg / vb, h = pair % a.H;
     const int tid = threadIdx.x, cq = tid % LD_CQ, rg = tid / LD_CQ;
-    const int r0 = RPT * rg, c0 = (int)(blockIdx.x % vb) * LD_COLS + 4 * cq;
+    const int r0 = RPT * rg, c0 = (int)(wg % vb) * LD_COLS + 4 * cq;
     const int64_t base = (int64_t)pair * K * a.V + (int64_t)r0 * a.V + c0;
 
     floatx4 S[RPT];
@@ -67,7 +69,7 @@ __global__ __launch_bounds__(LD_THREADS) void la_decode_kernel(LaDecodeArgs a) {
 }
 
 void launch_la_decode(const LaDecodeArgs& a, int K, hipStream_t stream) {
-    const dim3 grid((unsigned)((int64_t)a.n_pairs * (a.V / LD_COLS)));
+    const dim3 grid = wide_grid((int64_t)a.n_pairs * (a.V / LD_COLS), LD_THREADS);
     if (K == 128) hipLaunchKernelGGL((la_decode_kernel<128>), grid, dim3(LD_THREADS), 0, stream, a);
     else hipLaunchKernelGGL((la_decode_kernel<64>), grid, dim3(LD_THREADS), 0, stream, a);
 }

@@ -464,8 +464,8 @@ int la_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float*
 /* One token for each of N sequences (see kda_decode for the layouts): q, k
  * [N, H, K], v, o [N, H, V] bf16; state_in (NULL: zeros), state_out
  * [N, H, K, V] fp32, which may be the same array (update in place).  T steps
- * equal the forward pass over T tokens up to rounding.  Alignment: q, k,
- * states 16 bytes; v, o 8. */
+ * equal the forward pass over T tokens up to rounding.  N * H * V / 64 < 2^31.
+ * Alignment: q, k, states 16 bytes; v, o 8. */
 int la_decode(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float* log_decay,
               float scale, const float* state_in, float* state_out, int32_t N, int32_t H,
               int32_t K, int32_t V, uint16_t* o, void* stream);

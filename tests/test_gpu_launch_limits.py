@@ -101,3 +101,21 @@ def test_gated_norm_gradients_of_2_to_the_24_heads():
         for n in ("dx", "dgate", "dresidual"):
             assert torch.equal(r[n][:, s], h[n]), n
         assert torch.equal(r["dresidual_scale"][s], h["dresidual_scale"])
+
+
+def test_decode_of_2_to_the_24_pairs():
+    """256 GiB of states, updated in place."""
+    N, H, D = (1 << 18) + 1, 64, 64
+    free = torch.cuda.mem_get_info()[0]
+    if free < (N * H * D * (D * 4 + 8) + (2 << 30)):
+        pytest.skip(f"{free / 2 ** 30:.0f} GiB of device memory are free")
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    q, k, v = (normal(gen, N, H, D) for _ in range(3))
+    ld = torch.full((H,), -0.3, device=DEV)
+    state = torch.full((N, H, D, D), 0.5, device=DEV)
+    say(f"[la] {N} sequences, {H} heads, {state.numel() * 4 / 2 ** 30:.0f} GiB of states")
+    o, S = kda.la_decode(q, k, v, ld, state=state, state_out=state)
+    for i in (0, 1 << 17, N - 2, N - 1):
+        one = [t[i:i + 1].contiguous() for t in (q, k, v)]
+        ow, Sw = kda.la_decode(*one, ld, state=torch.full((1, H, D, D), 0.5, device=DEV))
+        assert torch.equal(o[i:i + 1], ow) and torch.equal(S[i:i + 1], Sw), i
