@@ -103,11 +103,29 @@ bool valid_sizes(const LaCall& c) {
            (int64_t)c.B * c.T < I31;
 }
 
+// Workgroups of a launch are counted in 32 bits: three passes over the slots and heads,
+// sixteen pieces of a state.
+bool countable(const kda::LaSeqs& s) { return (int64_t)s.n_slots * s.H < I31 / 64; }
+
 // workspace bytes (dirs: 1 forward, 2 backward); 0: sizes that are not supported
 size_t la_workspace(const LaCall& c, int dirs) {
     if (!valid_sizes(c)) return 0;
     const kda::LaSeqs s = plan(c, dirs == 2 ? 3 : 1).s;
-    return std::max(ALIGN, (size_t)dirs * la_states_bytes(c, s));
+    return countable(s) ? std::max(ALIGN, (size_t)dirs * la_states_bytes(c, s)) : 0;
+}
+
+// The same without knowing whether cu_seqlens will be passed: batches of these sizes plan
+// alike but for the slots.  One row with num_seqs other than 1 is packed; else a B = 1
+// batch may be either, and gets the larger of the two.
+size_t la_any_workspace(int32_t B, int32_t T, int32_t H, int32_t K, int32_t V, int32_t num_seqs, int32_t segments,
+                        int dirs) {
+    const LaCall fixed{nullptr, false, num_seqs, B, T, H, K, V, segments};
+    const size_t f = la_workspace(fixed, dirs);
+    if (B != 1) return f;
+    LaCall packed = fixed;
+    packed.packed = true;
+    const size_t p = la_workspace(packed, dirs);
+    return num_seqs != 1 && !p ? 0 : std::max(f, p);
 }
 
 // Checks of every pass; fills the plan.
@@ -121,9 +139,7 @@ int check_la(const LaCall& c, float scale, const float* log_decay, const void* w
     if (c.packed && (c.B != 1 || c.num_seqs < 1 || !aligned(c.cu, 4))) return KDA_ERR_INVALID_ARG;
     plan_out = plan(c, dirs == 2 ? 3 : 1);
     const kda::LaSeqs& s = plan_out.s;
-    // (workgroups of a launch are counted in 32 bits: three passes over the slots and
-    // heads, sixteen pieces of a state)
-    if ((int64_t)s.n_slots * c.H >= I31 / 64) return KDA_ERR_INVALID_ARG;
+    if (!countable(s)) return KDA_ERR_INVALID_ARG;
     const size_t need = (size_t)dirs * la_states_bytes(c, s);
     if (need && (!ws || !aligned(ws, ALIGN) || ws_bytes < need)) return KDA_ERR_WORKSPACE;
     return KDA_OK;
@@ -177,22 +193,12 @@ extern "C" {
 
 size_t la_fwd_workspace_size(int32_t B, int32_t T, int32_t H, int32_t K, int32_t V, int32_t num_seqs,
                              int32_t segment_chunks) {
-    // (packed and fixed-length batches of these sizes plan alike but for the
-    // slots: the larger of the two)
-    const LaCall f{nullptr, false, num_seqs, B, T, H, K, V, segment_chunks};
-    LaCall p = f;
-    p.packed = true;
-    const size_t a = la_workspace(f, 1);
-    return B == 1 && a ? std::max(a, la_workspace(p, 1)) : a;
+    return la_any_workspace(B, T, H, K, V, num_seqs, segment_chunks, 1);
 }
 
 size_t la_bwd_workspace_size(int32_t B, int32_t T, int32_t H, int32_t K, int32_t V, int32_t num_seqs,
                              int32_t segment_chunks) {
-    const LaCall f{nullptr, false, num_seqs, B, T, H, K, V, segment_chunks};
-    LaCall p = f;
-    p.packed = true;
-    const size_t a = la_workspace(f, 2);
-    return B == 1 && a ? std::max(a, la_workspace(p, 2)) : a;
+    return la_any_workspace(B, T, H, K, V, num_seqs, segment_chunks, 2);
 }
 
 int la_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float* log_decay, float scale,

@@ -150,3 +150,23 @@ def test_la_refuses_rows_that_32_bit_offsets_do_not_reach(lib):
 def test_la_workspace_of_unsupported_heads(lib):
     assert kda.la_workspace_size(1, 16, 65537, 64, 64) == 0
     assert kda.la_workspace_size(1, 16, 65537, 64, 64, backward=True) == 0
+
+
+@pytest.mark.parametrize("packed,N,T,H,seg,refused", [
+    (False, 1 << 23, 2, 64, 0, True), (False, 1 << 23, 2, 4, -1, True), (False, 1 << 23, 2, 3, 0, False),
+    (False, 1 << 20, 1024, 64, 1, True), (False, 1 << 19, 1024, 4, 4, False), (False, 1 << 25, 1, 1, 0, True),
+    (False, (1 << 25) - 1, 1, 1, 0, False), (False, 3, 1 << 20, 2048, 1, True), (False, 3, 1 << 20, 512, 1, False),
+    (True, 1 << 24, 5, 2, 0, True), (True, (1 << 24) - 1, 5, 2, 0, False), (True, 7, (1 << 31) - 1, 1, 1, True),
+    (True, 7, 1 << 30, 1, 1, False)])
+def test_la_workspace_size_is_0_where_the_call_refuses(lib, packed, N, T, H, seg, refused):
+    """More pairs of a head and a slot than a launch counts: refused by the size already,
+    not by an allocation of terabytes."""
+    B = 1 if packed else N
+    over = dict(cu=FAKE if packed else None, N=N, B=B, T=T, H=H, K=64, V=64, seg=seg)
+    for call, backward in ((la_fwd, False), (la_bwd, True)):
+        size = kda.la_workspace_size(B, T, H, 64, 64, N, seg, backward=backward)
+        assert (size == 0) == refused
+        if refused:  # (of a call that is not, nothing may be enqueued here)
+            assert call(lib, **over, ws=FAKE, wsb=1 << 62) == 1
+        elif size > 256:
+            assert call(lib, **over) == 3
