@@ -51,8 +51,12 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-// 1 / (1 + e^-z), to a few ulps for every finite z
-__device__ __forceinline__ float gate_sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
+// 1 / (1 + e^-z) as e^min(z, 0) / (1 + e^-|z|): to a few ulps where it is normal, and
+// subnormal below z = -87 (e^-z would be infinite there, and the gate closed too early).
+__device__ __forceinline__ float gate_sigmoid(float z) {
+    const float e = expf(-fabsf(z));
+    return (z < 0.f ? e : 1.f) / (1.f + e);
+}
 
 }  // namespace
 

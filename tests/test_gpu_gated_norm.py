@@ -212,3 +212,25 @@ def test_layer_forward_backward_and_decode(kind):
                             p["residual_scale"])
         # the attention's output is rounded to bf16 between the two, and the result again
         assert np.linalg.norm(y1.double().cpu().numpy() - yc) <= 3 * 2.0 ** -8 * np.linalg.norm(yc)
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+def test_closed_gates_keep_their_tail(act):
+    """sigmoid(z) is subnormal from z = -88 to -103.  There e^z and what is multiplied
+    by it are multiples of 2^-149 and off by a few of them (at most four roundings and
+    an ulp or two of the exponential: 8 * 2^-149 times the other factors), and the
+    result is a multiple of bf16's 2^-133: half a step is 2^-134."""
+    w = make((16, 2, 64), seed=59, res=False)
+    w["gate"] = (-86.0 - 14.0 * torch.rand(16, 2, 64, generator=torch.Generator().manual_seed(61))).to(torch.bfloat16)
+    y, r = run(w, act)
+    c = {k: None if t is None else t.double() for k, t in w.items()}
+    want = ref.gated_norm(c["x"], c["gate"], c["weight"], act, 1e-6, None, None, c["dy"])
+    x, z, wt, dy = (c[n].numpy() for n in ("x", "gate", "weight", "dy"))
+    n = np.abs(x) / np.sqrt((x * x).mean(-1, keepdims=True) + 1e-6)
+    factor = 1 + np.abs(z)  # (silu's z s, and z (1 - s) in its slope)
+    for name, got, others in (("y", y, n * np.abs(wt)), ("dgate", r["dgate"], np.abs(dy * wt) * n)):
+        g = got.double().cpu().numpy()
+        tiny = 8 * 2.0 ** -149 * others * factor + 2.0 ** -134
+        bad = np.abs(g - want[name]) - 2.0 ** -8 * np.abs(want[name]) - FINE * others * factor * np.exp(z) - tiny
+        assert bad.max() <= 0, (name, bad.max())
+        assert np.abs(want[name]).max() > 64 * 2.0 ** -133  # not all below what is told apart
