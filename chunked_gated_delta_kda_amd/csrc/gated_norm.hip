@@ -51,12 +51,18 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-// 1 / (1 + e^-z) as e^min(z, 0) / (1 + e^-|z|): to a few ulps where it is normal, and
-// subnormal below z = -87 (e^-z would be infinite there, and the gate closed too early).
-__device__ __forceinline__ float gate_sigmoid(float z) {
-    const float e = expf(-fabsf(z));
-    return (z < 0.f ? e : 1.f) / (1.f + e);
-}
+// A gate's sigmoid 1 / (1 + e^-z) as e^min(z, 0) / (1 + e^-|z|): to a few ulps where it
+// is normal, and subnormal below z = -87 (e^-z would be infinite there, and the gate
+// closed too early).  `rest` is 1 - s, which a difference would round away where the gate
+// is open; the slope is their product.
+struct Sigmoid {
+    float s, rest;
+    __device__ __forceinline__ explicit Sigmoid(float z) {
+        const float e = expf(-fabsf(z)), r = 1.f / (1.f + e);
+        s = z < 0.f ? e * r : r;
+        rest = z < 0.f ? r : e * r;
+    }
+};
 
 }  // namespace
 
@@ -91,7 +97,7 @@ __global__ __launch_bounds__(GN_THREADS) void gated_norm_fwd_kernel(GatedNormArg
     for (int e = 0; e < 8; ++e) {
         u[e] *= rho * w[e];
         if (a.gate) {
-            const float s = gate_sigmoid(z[e]);
+            const float s = Sigmoid(z[e]).s;
             u[e] *= a.silu ? z[e] * s : s;
         }
     }
@@ -132,9 +138,9 @@ __global__ __launch_bounds__(GN_THREADS) void gated_norm_bwd_kernel(GatedNormArg
             act[e] = 1.f;
             slope[e] = 0.f;
             if (a.gate) {
-                const float s = gate_sigmoid(z[e]);
-                act[e] = a.silu ? z[e] * s : s;
-                slope[e] = a.silu ? s * (1.f + z[e] * (1.f - s)) : s * (1.f - s);
+                const Sigmoid g(z[e]);
+                act[e] = a.silu ? z[e] * g.s : g.s;
+                slope[e] = a.silu ? g.s * (1.f + z[e] * g.rest) : g.s * g.rest;
             }
             ss = fmaf(u[e], u[e], ss);
             pu = fmaf(dy[e] * w[e] * act[e], u[e], pu);

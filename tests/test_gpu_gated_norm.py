@@ -234,3 +234,18 @@ def test_closed_gates_keep_their_tail(act):
         bad = np.abs(g - want[name]) - 2.0 ** -8 * np.abs(want[name]) - FINE * others * factor * np.exp(z) - tiny
         assert bad.max() <= 0, (name, bad.max())
         assert np.abs(want[name]).max() > 64 * 2.0 ** -133  # not all below what is told apart
+
+
+def test_open_gates_keep_their_slope():
+    """sigmoid'(z) = s (1 - s), of which 1 - s is e^-z for an open gate: it is to be as
+    good as s is, though s is next to one (2^-17 of the product, as everywhere here, and
+    below z = 80 it is normal)."""
+    w = make((16, 2, 64), seed=67, res=False)
+    w["gate"] = (80.0 * torch.rand(16, 2, 64, generator=torch.Generator().manual_seed(71))).to(torch.bfloat16)
+    _, r = run(w, "sigmoid")
+    x, z, wt, dy = (w[n].double().numpy() for n in ("x", "gate", "weight", "dy"))
+    want = dy * wt * x / np.sqrt((x * x).mean(-1, keepdims=True) + 1e-6) * np.exp(-z) / (1 + np.exp(-z)) ** 2
+    g = r["dgate"].double().cpu().numpy()
+    bad = np.abs(g - want) - (2.0 ** -8 + FINE) * np.abs(want) - 2.0 ** -134
+    assert bad.max() <= 0, bad.max()
+    assert (np.abs(g) > 0).mean() > 0.9
