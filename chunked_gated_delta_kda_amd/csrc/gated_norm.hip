@@ -51,6 +51,23 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
+// Power of two that a row is multiplied by where the mean of its squares, plus eps, is
+// not within 2^-100 .. 2^100: there the squares (or rho^2 in the gradients) leave fp32's
+// range, though the norm is of the size of one.  It brings the larger of the row's
+// largest value and sqrt(eps) to 1 .. 2.  1 for the other rows, for a row of zeros
+// without eps and for one with an infinity or a NaN.
+template <int L>
+__device__ __forceinline__ float row_scale(const float (&u)[8], float mean, float eps) {
+    if (mean >= 0x1p-100f && mean <= 0x1p100f) return 1.f;
+    float m = sqrtf(eps);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(u[e]));
+#pragma unroll
+    for (int k = 1; k < L; k <<= 1) m = fmaxf(m, __shfl_xor(m, k));
+    if (!(m > 0.f && m <= 0x1.fffffep127f)) return 1.f;
+    return ldexpf(1.f, min(max(-ilogbf(m), -126), 126));
+}
+
 // A gate's sigmoid 1 / (1 + e^-z) as e^min(z, 0) / (1 + e^-|z|): to a few ulps where it
 // is normal, and subnormal below z = -87 (e^-z would be infinite there, and the gate
 // closed too early).  `rest` is 1 - s, which a difference would round away where the gate
@@ -91,7 +108,18 @@ __global__ __launch_bounds__(GN_THREADS) void gated_norm_fwd_kernel(GatedNormArg
     float ss = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(u[e], u[e], ss);
-    const float rho = 1.f / sqrtf(row_sum<L>(ss) / (float)a.D + a.eps);
+    float mean = row_sum<L>(ss) / (float)a.D + a.eps;
+    const float scale = row_scale<L>(u, mean, a.eps);
+    if (scale != 1.f) {
+        ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            u[e] *= scale;
+            ss = fmaf(u[e], u[e], ss);
+        }
+        mean = row_sum<L>(ss) / (float)a.D + a.eps * scale * scale;
+    }
+    const float rho = 1.f / sqrtf(mean);
     if (!in) return;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -147,13 +175,27 @@ __global__ __launch_bounds__(GN_THREADS) void gated_norm_bwd_kernel(GatedNormArg
         }
         ss = row_sum<L>(ss);
         pu = row_sum<L>(pu);
-        const float rho = 1.f / sqrtf(ss * inv_d + a.eps);
+        float mean = ss * inv_d + a.eps;
+        const float scale = row_scale<L>(u, mean, a.eps);
+        if (scale != 1.f) {
+            ss = pu = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                u[e] *= scale;
+                ss = fmaf(u[e], u[e], ss);
+                pu = fmaf(dy[e] * w[e] * act[e], u[e], pu);
+            }
+            ss = row_sum<L>(ss);
+            pu = row_sum<L>(pu);
+            mean = ss * inv_d + a.eps * scale * scale;
+        }
+        const float rho = 1.f / sqrtf(mean);
         const float back = rho * rho * pu * inv_d;  // rho mean(p n), n = u rho
         float dx[8], dz[8], ds = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float n = u[e] * rho, t = dy[e] * n;
-            dx[e] = rho * (dy[e] * w[e] * act[e] - u[e] * back);
+            dx[e] = rho * (dy[e] * w[e] * act[e] - u[e] * back) * scale;
             dz[e] = t * w[e] * slope[e];
             dw[e] = fmaf(t, act[e], dw[e]);
             ds = fmaf(dx[e], res[e], ds);

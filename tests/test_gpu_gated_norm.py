@@ -249,3 +249,14 @@ def test_open_gates_keep_their_slope():
     bad = np.abs(g - want) - (2.0 ** -8 + FINE) * np.abs(want) - 2.0 ** -134
     assert bad.max() <= 0, bad.max()
     assert (np.abs(g) > 0).mean() > 0.9
+
+
+@pytest.mark.parametrize("res", [False, True])
+@pytest.mark.parametrize("spread,eps", [(1e25, 1e-6), (1e37, 0.0), (1e-25, 0.0), (1e-18, 1e-36), (1e-30, 1e-36)])
+def test_rows_whose_squares_leave_the_range(spread, eps, res):
+    """The norm is of the size of one whatever the row's: squares of 1e20 or 1e-23 have
+    no place in fp32."""
+    w = make((40, 2, 72), seed=53, spread=spread, res=res)
+    if res:  # of the row's own size
+        w["residual"] = (w["residual"].double() * spread).to(torch.bfloat16)
+    check(w, "silu", eps)
