@@ -681,6 +681,14 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _need_workspace(t, need, dev):
+    """A caller's workspace: one piece of at least ``need`` bytes."""
+    if _nbytes(t) < need or t.device != dev:
+        raise LibKdaError(3, status_str(3))
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 def la_workspace_size(B, T, H, K, V, num_seqs=None, segment_chunks=0, backward=False) -> int:
     """Workspace bytes of la_fwd (or la_bwd).  0: unsupported sizes."""
     fn = load().la_bwd_workspace_size if backward else load().la_fwd_workspace_size
@@ -718,8 +726,8 @@ def _la_prepare(q, k, v, log_decay, scale, initial_state, cu_seqlens, workspace,
     if workspace is None:
         if need > 256:  # (one alignment unit: no segments, no workspace)
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif _nbytes(workspace) < need or workspace.device != dev:
-        raise LibKdaError(3, status_str(3))
+    else:
+        _need_workspace(workspace, need, dev)
     return (dev, B, T, H, K, V, N, float(K ** -0.5 if scale is None else scale), workspace,
             0 if workspace is None else _nbytes(workspace),
             _stream(dev))
@@ -874,8 +882,8 @@ def gated_norm_bwd(x, gate, weight, dy, activation="sigmoid", eps=1e-6, residual
         raise LibKdaError(2, status_str(2))
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif _nbytes(workspace) < need or workspace.device != dev:
-        raise LibKdaError(3, status_str(3))
+    else:
+        _need_workspace(workspace, need, dev)
     r = {"dx": torch.empty_like(x), "dgate": None if gate is None else torch.empty_like(gate),
          "dweight": torch.empty_like(weight),
          "dresidual": None if residual is None else torch.empty_like(residual),

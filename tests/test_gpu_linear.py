@@ -434,3 +434,15 @@ def test_no_second_derivative():
     (g,) = torch.autograd.grad(y.float().square().sum(), leaf["q"], create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable|does not require grad"):
         g.float().sum().backward()
+
+
+def test_workspaces_that_are_not_one_piece_are_refused():
+    d = dev(make(1, 300, 2, 64, 64, seed=780))
+    size = kda.la_workspace_size(1, 300, 2, 64, 64, segment_chunks=1, backward=True)
+    for ws in (torch.empty(1, dtype=torch.uint8, device=DEV).expand(size),
+               torch.empty(2 * size, dtype=torch.uint8, device=DEV)[::2]):
+        for call in (fwd, bwd):
+            with pytest.raises(ValueError, match="contiguous"):
+                call(d, workspace=ws, segment_chunks=1)
+        with pytest.raises(ValueError, match="contiguous"):
+            kda.gated_norm_bwd(d["q"], None, torch.ones(64, device=DEV), d["do"], workspace=ws)

@@ -170,3 +170,20 @@ def test_la_workspace_size_is_0_where_the_call_refuses(lib, packed, N, T, H, seg
             assert call(lib, **over, ws=FAKE, wsb=1 << 62) == 1
         elif size > 256:
             assert call(lib, **over) == 3
+
+
+def test_workspaces_that_are_not_one_piece_are_refused():
+    """The kernels write a workspace from its address on: an expanded or strided view
+    has as many elements, but not the memory."""
+    from chunked_gated_delta_kda_amd import _binding as b
+
+    cpu = torch.device("cpu")
+    piece = torch.empty(4096, dtype=torch.uint8)
+    b._need_workspace(piece, 4096, cpu)
+    b._need_workspace(piece.view(64, 64)[:], 4096, cpu)
+    with pytest.raises(kda.LibKdaError, match="WORKSPACE"):
+        b._need_workspace(piece, 4097, cpu)
+    with pytest.raises(ValueError, match="contiguous"):
+        b._need_workspace(piece[:1].expand(4096), 4096, cpu)
+    with pytest.raises(ValueError, match="contiguous"):
+        b._need_workspace(torch.empty(8192, dtype=torch.uint8)[::2], 4096, cpu)
