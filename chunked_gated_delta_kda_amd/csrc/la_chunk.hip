@@ -209,8 +209,7 @@ __device__ __forceinline__ void chunk_pass(const LaArgs& a, const LaPass& p, int
             }
         };
 
-        constexpr int SETS = 2;  // chunks ahead in registers
-        u32x4 xr[SETS][RV], yr[SETS][RV], zr[SETS][ZV];
+        u32x4 xr[2][RV], yr[2][RV], zr[2][ZV];  // two chunks ahead
         {
             u32x4 x0[RV], y0[RV], z0[ZV], x1[RV], y1[RV];
             if constexpr (!STATES) load_rows(x_ptr, 0, x0);
@@ -219,7 +218,7 @@ __device__ __forceinline__ void chunk_pass(const LaArgs& a, const LaPass& p, int
             if constexpr (!STATES) load_rows(x_ptr, 1, x1);
             load_rows(y_ptr, 1, y1);
 #pragma unroll
-            for (int k = 0; k < SETS; ++k) {
+            for (int k = 0; k < 2; ++k) {
                 load_z(1 + k, zr[k]);
                 if constexpr (!STATES) load_rows(x_ptr, 2 + k, xr[k]);
                 load_rows(y_ptr, 2 + k, yr[k]);
@@ -248,15 +247,15 @@ __device__ __forceinline__ void chunk_pass(const LaArgs& a, const LaPass& p, int
             }
             put_rows(ytile[(c + 2) % 3], y);
             put_z(c + 1, z);
-            if constexpr (!STATES) load_rows(x_ptr, c + 2 + SETS, x);
-            load_rows(y_ptr, c + 2 + SETS, y);
-            load_z(c + 1 + SETS, z);
+            if constexpr (!STATES) load_rows(x_ptr, c + 4, x);
+            load_rows(y_ptr, c + 4, y);
+            load_z(c + 3, z);
             __syncthreads();
         };
         int c = 0;
-        for (; c + SETS < nc; c += SETS) {
+        for (; c + 2 < nc; c += 2) {
             interval(c, xr[0], yr[0], zr[0]);
-            if constexpr (SETS == 2) interval(c + 1, xr[1], yr[1], zr[1]);
+            interval(c + 1, xr[1], yr[1], zr[1]);
         }
         if (c + 1 < nc) interval(c, xr[0], yr[0], zr[0]);
         if (!STATES && nc > 1) store_rows(nc - 2, std::true_type{});

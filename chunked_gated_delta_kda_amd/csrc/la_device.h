@@ -89,13 +89,8 @@ __device__ __forceinline__ bool find_seg(const LaSeqs& s, int slot, Seg& g) {
     return true;
 }
 
-// Row r of tile t of the state (and of an operand that contracts over the
-// chunk's tokens): channel 32 (t / 2) + 8 (r / 4) + 4 (t % 2) + r % 4, so the
-// accumulators of tiles 2j and 2j+1 are the eight channels 32 j + 8 g + e of
-// the operand of a product that contracts over them.
-
 // Operand that contracts over tokens: lane (r, g) receives rows 4 g .. 4 g + 3,
-// column channel(t, r) of 16 rows of an LDS tile, by one transposing read
+// column tile_channel(t, r) of 16 rows of an LDS tile, by one transposing read
 // (ds_read_b64_tr_b16): in each group of 16 lanes, lane r fetches four
 // consecutive columns of row 4 g + r / 4, those that lanes 4 (r % 4) .. + 3
 // receive.
@@ -180,8 +175,8 @@ __device__ __forceinline__ uint32_t take_term(float& v0, float& v1) {
     v1 -= __uint_as_float(__float_as_uint(v1) & 0xffff0000u);
     return term;
 }
-// (the rounded product, not contracted into the differences: the two kernels give the
-// same bits)
+// (the rounded product, not contracted into the differences: where la_chunk.hip takes
+// three terms too, the two kernels give the same bits)
 __device__ __forceinline__ float decayed(float z, float w) {
 #pragma clang fp contract(off)
     return z * w;

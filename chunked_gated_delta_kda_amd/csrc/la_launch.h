@@ -71,7 +71,6 @@ struct LaScanArgs {
     const float* init[2];  // [n_seqs, H, elems] or null: the state entering a sequence
     float* state[2];       // [n_slots, H, elems]: in, what each segment adds to a zero
                            // state (not read for the last); out, the state entering it
-    int32_t reverse[2];
     int32_t elems;         // K * V
     int32_t n_dirs;
 };

@@ -1,6 +1,9 @@
 // la_narrow.hip -- chunked linear attention for few (sequence, head) pairs (gfx950):
-// the passes of la_chunk.hip (its mathematics and precision, and the same bits) over
-// whole sequences, in workgroups of 32 state columns.
+// the passes of la_chunk.hip (its mathematics and precision) over whole sequences, in
+// workgroups of 32 state columns.  A decayed z always has three terms here; la_chunk.hip
+// takes two in launches that return no state.  With a state returned the two give the
+// same bits, without one outputs differ by the third term, below 2^-15 of a summand
+// before they are rounded to bf16.
 //
 // One workgroup per (sequence, head, 32 columns); the column blocks of one head are
 // neighbours on one XCD, whose L2 serves the rows of x and y to all of them.  Eight

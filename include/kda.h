@@ -430,6 +430,11 @@ int gdn_bwd_saved(const uint16_t* q, const uint16_t* k, const uint16_t* v, const
  *    segments: a first pass forms what each adds to a zero state, a scan
  *    gives each its entering state, and a second pass computes them all at
  *    once.  The result is the unsplit one up to fp32 rounding.
+ *  - Equal calls give equal bits.  Between calls that cut a sequence otherwise,
+ *    or of which one returns states (final_state, dh0) and one does not, the
+ *    bf16 outputs may differ by rounding: the state that an output is read from
+ *    is then summed in another order, or from 16 instead of 24 bits of each
+ *    decayed value.  States that are returned are always sums of all 24.
  *
  * la_fwd_workspace_size / la_bwd_workspace_size: bytes of device workspace
  * (num_seqs: packed sequences when cu_seqlens will be passed, else B), 0 for
