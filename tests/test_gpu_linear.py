@@ -446,3 +446,42 @@ def test_workspaces_that_are_not_one_piece_are_refused():
                 call(d, workspace=ws, segment_chunks=1)
         with pytest.raises(ValueError, match="contiguous"):
             kda.gated_norm_bwd(d["q"], None, torch.ones(64, device=DEV), d["do"], workspace=ws)
+
+
+def test_automatic_segments_of_a_packed_batch():
+    lens, H = [9000, 1, 0, 13000, 64], 2
+    T = sum(lens) + 11
+    for backward in (False, True):
+        assert kda.la_workspace_size(1, T, H, 128, 64, len(lens), backward=backward) > 256
+    d = dev(make(0, 0, H, 128, 64, seed=790, lens=lens, lead=4, tail=7))
+    o, S = fwd(d)
+    o1, S1 = fwd(d, segment_chunks=-1)
+    r, r1 = bwd(d), bwd(d, segment_chunks=-1)
+    assert (S - S1).norm() <= 2.0 ** -18 * S1.norm()
+    assert (r["dh0"] - r1["dh0"]).norm() <= 2.0 ** -18 * r1["dh0"].norm()
+    for a, b in ((o, o1), (r["dq"], r1["dq"]), (r["dk"], r1["dk"]), (r["dv"], r1["dv"])):
+        assert (a.float() - b.float()).norm() <= 2.0 ** -8 * b.float().norm()
+        assert not a[:, :4].any() and not a[:, -7:].any()
+
+
+@pytest.mark.parametrize("H", [3, MANY])
+def test_outputs_carry_two_roundings(H):
+    """On inputs of random sign a rounding to bf16 is off by u = 2^-8 / sqrt(3) *
+    sqrt(3 / (8 ln 2)) = 1.66e-3 of the value as a root mean square (uniform in half a
+    step of 2^-8, over a mantissa spread evenly over its logarithm).  Terms with one
+    such rounding each, added up with random signs and rounded again, are off by
+    sqrt(2) u = 2.35e-3 as a whole; a tenth more is for the sample."""
+    w = make(1, 333, H, 64, 128, seed=800)
+    d = dev(w)
+    o, _ = fwd(d)
+    r = bwd(d)
+    one = {n: (t[:, :, :3] if n in ("q", "k", "v", "do") else t) for n, t in w.items()}
+    one.update(ld=w["ld"][:3], h0=w["h0"][:, :3], dfin=w["dfin"][:, :3])
+    want = dict(ref.la_bwd(one["q"], one["k"], one["v"], one["ld"], w["scale"], one["do"], one["h0"], one["dfin"]),
+                o=ref.la_fwd(one["q"], one["k"], one["v"], one["ld"], w["scale"], one["h0"])[0])
+    for n, got in dict(r, o=o).items():
+        if n == "dh0":
+            continue
+        rel = np.linalg.norm(f64(got[:, :, :3]) - want[n]) / np.linalg.norm(want[n])
+        say(f"  {n}: rel {rel:.2e}")
+        assert rel <= 1.1 * 2 ** 0.5 * 1.66e-3, n
