@@ -15,10 +15,10 @@
 // leaves one row of sums, and a second kernel adds them in a fixed order, in
 // 64 bits, so gradients are the same from call to call.
 //
-// 4096 tokens, 32 heads of 128, a gate: forward 22 us (101 MB, 4.6 TB/s), backward
-// 35 us (168 MB, 4.8 TB/s) and 4.6 us for the sums.  2048 workgroups instead of 1024
-// in the backward kernel make it 44 us, a row's loads ahead of the row before change
-// nothing.
+// 4096 tokens, 32 heads of 128, a gate: forward 23 us (101 MB, 4.4 TB/s), backward
+// 37 us (168 MB, 4.6 TB/s; 36 without row_scale) and 4.7 us for the sums.  2048
+// workgroups instead of 1024 make the backward kernel 9 us slower, a row's loads ahead of
+// the row before change nothing.
 #include "kda_common.h"
 #include "la_launch.h"
 

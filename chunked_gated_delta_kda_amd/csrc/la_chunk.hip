@@ -26,7 +26,8 @@
 // One barrier a chunk.
 //
 // What bounds it: with every CU busy, HBM: 16 sequences of 256 to 8192 tokens, 32 heads
-// of 128 x 128, take 590 us for 2.55 GB, 4.3 TB/s, where a copy reaches 4.9.  With 64
+// of 128 x 128, take 591 to 612 us for 2.55 GB, 4.2 to 4.3 TB/s, where a copy of 2 GiB
+// reaches 4.9.  With 64
 // workgroups the issue of instructions: a chunk costs a SIMD 152 products of 16 cycles
 // and about 700 other vector instructions, which overlap for a fifth only, 2.6 us in
 // all.  Measured on the way there (the packed batch):

@@ -19,9 +19,9 @@
 //
 // What bounds it: the way it reads.  A column block reads z in 64-byte pieces and x
 // and y once per block through L2: 2 x 2048 tokens, 32 heads of 128 x 128 (134 MB)
-// take 50 us with or without the products, 2.7 TB/s; the products alone 35 us.  With
-// few workgroups it is the chain within a chunk, 1.0 to 1.3 us: 256 tokens,
-// 4 heads of 64 x 64, take 6.4 us where la_chunk.hip takes 8.5.
+// take 44 to 48 us, 2.8 to 3.0 TB/s, with or without the products; the products alone
+// 35 us.  With few workgroups it is the chain within a chunk, 1.0 to 1.3 us: 256 tokens,
+// 4 heads of 64 x 64, take 6.0 us where la_chunk.hip takes 8.5.
 #include "la_device.h"
 
 namespace kda {

@@ -420,7 +420,9 @@ int gdn_bwd_saved(const uint16_t* q, const uint16_t* k, const uint16_t* v, const
  *    cu_seqlens[num_seqs] on) get zeros.
  *  - Inputs are finite.  A NaN or an infinity in a row of k or v makes the
  *    outputs of its 64-token chunk, and all later ones of its sequence, what
- *    they happen to be; it never leaves its sequence and head.
+ *    they happen to be; in a row of q it makes its own output so.  For la_bwd
+ *    any row may make all gradients of its sequence so.  It never leaves its
+ *    sequence and head.
  *  - Alignment: q, k, v, o, states and all gradients 16 bytes; log_decay 4.
  *    H is at most 65536, and there are fewer than 2^25 pairs of a head and a
  *    sequence (or segment).
@@ -486,7 +488,11 @@ int la_decode(const uint16_t* q, const uint16_t* k, const uint16_t* v, const flo
  * D is a multiple of 8 from 8 to 512, else KDA_ERR_UNSUPPORTED; eps >= 0;
  * tokens * H < 2^31.  tokens = 0 is allowed (row tensors may then be NULL).
  * y may be x or gate (each row is read before it is written).  Arithmetic is
- * fp32, each output is rounded once; a NaN or infinity in a row stays in it.  Alignment: row tensors 16 bytes.
+ * fp32, each output is rounded once; a NaN or infinity in a row stays in it
+ * (and in the sums over rows).  Rows of any size keep their precision: where
+ * their squares would leave fp32's range they are scaled by a power of two
+ * first.  A row of zeros with eps = 0 gives NaN.  Alignment: row tensors 16
+ * bytes.
  *
  * gated_norm_bwd: dL/dy = dy -> dx, dgate, dresidual [tokens, H, D] bf16 and
  * dweight [D], dresidual_scale [H] fp32 (sums over all rows in a fixed order:
