@@ -25,7 +25,11 @@ EXPORTS = ("kda_fwd", "gdn_fwd", "kda_fwd_workspace_size", "gdn_fwd_workspace_si
            "kda_bwd", "gdn_bwd", "kda_fwd_save", "gdn_fwd_save", "kda_bwd_saved",
            "gdn_bwd_saved", "la_fwd_workspace_size", "la_fwd", "la_bwd_workspace_size", "la_bwd",
            "la_decode", "gated_norm_fwd", "gated_norm_bwd_workspace_size", "gated_norm_bwd",
-           "kda_status_str", "kda_version")
+           "gated_scan_states", "gated_scan_fwd_workspace_size", "gated_scan_fwd",
+           "gated_scan_bwd_workspace_size", "gated_scan_bwd", "gated_scan_decode",
+           "short_conv_fwd", "short_conv_bwd_workspace_size", "short_conv_bwd",
+           "short_conv_decode", "layer_norm_fwd", "layer_norm_bwd_workspace_size",
+           "layer_norm_bwd", "kda_status_str", "kda_version")
 
 
 class LibKdaError(RuntimeError):
@@ -134,6 +138,36 @@ def load(path: Path | str | None = None):
     lib.gated_norm_bwd.restype = ctypes.c_int
     lib.gated_norm_bwd.argtypes = [u16p, u16p, f32p, u16p, f32p, i32, f32, i64, i32, i32, u16p,
                                    u16p, u16p, f32p, u16p, f32p, vp, sz, vp]
+    for name in ("gated_scan_fwd_workspace_size", "gated_scan_bwd_workspace_size"):
+        getattr(lib, name).restype = ctypes.c_size_t
+        getattr(lib, name).argtypes = [i32] * 3
+    lib.gated_scan_states.restype = i64
+    lib.gated_scan_states.argtypes = [i32] * 3
+    lib.gated_scan_fwd.restype = ctypes.c_int
+    lib.gated_scan_fwd.argtypes = [vp, vp, vp, f32p, f32p, f32p, f32p, i32p, i32, i32, i32, i32,
+                                   i32, vp, f32p, vp, sz, vp]
+    lib.gated_scan_bwd.restype = ctypes.c_int
+    lib.gated_scan_bwd.argtypes = [vp, vp, vp, f32p, f32p, f32p, i32p, i32, i32, i32, i32, i32,
+                                   vp, f32p, f32p, vp, vp, vp, f32p, f32p, f32p, vp, sz, vp]
+    lib.gated_scan_decode.restype = ctypes.c_int
+    lib.gated_scan_decode.argtypes = [vp, vp, vp, f32p, f32p, f32p, f32p, i32, i32, i32, vp, vp]
+    lib.short_conv_fwd.restype = ctypes.c_int
+    lib.short_conv_fwd.argtypes = [vp, f32p, f32p, i32, vp, vp, i32p, i32, i32, i32, i32, i32,
+                                   i32, vp, vp]
+    lib.short_conv_bwd_workspace_size.restype = ctypes.c_size_t
+    lib.short_conv_bwd_workspace_size.argtypes = [i32] * 4
+    lib.short_conv_bwd.restype = ctypes.c_int
+    lib.short_conv_bwd.argtypes = [vp, f32p, f32p, i32, vp, i32p, i32, i32, i32, i32, i32, i32,
+                                   vp, vp, vp, f32p, f32p, vp, vp, sz, vp]
+    lib.short_conv_decode.restype = ctypes.c_int
+    lib.short_conv_decode.argtypes = [vp, f32p, f32p, i32, vp, vp, i32, i32, i32, i32, vp, vp]
+    lib.layer_norm_fwd.restype = ctypes.c_int
+    lib.layer_norm_fwd.argtypes = [vp, vp, f32p, f32p, f32, i32, i64, i32, vp, vp, vp]
+    lib.layer_norm_bwd_workspace_size.restype = ctypes.c_size_t
+    lib.layer_norm_bwd_workspace_size.argtypes = [i32, i64, i32]
+    lib.layer_norm_bwd.restype = ctypes.c_int
+    lib.layer_norm_bwd.argtypes = [vp, f32p, f32, i32, i64, i32, vp, vp, vp, f32p, f32p, vp, sz,
+                                   vp]
     lib.kda_status_str.restype = ctypes.c_char_p
     lib.kda_status_str.argtypes = [ctypes.c_int]
     lib.kda_version.restype = ctypes.c_int
@@ -893,4 +927,311 @@ def gated_norm_bwd(x, gate, weight, dy, activation="sigmoid", eps=1e-6, residual
                                      _addr(r["dweight"]), _addr(r["dresidual"]),
                                      _addr(r["dresidual_scale"]), _addr(workspace),
                                      _nbytes(workspace), stream))
+    return r
+
+
+# ------------------------- around a block: recurrence, convolution, layer norm
+def _token_type(t, name):
+    """The dtype code of a call's token tensors."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype == torch.bfloat16:
+        return 0
+    if t.dtype == torch.float32:
+        return 1
+    raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+
+
+def _batch(x, cu_seqlens):
+    """Checks of a batch of tokens x [B, T, C]; (dtype code, device, B, T, C, sequences)."""
+    torch = _torch()
+    code = _token_type(x, "x")
+    _need(x, "x", x.dtype)
+    if x.dim() != 3:
+        raise ValueError("x must be [B, T, C]")
+    dev = x.device
+    B, T, C = x.shape
+    N = B
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be 1-D with num_seqs + 1 entries")
+        if B != 1:
+            raise ValueError("cu_seqlens needs B == 1 (sequences packed along T)")
+        N = cu_seqlens.numel() - 1
+    return code, dev, B, T, C, N
+
+
+def _space(workspace, need, dev):
+    """The caller's workspace, checked, or a new one; 0 bytes: unsupported sizes."""
+    if need == 0:
+        raise LibKdaError(2, status_str(2))
+    if workspace is None:
+        return _torch().empty(need, dtype=_torch().uint8, device=dev)
+    _need_workspace(workspace, need, dev)
+    return workspace
+
+
+def _given(t, name, dtype, shape, dev):
+    """The caller's output, checked, or a new one."""
+    if t is None:
+        return _torch().empty(shape, dtype=dtype, device=dev)
+    _need(t, name, dtype, shape, dev)
+    return t
+
+
+def gated_scan_workspace_size(B, T, C, backward=False) -> int:
+    """Workspace bytes of gated_scan_fwd (or gated_scan_bwd).  0: unsupported sizes."""
+    fn = load().gated_scan_bwd_workspace_size if backward else load().gated_scan_fwd_workspace_size
+    return int(fn(B, T, C))
+
+
+def _scan_prepare(x, g, input_gate, A_log, dt_bias, initial_state, cu_seqlens, workspace,
+                  backward):
+    torch = _torch()
+    code, dev, B, T, C, N = _batch(x, cu_seqlens)
+    _need(g, "g", x.dtype, x.shape, dev)
+    _need(input_gate, "input_gate", x.dtype, x.shape, dev)
+    _need(A_log, "A_log", torch.float32, (C,), dev)
+    _need(dt_bias, "dt_bias", torch.float32, (C,), dev)
+    if initial_state is not None:
+        _need(initial_state, "initial_state", torch.float32, (N, C), dev)
+    ws = _space(workspace, gated_scan_workspace_size(B, T, C, backward), dev)
+    return code, dev, B, T, C, N, ws
+
+
+def _scan_fwd(x, g, input_gate, A_log, dt_bias, initial_state, output_final_state, cu_seqlens,
+              workspace, out, final_out, keep):
+    torch = _torch()
+    code, dev, B, T, C, N, ws = _scan_prepare(x, g, input_gate, A_log, dt_bias, initial_state,
+                                              cu_seqlens, workspace, False)
+    out = _given(out, "out", x.dtype, (B, T, C), dev)
+    final = None
+    if output_final_state:
+        final = _given(final_out, "final_out", torch.float32, (N, C), dev)
+    states = None
+    if keep:
+        states = torch.empty(int(load().gated_scan_states(B, T, C)), dtype=torch.float32,
+                             device=dev)
+    with _on(dev):
+        _check(load().gated_scan_fwd(_addr(x), _addr(g), _addr(input_gate), _addr(A_log),
+                                     _addr(dt_bias), _addr(initial_state), _addr(final),
+                                     _addr(cu_seqlens), N, code, B, T, C, _addr(out),
+                                     _addr(states), _addr(ws), _nbytes(ws), _stream(dev)))
+    return out, final, states
+
+
+def gated_scan_fwd(x, g, input_gate, A_log, dt_bias, initial_state=None, output_final_state=True,
+                   cu_seqlens=None, workspace=None, out=None, final_out=None):
+    """The gated linear recurrence over channels: a_t = exp(-exp(A_log) softplus(g_t +
+    dt_bias)), h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(input_gate_t) x_t, o_t = h_t.
+    x, g, input_gate [B,T,C], all bf16 or all fp32 (C a multiple of 8); A_log, dt_bias [C]
+    fp32; initial_state [N,C] fp32 or None; cu_seqlens int32 [N+1] or None (B must then be
+    1; rows outside every sequence get zeros).  ``workspace`` (gated_scan_workspace_size
+    bytes), ``out`` and ``final_out`` optionally supply device buffers.  Returns (o [B,T,C]
+    as x, final_state [N,C] fp32 or None)."""
+    return _scan_fwd(x, g, input_gate, A_log, dt_bias, initial_state, output_final_state,
+                     cu_seqlens, workspace, out, final_out, False)[:2]
+
+
+def gated_scan_fwd_save(x, g, input_gate, A_log, dt_bias, initial_state=None,
+                        output_final_state=True, cu_seqlens=None, workspace=None, out=None,
+                        final_out=None):
+    """gated_scan_fwd for training: returns (o, final_state, states), the last for
+    gated_scan_bwd on the same inputs."""
+    return _scan_fwd(x, g, input_gate, A_log, dt_bias, initial_state, output_final_state,
+                     cu_seqlens, workspace, out, final_out, True)
+
+
+def gated_scan_bwd(x, g, input_gate, A_log, dt_bias, do, states, initial_state=None, dfinal=None,
+                   cu_seqlens=None, workspace=None, need_dh0=True):
+    """Gradients of gated_scan_fwd_save for dL/do = ``do`` (as x) and dL/d(final state) =
+    ``dfinal`` [N,C] fp32 (None: zero): a dict with dx, dg, dinput_gate (as x), dA_log,
+    ddt_bias [C] and dh0 [N,C] (fp32; None unless ``need_dh0``).  ``states`` is what the
+    forward call on the same inputs returned."""
+    torch = _torch()
+    code, dev, B, T, C, N, ws = _scan_prepare(x, g, input_gate, A_log, dt_bias, initial_state,
+                                              cu_seqlens, workspace, True)
+    _need(do, "do", x.dtype, x.shape, dev)
+    _need(states, "states", torch.float32, (int(load().gated_scan_states(B, T, C)),), dev)
+    if dfinal is not None:
+        _need(dfinal, "dfinal", torch.float32, (N, C), dev)
+    r = {"dx": torch.empty_like(x), "dg": torch.empty_like(x), "dinput_gate": torch.empty_like(x),
+         "dA_log": torch.empty_like(A_log), "ddt_bias": torch.empty_like(dt_bias),
+         "dh0": torch.empty((N, C), dtype=torch.float32, device=dev) if need_dh0 else None}
+    with _on(dev):
+        _check(load().gated_scan_bwd(_addr(x), _addr(g), _addr(input_gate), _addr(A_log),
+                                     _addr(dt_bias), _addr(initial_state), _addr(cu_seqlens), N,
+                                     code, B, T, C, _addr(do), _addr(dfinal), _addr(states),
+                                     _addr(r["dx"]), _addr(r["dg"]), _addr(r["dinput_gate"]),
+                                     _addr(r["dA_log"]), _addr(r["ddt_bias"]), _addr(r["dh0"]),
+                                     _addr(ws), _nbytes(ws), _stream(dev)))
+    return r
+
+
+def gated_scan_decode(x, g, input_gate, A_log, dt_bias, state=None, state_out=None, out=None):
+    """One token of the recurrence for N sequences: x, g, input_gate [N,C], all bf16 or all
+    fp32; state [N,C] fp32 or None (zeros).  ``state_out`` may be ``state`` (update in
+    place).  Returns (o [N,C] as x, new state [N,C] fp32)."""
+    torch = _torch()
+    code = _token_type(x, "x")
+    _need(x, "x", x.dtype)
+    if x.dim() != 2:
+        raise ValueError("x must be [N, C]")
+    dev = x.device
+    N, C = x.shape
+    _need(g, "g", x.dtype, (N, C), dev)
+    _need(input_gate, "input_gate", x.dtype, (N, C), dev)
+    _need(A_log, "A_log", torch.float32, (C,), dev)
+    _need(dt_bias, "dt_bias", torch.float32, (C,), dev)
+    if state is not None:
+        _need(state, "state", torch.float32, (N, C), dev)
+    state_out = _given(state_out, "state_out", torch.float32, (N, C), dev)
+    out = _given(out, "out", x.dtype, (N, C), dev)
+    with _on(dev):
+        _check(load().gated_scan_decode(_addr(x), _addr(g), _addr(input_gate), _addr(A_log),
+                                        _addr(dt_bias), _addr(state), _addr(state_out), code, N, C,
+                                        _addr(out), _stream(dev)))
+    return out, state_out
+
+
+_CONV_ACTIVATIONS = {None: 0, "none": 0, "silu": 1}
+
+
+def _conv_parameters(x, C, weight, bias, activation, dev):
+    """Checks of a convolution's parameters; (taps, activation code)."""
+    torch = _torch()
+    _need(weight, "weight", torch.float32, None, dev)
+    if weight.dim() != 2 or weight.shape[0] != C:
+        raise ValueError(f"weight must be [C, W] with C = {C}, got {tuple(weight.shape)}")
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (C,), dev)
+    if activation not in _CONV_ACTIVATIONS:
+        raise ValueError(f"activation must be 'none' or 'silu', got {activation!r}")
+    W = weight.shape[1]
+    if W not in (2, 3, 4):
+        raise LibKdaError(2, status_str(2))
+    return W, _CONV_ACTIVATIONS[activation]
+
+
+def short_conv_fwd(x, weight, bias=None, activation="silu", initial_state=None,
+                   output_final_state=True, cu_seqlens=None, out=None, final_out=None):
+    """The short causal convolution in front of a block: y_t = act(bias + sum_j weight[:, j]
+    x_{t-W+1+j}).  x [B,T,C] bf16 or fp32 (C a multiple of 8); weight [C,W] (W 2, 3 or 4),
+    bias [C] or None, fp32; activation "silu" or "none"; initial_state [N,W-1,C] as x (the
+    W - 1 tokens in front of each sequence, the oldest first) or None (zeros); cu_seqlens
+    int32 [N+1] or None (B must then be 1; rows outside every sequence get zeros).  Returns
+    (y [B,T,C] as x, final_state [N,W-1,C] as x or None)."""
+    code, dev, B, T, C, N = _batch(x, cu_seqlens)
+    W, act = _conv_parameters(x, C, weight, bias, activation, dev)
+    if initial_state is not None:
+        _need(initial_state, "initial_state", x.dtype, (N, W - 1, C), dev)
+    out = _given(out, "out", x.dtype, (B, T, C), dev)
+    final = None
+    if output_final_state:
+        final = _given(final_out, "final_out", x.dtype, (N, W - 1, C), dev)
+    with _on(dev):
+        _check(load().short_conv_fwd(_addr(x), _addr(weight), _addr(bias), act,
+                                     _addr(initial_state), _addr(final), _addr(cu_seqlens), N,
+                                     code, B, T, C, W, _addr(out), _stream(dev)))
+    return out, final
+
+
+def short_conv_bwd(x, weight, dy, bias=None, activation="silu", initial_state=None, dfinal=None,
+                   cu_seqlens=None, workspace=None, need_dh0=True):
+    """Gradients of short_conv_fwd for dL/dy = ``dy`` (as x) and dL/d(final state) =
+    ``dfinal`` [N,W-1,C] as x (None: zero): a dict with dx (as x), dweight [C,W], dbias [C]
+    (fp32; None without a bias) and dh0 [N,W-1,C] (as x; None unless ``need_dh0``)."""
+    torch = _torch()
+    code, dev, B, T, C, N = _batch(x, cu_seqlens)
+    W, act = _conv_parameters(x, C, weight, bias, activation, dev)
+    _need(dy, "dy", x.dtype, x.shape, dev)
+    for t, name in ((initial_state, "initial_state"), (dfinal, "dfinal")):
+        if t is not None:
+            _need(t, name, x.dtype, (N, W - 1, C), dev)
+    ws = _space(workspace, int(load().short_conv_bwd_workspace_size(B, T, C, W)), dev)
+    r = {"dx": torch.empty_like(x), "dweight": torch.empty_like(weight),
+         "dbias": None if bias is None else torch.empty_like(bias),
+         "dh0": torch.empty((N, W - 1, C), dtype=x.dtype, device=dev) if need_dh0 else None}
+    with _on(dev):
+        _check(load().short_conv_bwd(_addr(x), _addr(weight), _addr(bias), act,
+                                     _addr(initial_state), _addr(cu_seqlens), N, code, B, T, C, W,
+                                     _addr(dy), _addr(dfinal), _addr(r["dx"]), _addr(r["dweight"]),
+                                     _addr(r["dbias"]), _addr(r["dh0"]), _addr(ws), _nbytes(ws),
+                                     _stream(dev)))
+    return r
+
+
+def short_conv_decode(x, weight, state, bias=None, activation="silu", state_out=None, out=None):
+    """One token of the convolution for N sequences: x [N,C] bf16 or fp32, state [N,W-1,C]
+    as x, the oldest token first.  ``state_out`` may be ``state`` (update in place).
+    Returns (y [N,C], new state [N,W-1,C]), as x."""
+    code = _token_type(x, "x")
+    _need(x, "x", x.dtype)
+    if x.dim() != 2:
+        raise ValueError("x must be [N, C]")
+    dev = x.device
+    N, C = x.shape
+    W, act = _conv_parameters(x, C, weight, bias, activation, dev)
+    _need(state, "state", x.dtype, (N, W - 1, C), dev)
+    state_out = _given(state_out, "state_out", x.dtype, (N, W - 1, C), dev)
+    out = _given(out, "out", x.dtype, (N, C), dev)
+    with _on(dev):
+        _check(load().short_conv_decode(_addr(x), _addr(weight), _addr(bias), act, _addr(state),
+                                        _addr(state_out), code, N, C, W, _addr(out),
+                                        _stream(dev)))
+    return out, state_out
+
+
+def _rows(x, name, weight):
+    """Checks of rows x [..., D] and their weight; (dtype code, device, rows, D)."""
+    code = _token_type(x, name)
+    _need(x, name, x.dtype)
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError(f"{name} must be [..., D]")
+    D = x.shape[-1]
+    _need(weight, "weight", _torch().float32, (D,), x.device)
+    return code, x.device, x.numel() // D, D
+
+
+def layer_norm_fwd(x, weight, bias=None, eps=1e-5, residual=None, out=None, sum_out=None):
+    """Layer norm in front of a block, on rows x [..., D], bf16 or fp32 (D a multiple of 8 up
+    to 16384): u = x + residual (if given; rounded to x's type), y = (u - mean(u)) /
+    sqrt(var(u) + eps) weight + bias.  residual as x; weight [D], bias [D] or None, fp32.
+    ``out`` and ``sum_out`` may be ``x`` or ``residual``, one each.  Returns (y, u), both as
+    x; u is ``x`` itself without a residual."""
+    code, dev, rows, D = _rows(x, "x", weight)
+    if bias is not None:
+        _need(bias, "bias", _torch().float32, (D,), dev)
+    total = x
+    if residual is not None:
+        _need(residual, "residual", x.dtype, x.shape, dev)
+        total = _given(sum_out, "sum_out", x.dtype, x.shape, dev)
+    out = _given(out, "out", x.dtype, x.shape, dev)
+    if out is total and residual is not None:
+        raise ValueError("out and sum_out must be two tensors")
+    with _on(dev):
+        _check(load().layer_norm_fwd(_addr(x), _addr(residual), _addr(weight), _addr(bias),
+                                     float(eps), code, rows, D, _addr(out),
+                                     None if residual is None else _addr(total), _stream(dev)))
+    return out, total
+
+
+def layer_norm_bwd(total, weight, dy, eps=1e-5, dsum=None, workspace=None, need_dbias=True):
+    """Gradients of layer_norm_fwd for dL/dy = ``dy`` and dL/du = ``dsum`` (None: none), from
+    the ``total`` u that it returned: a dict with dx (as u; that of x and of the residual
+    alike), dweight [D] and dbias [D] (fp32; None unless ``need_dbias``)."""
+    torch = _torch()
+    code, dev, rows, D = _rows(total, "total", weight)
+    _need(dy, "dy", total.dtype, total.shape, dev)
+    if dsum is not None:
+        _need(dsum, "dsum", total.dtype, total.shape, dev)
+    ws = _space(workspace, int(load().layer_norm_bwd_workspace_size(code, rows, D)), dev)
+    r = {"dx": torch.empty_like(total), "dweight": torch.empty_like(weight),
+         "dbias": torch.empty_like(weight) if need_dbias else None}
+    with _on(dev):
+        _check(load().layer_norm_bwd(_addr(total), _addr(weight), float(eps), code, rows, D,
+                                     _addr(dy), _addr(dsum), _addr(r["dx"]), _addr(r["dweight"]),
+                                     _addr(r["dbias"]), _addr(ws), _nbytes(ws), _stream(dev)))
     return r

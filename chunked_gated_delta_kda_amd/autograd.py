@@ -263,3 +263,136 @@ def gated_norm(x, gate, weight, activation="sigmoid", eps=1e-6, residual=None,
     reach x, gate, weight, residual and residual_scale."""
     return _GatedNorm.get().apply(x, gate, weight, residual, residual_scale, activation,
                                   float(eps))
+
+
+class _GatedScan:
+    fn = None
+
+    @classmethod
+    def get(cls):
+        if cls.fn is None:
+            torch = _torch()
+
+            class GatedScanFunction(torch.autograd.Function):
+                @staticmethod
+                def forward(ctx, x, g, input_gate, A_log, dt_bias, initial_state, cu_seqlens,
+                            output_final_state):
+                    o, final, states = _b.gated_scan_fwd_save(
+                        x, g, input_gate, A_log, dt_bias, initial_state, output_final_state,
+                        cu_seqlens)
+                    ctx.save_for_backward(x, g, input_gate, A_log, dt_bias, states, initial_state,
+                                          cu_seqlens)
+                    ctx.set_materialize_grads(False)
+                    if final is None:
+                        return o
+                    return o, final
+
+                @staticmethod
+                @torch.autograd.function.once_differentiable
+                def backward(ctx, do, dfinal=None):
+                    x, g, input_gate, A_log, dt_bias, states, h0, cu = ctx.saved_tensors
+                    do = torch.zeros_like(x) if do is None else do.contiguous()
+                    r = _b.gated_scan_bwd(x, g, input_gate, A_log, dt_bias, do, states,
+                                          h0, None if dfinal is None else dfinal.contiguous(), cu,
+                                          need_dh0=h0 is not None and ctx.needs_input_grad[5])
+                    return (r["dx"], r["dg"], r["dinput_gate"], r["dA_log"], r["ddt_bias"],
+                            r["dh0"], None, None)
+
+            cls.fn = GatedScanFunction
+        return cls.fn
+
+
+class _ShortConv:
+    fn = None
+
+    @classmethod
+    def get(cls):
+        if cls.fn is None:
+            torch = _torch()
+
+            class ShortConvFunction(torch.autograd.Function):
+                @staticmethod
+                def forward(ctx, x, weight, bias, initial_state, activation, cu_seqlens,
+                            output_final_state):
+                    y, final = _b.short_conv_fwd(x, weight, bias, activation, initial_state,
+                                                 output_final_state, cu_seqlens)
+                    ctx.save_for_backward(x, weight, bias, initial_state, cu_seqlens)
+                    ctx.activation = activation
+                    ctx.set_materialize_grads(False)
+                    if final is None:
+                        return y
+                    return y, final
+
+                @staticmethod
+                @torch.autograd.function.once_differentiable
+                def backward(ctx, dy, dfinal=None):
+                    x, weight, bias, h0, cu = ctx.saved_tensors
+                    dy = torch.zeros_like(x) if dy is None else dy.contiguous()
+                    r = _b.short_conv_bwd(x, weight, dy, bias, ctx.activation, h0,
+                                          None if dfinal is None else dfinal.contiguous(), cu,
+                                          need_dh0=h0 is not None and ctx.needs_input_grad[3])
+                    return r["dx"], r["dweight"], r["dbias"], r["dh0"], None, None, None
+
+            cls.fn = ShortConvFunction
+        return cls.fn
+
+
+class _LayerNorm:
+    fn = None
+
+    @classmethod
+    def get(cls):
+        if cls.fn is None:
+            torch = _torch()
+
+            class LayerNormFunction(torch.autograd.Function):
+                @staticmethod
+                def forward(ctx, x, weight, bias, residual, eps):
+                    y, total = _b.layer_norm_fwd(x, weight, bias, eps, residual)
+                    ctx.save_for_backward(total, weight)
+                    ctx.eps = eps
+                    ctx.has_bias, ctx.has_residual = bias is not None, residual is not None
+                    ctx.set_materialize_grads(False)
+                    return (y, total) if residual is not None else y
+
+                @staticmethod
+                @torch.autograd.function.once_differentiable
+                def backward(ctx, dy, dsum=None):
+                    total, weight = ctx.saved_tensors
+                    dy = torch.zeros_like(total) if dy is None else dy.contiguous()
+                    r = _b.layer_norm_bwd(total, weight, dy, ctx.eps,
+                                          None if dsum is None else dsum.contiguous(),
+                                          need_dbias=ctx.has_bias)
+                    return (r["dx"], r["dweight"], r["dbias"],
+                            r["dx"] if ctx.has_residual else None, None)
+
+            cls.fn = LayerNormFunction
+        return cls.fn
+
+
+def gated_scan(x, g, input_gate, A_log, dt_bias, initial_state=None, output_final_state=False,
+               cu_seqlens=None):
+    """Differentiable gated linear recurrence over channels (see gated_scan_fwd).  Returns
+    (o, final_state); final_state is None unless ``output_final_state``.  Gradients reach x,
+    g, input_gate, A_log, dt_bias and initial_state."""
+    out = _GatedScan.get().apply(x, g, input_gate, A_log, dt_bias, initial_state, cu_seqlens,
+                                 bool(output_final_state))
+    return out if output_final_state else (out, None)
+
+
+def short_conv(x, weight, bias=None, activation="silu", initial_state=None,
+               output_final_state=False, cu_seqlens=None):
+    """Differentiable short causal convolution (see short_conv_fwd).  Returns (y,
+    final_state); final_state is None unless ``output_final_state``.  Gradients reach x,
+    weight, bias and initial_state."""
+    out = _ShortConv.get().apply(x, weight, bias, initial_state, activation, cu_seqlens,
+                                 bool(output_final_state))
+    return out if output_final_state else (out, None)
+
+
+def layer_norm(x, weight, bias=None, eps=1e-5, residual=None):
+    """Differentiable layer norm on rows x [..., D] (see layer_norm_fwd).  Returns (y, u)
+    with u = x + residual, or (y, x) without a residual.  Gradients reach x, weight, bias
+    and residual, through y and through u."""
+    out = _LayerNorm.get().apply(x, weight, bias, residual, float(eps))
+    return out if residual is not None else (out, x)

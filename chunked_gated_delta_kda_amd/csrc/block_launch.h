@@ -1,0 +1,126 @@
+// block_launch.h -- host-side launch interface of what stands around an
+// attention block (gated_scan.hip, short_conv.hip, layer_norm.hip) for the
+// C-ABI layer (block_api.hip).  Pointers are device pointers; token tensors are
+// bf16 or fp32, as the call's dtype says, everything else fp32.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "la_launch.h"
+
+namespace kda {
+
+// Tokens of a tile of the recurrence: the unit that a workgroup scans, and the distance
+// of the states that the forward pass keeps for its gradients.
+constexpr int GS_TILE = 128;
+
+struct ScanArgs {
+    const void* x;          // [B, T, C] tokens
+    const void* g;          // [B, T, C] tokens
+    const void* gate;       // [B, T, C] tokens
+    const float* A_log;     // [C]
+    const float* dt_bias;   // [C]
+    const float* h0;        // [N, C] or null
+    float* h_final;         // [N, C] or null
+    const int32_t* cu;      // [N + 1] or null (fixed length, N = B)
+    int32_t B, T, C, N;
+    int32_t tiles;          // of a row of the batch
+    void* o;                // [B, T, C] tokens
+    float* states;          // [B, tiles, C]: the state entering each tile (forward: or null)
+    // packed batches (gated_scan_marks): per 16 tokens, whether each begins a sequence,
+    // belongs to one, ends one; per token, which
+    uint2* marks;           // [ceil(T / 16)]
+    int32_t* seq;           // [16 * ceil(T / 16)]
+    // backward
+    const void* d_o;        // [B, T, C] tokens
+    const float* d_final;   // [N, C] or null
+    void* dx;               // [B, T, C] tokens
+    void* dg;
+    void* dgate;
+    float* dA_log;          // [C]
+    float* ddt_bias;        // [C]
+    float* dh0;             // [N, C] or null
+    float* part;            // [B * tiles, 2, C]: a tile's sums for dA_log and ddt_bias
+};
+
+struct ScanDecodeArgs {
+    const void* x;          // [N, C] tokens
+    const void* g;
+    const void* gate;
+    const float* A_log;
+    const float* dt_bias;
+    const float* state_in;  // [N, C] or null (zeros)
+    float* state_out;       // [N, C] (may equal state_in)
+    void* o;
+    int32_t N, C;
+};
+
+struct ConvArgs {
+    const void* x;          // [B, T, C] tokens
+    const float* weight;    // [C, W]
+    const float* bias;      // [C] or null
+    const void* h0;         // [N, W - 1, C] tokens or null
+    void* h_final;          // [N, W - 1, C] tokens or null
+    const int32_t* cu;
+    int32_t B, T, C, N;
+    int32_t silu;
+    void* y;                // [B, T, C] tokens
+    // backward
+    const void* dy;
+    const void* d_final;    // [N, W - 1, C] tokens or null
+    void* dx;
+    void* dh0;              // [N, W - 1, C] tokens or null
+    float* dweight;         // [C, W]
+    float* dbias;           // [C] or null
+    float* part;            // [groups, W + 1, C]: a workgroup's sums
+    int64_t groups;
+};
+
+struct ConvDecodeArgs {
+    const void* x;          // [N, C] tokens
+    const float* weight;
+    const float* bias;
+    const void* state_in;   // [N, W - 1, C] tokens
+    void* state_out;        // (may equal state_in)
+    void* y;
+    int32_t N, C;
+    int32_t silu;
+};
+
+struct LayerNormArgs {
+    const void* x;          // [rows, D] tokens (backward: the sum that was normalised)
+    const void* res;        // [rows, D] tokens or null
+    const float* weight;    // [D]
+    const float* bias;      // [D] or null
+    float eps;
+    int32_t D;
+    int64_t rows;
+    void* y;                // [rows, D] tokens
+    void* sum;              // [rows, D] tokens (with res)
+    // backward
+    const void* dy;
+    const void* dsum;       // [rows, D] tokens or null
+    void* dx;
+    float* dweight;         // [D]
+    float* dbias;           // [D] or null
+    float* part;            // [groups, 2, D]
+    int32_t groups;
+};
+
+// fp32: token tensors are fp32 (else bf16)
+void launch_gated_scan_fwd(const ScanArgs& a, bool fp32, hipStream_t stream);
+void launch_gated_scan_bwd(const ScanArgs& a, bool fp32, hipStream_t stream);
+void launch_gated_scan_decode(const ScanDecodeArgs& a, bool fp32, hipStream_t stream);
+// W: 2, 3 or 4 taps
+void launch_short_conv_fwd(const ConvArgs& a, int W, bool fp32, hipStream_t stream);
+void launch_short_conv_bwd(const ConvArgs& a, int W, bool fp32, hipStream_t stream);
+void launch_short_conv_decode(const ConvDecodeArgs& a, int W, bool fp32, hipStream_t stream);
+// rows of sums that the convolution's backward kernel leaves in part
+int64_t short_conv_groups(int32_t B, int32_t T);
+void launch_layer_norm_fwd(const LayerNormArgs& a, bool fp32, hipStream_t stream);
+void launch_layer_norm_bwd(const LayerNormArgs& a, bool fp32, hipStream_t stream);
+// workgroups of the norm's backward kernel, each leaving a row of sums in part
+int32_t layer_norm_groups(int64_t rows, int32_t D, bool fp32);
+
+}  // namespace kda

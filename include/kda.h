@@ -3,7 +3,8 @@
  * linear attention on AMD Instinct MI355X (gfx950).
  *
  * Two operations (and, at the end, linear attention with a decay for each
- * head, la_*, and the gated norm behind any of them):
+ * head, la_*, the gated norm behind any of them, and what stands around a
+ * block: gated_scan_*, short_conv_*, layer_norm_*):
  *   kda_fwd  Kimi Delta Attention: per-channel decay computed from a
  *            pre-activation gate, beta given as logits.
  *   gdn_fwd  Gated DeltaNet: one scalar log decay per (token, head), beta
@@ -513,6 +514,123 @@ int gated_norm_bwd(const uint16_t* x, const uint16_t* gate, const float* weight,
                    uint16_t* dx, uint16_t* dgate, float* dweight, uint16_t* dresidual,
                    float* dresidual_scale, void* workspace, size_t workspace_bytes,
                    void* stream);
+
+/* ------------------------------------------------------------------------
+ * What stands around an attention block of this family: a gated linear
+ * recurrence over channels (gated_scan_*), the short causal convolution in front
+ * of it and of q, k and v (short_conv_*), and the layer norm in front of the
+ * block (layer_norm_*).
+ *
+ * Conventions shared by the three, beyond those at the top of this file:
+ *  - Token tensors are bf16 or fp32, all of a call the same, as `dtype` says;
+ *    parameters, their gradients and the recurrence's states are fp32, the
+ *    convolution's states (they hold tokens) of the tokens' type.
+ *  - C (and D) are multiples of 8, C at most 2^20 and D at most 16384, else
+ *    KDA_ERR_UNSUPPORTED.  Alignment: token tensors and states 16 bytes,
+ *    parameters and their gradients 4, workspaces 256.
+ *  - cu_seqlens as for kda_fwd (B = 1); every row of an output is written: rows
+ *    outside every sequence get zeros, whatever the inputs hold there.
+ *    num_seqs is read only with cu_seqlens.
+ *  - Arithmetic is fp32, each output is rounded once; sums over tokens or rows
+ *    have a fixed order: equal calls give equal bits.
+ *  - A NaN or an infinity stays in its channel and sequence (convolution: in the
+ *    W tokens that see it; layer norm: in its row), and in the parameters'
+ *    gradients of its channel (layer norm: of all channels, for dweight). */
+enum kda_dtype { KDA_BF16 = 0, KDA_FP32 = 1 };
+
+/* Gated linear recurrence: per channel c, with KDA's decay gate,
+ *   L_t = exp(A_log[c]) softplus(g_t + dt_bias[c]),  a_t = exp(-L_t),
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(input_gate_t) x_t,  o_t = h_t.
+ * x, g, input_gate, o [B, T, C] tokens; A_log, dt_bias [C]; states
+ * [N, C].  initial_state NULL: zeros; final_state NULL: not written; a sequence
+ * without a token returns its initial state.  exp(A_log[c]) has to be finite.
+ * states (NULL: not kept): gated_scan_states(B, T, C) fp32 numbers, what
+ * gated_scan_bwd needs of the forward pass (the state that enters every 128th
+ * token of a row of the batch).  gated_scan_states is -1 for sizes that are not
+ * supported. */
+int64_t gated_scan_states(int32_t B, int32_t T, int32_t C);
+
+size_t gated_scan_fwd_workspace_size(int32_t B, int32_t T, int32_t C);
+
+int gated_scan_fwd(const void* x, const void* g, const void* input_gate, const float* A_log,
+                   const float* dt_bias, const float* initial_state, float* final_state,
+                   const int32_t* cu_seqlens, int32_t num_seqs, int32_t dtype, int32_t B,
+                   int32_t T, int32_t C, void* o, float* states, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* Gradients for dL/do = d_o and dL/d(final state) = d_final (NULL: zero):
+ * dx, dg, dinput_gate [B, T, C] tokens, dA_log, ddt_bias [C], dh0 [N, C] or NULL
+ * (not written).  states: those of a gated_scan_fwd call on the same inputs,
+ * sizes, initial_state and cu_seqlens. */
+size_t gated_scan_bwd_workspace_size(int32_t B, int32_t T, int32_t C);
+
+int gated_scan_bwd(const void* x, const void* g, const void* input_gate, const float* A_log,
+                   const float* dt_bias, const float* initial_state, const int32_t* cu_seqlens,
+                   int32_t num_seqs, int32_t dtype, int32_t B, int32_t T, int32_t C,
+                   const void* d_o, const float* d_final, const float* states, void* dx, void* dg,
+                   void* dinput_gate, float* dA_log, float* ddt_bias, float* dh0, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* One token for each of N sequences: x, g, input_gate, o [N, C] tokens; state_in
+ * (NULL: zeros), state_out [N, C], which may be the same array. */
+int gated_scan_decode(const void* x, const void* g, const void* input_gate, const float* A_log,
+                      const float* dt_bias, const float* state_in, float* state_out, int32_t dtype,
+                      int32_t N, int32_t C, void* o, void* stream);
+
+/* Short causal convolution: per channel c, with W taps (2, 3 or 4, else
+ * KDA_ERR_UNSUPPORTED),
+ *   z_t = bias[c] + sum_{j < W} weight[c, j] x_{t - W + 1 + j},  y_t = act(z_t).
+ * x, y [B, T, C] tokens; weight [C, W], bias [C] (NULL: none) fp32; states
+ * [N, W - 1, C] tokens: the last W - 1 tokens, the oldest first (initial_state:
+ * those in front of a sequence, NULL: zeros; final_state: those behind it, NULL:
+ * not written).  activation: KDA_CONV_NONE or KDA_CONV_SILU. */
+enum kda_conv_activation { KDA_CONV_NONE = 0, KDA_CONV_SILU = 1 };
+
+int short_conv_fwd(const void* x, const float* weight, const float* bias, int32_t activation,
+                   const void* initial_state, void* final_state, const int32_t* cu_seqlens,
+                   int32_t num_seqs, int32_t dtype, int32_t B, int32_t T, int32_t C, int32_t W,
+                   void* y, void* stream);
+
+/* Gradients for dL/dy = dy and dL/d(final state) = d_final [N, W - 1, C] tokens
+ * (NULL: zero): dx [B, T, C] tokens, dweight [C, W], dbias [C] (NULL only without
+ * a bias), dh0 [N, W - 1, C] tokens or NULL (not written).  No result of the
+ * forward call is needed. */
+size_t short_conv_bwd_workspace_size(int32_t B, int32_t T, int32_t C, int32_t W);
+
+int short_conv_bwd(const void* x, const float* weight, const float* bias, int32_t activation,
+                   const void* initial_state, const int32_t* cu_seqlens, int32_t num_seqs,
+                   int32_t dtype, int32_t B, int32_t T, int32_t C, int32_t W, const void* dy,
+                   const void* d_final, void* dx, float* dweight, float* dbias, void* dh0,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token for each of N sequences: x, y [N, C] tokens; state_in, state_out
+ * [N, W - 1, C] tokens, which may be the same array. */
+int short_conv_decode(const void* x, const float* weight, const float* bias, int32_t activation,
+                      const void* state_in, void* state_out, int32_t dtype, int32_t N, int32_t C,
+                      int32_t W, void* y, void* stream);
+
+/* Layer norm, per row of D channels:
+ *   u = x + residual (rounded to the tokens' type: it is written to sum),
+ *   y = (u - mean(u)) / sqrt(mean((u - mean(u))^2) + eps) weight + bias.
+ * x, residual, y, sum [rows, D] tokens; weight [D], bias [D] (NULL: none) fp32.
+ * residual NULL: u = x, and sum is not written.  eps >= 0; rows < 2^31, rows = 0
+ * is allowed (row tensors may then be NULL).  y may be x or residual, and sum may
+ * be x or residual (each row is read before it is written), y and sum are two
+ * arrays.  Rows of any size keep their precision: where their squares would leave
+ * fp32's range they are scaled by a power of two first.  A row of equal values
+ * with eps = 0 gives NaN. */
+int layer_norm_fwd(const void* x, const void* residual, const float* weight, const float* bias,
+                   float eps, int32_t dtype, int64_t rows, int32_t D, void* y, void* sum,
+                   void* stream);
+
+/* Gradients for dL/dy = dy and dL/dsum = dsum [rows, D] tokens (NULL: none): dx
+ * [rows, D] tokens (that of x and of residual alike), dweight [D], dbias [D] or
+ * NULL (not written).  sum: what was normalised (x where there was no residual). */
+size_t layer_norm_bwd_workspace_size(int32_t dtype, int64_t rows, int32_t D);
+
+int layer_norm_bwd(const void* sum, const float* weight, float eps, int32_t dtype, int64_t rows,
+                   int32_t D, const void* dy, const void* dsum, void* dx, float* dweight,
+                   float* dbias, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static description of a status code (never NULL). */
 const char* kda_status_str(int status);
