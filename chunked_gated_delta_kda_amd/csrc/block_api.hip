@@ -38,22 +38,29 @@ bool valid_batch(int32_t B, int32_t T, int32_t C) {
     return B >= 1 && T >= 0 && C >= 8 && C % 8 == 0 && C <= MAX_CHANNELS && (int64_t)B * T < I31;
 }
 
-int32_t scan_tiles(int32_t T) { return (int32_t)(((int64_t)T + kda::GS_TILE - 1) / kda::GS_TILE); }
+int32_t scan_states(int32_t T) { return (int32_t)(((int64_t)T + kda::GS_STATES - 1) / kda::GS_STATES); }
 
-// Workspace of the recurrence: a packed batch's marks and sequences, and for the
-// gradients the tiles' sums.  One row of a batch may be packed or not.
+// Tiles of all rows, of 64 channels and more, are counted in 32 bits (their tickets).
+bool countable_tiles(int32_t B, int32_t T, int32_t C) {
+    return (int64_t)B * scan_states(T) * ((C + 63) / 64) < I31;
+}
+
+// Workspace of the recurrence: the tiles' words and the ticket, a packed batch's marks
+// and sequences, and for the gradients the tiles' sums.  One row of a batch may be packed
+// or not.
 struct ScanSpace {
-    size_t marks, seq, part, total;
+    size_t ticket, words, marks, seq, part, total;
 };
 
 ScanSpace scan_space(int32_t B, int32_t T, int32_t C, bool backward) {
     const size_t groups = ((size_t)T + 15) / 16;
     ScanSpace s{};
-    s.marks = 0;
+    s.ticket = 0;
+    s.words = ALIGN;
+    s.marks = s.words + align_up((size_t)B * scan_states(T) * C * sizeof(uint64_t));
     s.seq = s.marks + (B == 1 ? align_up(groups * sizeof(uint2)) : 0);
     s.part = s.seq + (B == 1 ? align_up(groups * 16 * sizeof(int32_t)) : 0);
-    s.total = s.part + (backward ? align_up((size_t)B * scan_tiles(T) * 2 * C * sizeof(float)) : 0);
-    s.total = std::max(s.total, ALIGN);
+    s.total = s.part + (backward ? align_up((size_t)B * scan_states(T) * 2 * C * sizeof(float)) : 0);
     return s;
 }
 
@@ -62,6 +69,7 @@ int check_scan(const void* x, const void* g, const void* gate, const float* A_lo
                int32_t C) {
     const int st = check_batch(dtype, cu, num_seqs, B, T, C);
     if (st != KDA_OK) return st;
+    if (!countable_tiles(B, T, C)) return KDA_ERR_INVALID_ARG;
     if (!A_log || !dt_bias || (T > 0 && (!x || !g || !gate))) return KDA_ERR_INVALID_ARG;
     if (!aligned({x, g, gate, initial_state}, 16) || !aligned({A_log, dt_bias}, 4)) return KDA_ERR_INVALID_ARG;
     return KDA_OK;
@@ -87,7 +95,9 @@ kda::ScanArgs scan_args(const void* x, const void* g, const void* gate, const fl
     a.T = T;
     a.C = C;
     a.N = cu ? num_seqs : B;
-    a.tiles = scan_tiles(T);
+    a.n_states = scan_states(T);
+    a.ticket = reinterpret_cast<uint32_t*>(ws + sp.ticket);
+    a.words = reinterpret_cast<uint64_t*>(ws + sp.words);
     a.marks = reinterpret_cast<uint2*>(ws + sp.marks);
     a.seq = reinterpret_cast<int32_t*>(ws + sp.seq);
     a.part = reinterpret_cast<float*>(ws + sp.part);
@@ -134,15 +144,15 @@ int check_layer_norm(const float* weight, float eps, int32_t dtype, int64_t rows
 extern "C" {
 
 int64_t gated_scan_states(int32_t B, int32_t T, int32_t C) {
-    return valid_batch(B, T, C) ? (int64_t)B * scan_tiles(T) * C : -1;
+    return valid_batch(B, T, C) && countable_tiles(B, T, C) ? (int64_t)B * scan_states(T) * C : -1;
 }
 
 size_t gated_scan_fwd_workspace_size(int32_t B, int32_t T, int32_t C) {
-    return valid_batch(B, T, C) ? scan_space(B, T, C, false).total : 0;
+    return valid_batch(B, T, C) && countable_tiles(B, T, C) ? scan_space(B, T, C, false).total : 0;
 }
 
 size_t gated_scan_bwd_workspace_size(int32_t B, int32_t T, int32_t C) {
-    return valid_batch(B, T, C) ? scan_space(B, T, C, true).total : 0;
+    return valid_batch(B, T, C) && countable_tiles(B, T, C) ? scan_space(B, T, C, true).total : 0;
 }
 
 int gated_scan_fwd(const void* x, const void* g, const void* input_gate, const float* A_log, const float* dt_bias,

@@ -11,9 +11,9 @@
 
 namespace kda {
 
-// Tokens of a tile of the recurrence: the unit that a workgroup scans, and the distance
-// of the states that the forward pass keeps for its gradients.
-constexpr int GS_TILE = 128;
+// The recurrence's tiles are 128 tokens of a row of the batch in the forward pass and 64
+// in the backward pass; the forward pass keeps the state that enters every 64th token.
+constexpr int GS_STATES = 64;
 
 struct ScanArgs {
     const void* x;          // [B, T, C] tokens
@@ -25,10 +25,14 @@ struct ScanArgs {
     float* h_final;         // [N, C] or null
     const int32_t* cu;      // [N + 1] or null (fixed length, N = B)
     int32_t B, T, C, N;
-    int32_t tiles;          // of a row of the batch
+    int32_t n_states;       // of a row of the batch
     void* o;                // [B, T, C] tokens
-    float* states;          // [B, tiles, C]: the state entering each tile (forward: or null)
-    // packed batches (gated_scan_marks): per 16 tokens, whether each begins a sequence,
+    float* states;          // [B, n_states, C] (forward: or null)
+    // what the tiles of a chain post for those behind them, and the next tile to be taken
+    // (neither is used where a row is one tile)
+    uint64_t* words;        // [tiles, B, C]
+    uint32_t* ticket;
+    // packed batches: per 16 tokens, whether each begins a sequence,
     // belongs to one, ends one; per token, which
     uint2* marks;           // [ceil(T / 16)]
     int32_t* seq;           // [16 * ceil(T / 16)]
@@ -41,7 +45,7 @@ struct ScanArgs {
     float* dA_log;          // [C]
     float* ddt_bias;        // [C]
     float* dh0;             // [N, C] or null
-    float* part;            // [B * tiles, 2, C]: a tile's sums for dA_log and ddt_bias
+    float* part;            // [B, n_states, 2, C]: a tile's sums for dA_log and ddt_bias
 };
 
 struct ScanDecodeArgs {

@@ -544,8 +544,9 @@ enum kda_dtype { KDA_BF16 = 0, KDA_FP32 = 1 };
  * x, g, input_gate, o [B, T, C] tokens; A_log, dt_bias [C]; states
  * [N, C].  initial_state NULL: zeros; final_state NULL: not written; a sequence
  * without a token returns its initial state.  exp(A_log[c]) has to be finite.
+ * B ceil(T / 64) ceil(C / 64) < 2^31.
  * states (NULL: not kept): gated_scan_states(B, T, C) fp32 numbers, what
- * gated_scan_bwd needs of the forward pass (the state that enters every 128th
+ * gated_scan_bwd needs of the forward pass (the state that enters every 64th
  * token of a row of the batch).  gated_scan_states is -1 for sizes that are not
  * supported. */
 int64_t gated_scan_states(int32_t B, int32_t T, int32_t C);

@@ -31,7 +31,8 @@ SCAN = dict(x=FAKE, g=FAKE, gate=FAKE, A=FAKE, b=FAKE, h0=None, hT=None, cu=None
             states=None, ws=FAKE, wsb=BIG, stream=None)
 SCAN_ONLY = [(dict(g=None), 1), (dict(gate=None), 1), (dict(A=None), 1), (dict(b=None), 1), (dict(g=odd(4)), 1),
              (dict(gate=odd(8)), 1), (dict(A=odd(2)), 1), (dict(b=odd(1)), 1), (dict(ws=None), 3),
-             (dict(ws=odd(16)), 3), (dict(wsb=255), 3), (dict(states=odd(8)), 1)]
+             (dict(ws=odd(16)), 3), (dict(wsb=255), 3), (dict(states=odd(8)), 1),
+             (dict(B=1 << 24, T=64, C=1 << 13), 1)]
 
 
 @pytest.mark.parametrize("over,code", SIZES + SCAN_ONLY + [(dict(o=None), 1), (dict(o=odd(8)), 1),
@@ -126,12 +127,16 @@ def test_no_rows_is_no_call(lib):
 
 
 def test_sizes(lib):
-    assert lib.gated_scan_states(2, 129, 64) == 2 * 2 * 64
+    assert lib.gated_scan_states(2, 129, 64) == 2 * 3 * 64
     assert lib.gated_scan_states(1, 0, 64) == 0
     for bad in ((0, 1, 64), (1, -1, 64), (1, 1, 12), (1, 1, (1 << 20) + 8), (1 << 16, 1 << 15, 64)):
         assert lib.gated_scan_states(*bad) == -1
         assert kda.gated_scan_workspace_size(*bad) == kda.gated_scan_workspace_size(*bad, backward=True) == 0
         assert lib.short_conv_bwd_workspace_size(*bad, 4) == 0
+    # more tiles than tickets: 2^24 of 64 tokens, 2^7 blocks of 64 channels
+    assert lib.gated_scan_states(1 << 24, 64, 1 << 13) == -1
+    assert kda.gated_scan_workspace_size(1 << 24, 64, 1 << 13) == 0
+    assert lib.gated_scan_states((1 << 24) - 1, 64, 1 << 13) == ((1 << 24) - 1) << 13
     assert kda.gated_scan_workspace_size(2, 100, 64) >= 256
     assert lib.short_conv_bwd_workspace_size(1, 1, 64, 5) == 0
     assert lib.layer_norm_bwd_workspace_size(0, 5, 12) == lib.layer_norm_bwd_workspace_size(3, 5, 64) == 0
