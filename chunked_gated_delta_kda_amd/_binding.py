@@ -155,7 +155,7 @@ def load(path: Path | str | None = None):
     lib.short_conv_fwd.argtypes = [vp, f32p, f32p, i32, vp, vp, i32p, i32, i32, i32, i32, i32,
                                    i32, vp, vp]
     lib.short_conv_bwd_workspace_size.restype = ctypes.c_size_t
-    lib.short_conv_bwd_workspace_size.argtypes = [i32] * 4
+    lib.short_conv_bwd_workspace_size.argtypes = [i32] * 5
     lib.short_conv_bwd.restype = ctypes.c_int
     lib.short_conv_bwd.argtypes = [vp, f32p, f32p, i32, vp, i32p, i32, i32, i32, i32, i32, i32,
                                    vp, vp, vp, f32p, f32p, vp, vp, sz, vp]
@@ -1150,7 +1150,7 @@ def short_conv_bwd(x, weight, dy, bias=None, activation="silu", initial_state=No
     for t, name in ((initial_state, "initial_state"), (dfinal, "dfinal")):
         if t is not None:
             _need(t, name, x.dtype, (N, W - 1, C), dev)
-    ws = _space(workspace, int(load().short_conv_bwd_workspace_size(B, T, C, W)), dev)
+    ws = _space(workspace, int(load().short_conv_bwd_workspace_size(code, B, T, C, W)), dev)
     r = {"dx": torch.empty_like(x), "dweight": torch.empty_like(weight),
          "dbias": None if bias is None else torch.empty_like(bias),
          "dh0": torch.empty((N, W - 1, C), dtype=x.dtype, device=dev) if need_dh0 else None}

@@ -242,9 +242,10 @@ int short_conv_fwd(const void* x, const float* weight, const float* bias, int32_
     return status();
 }
 
-size_t short_conv_bwd_workspace_size(int32_t B, int32_t T, int32_t C, int32_t W) {
-    if (!valid_batch(B, T, C) || W < 2 || W > 4) return 0;
-    return std::max(ALIGN, align_up((size_t)kda::short_conv_groups(B, T) * (W + 1) * C * sizeof(float)));
+size_t short_conv_bwd_workspace_size(int32_t dtype, int32_t B, int32_t T, int32_t C, int32_t W) {
+    if (!valid_batch(B, T, C) || W < 2 || W > 4 || !known_type(dtype)) return 0;
+    return std::max(
+        ALIGN, align_up((size_t)kda::short_conv_groups(B, T, C, dtype == KDA_FP32) * (W + 1) * C * sizeof(float)));
 }
 
 int short_conv_bwd(const void* x, const float* weight, const float* bias, int32_t activation,
@@ -255,7 +256,7 @@ int short_conv_bwd(const void* x, const float* weight, const float* bias, int32_
     if (st != KDA_OK) return st;
     if (!dweight || (bias && !dbias) || (T > 0 && (!dy || !dx))) return KDA_ERR_INVALID_ARG;
     if (!aligned({dy, d_final, dx, dh0}, 16) || !aligned({dweight, dbias}, 4)) return KDA_ERR_INVALID_ARG;
-    st = check_workspace(workspace, workspace_bytes, short_conv_bwd_workspace_size(B, T, C, W));
+    st = check_workspace(workspace, workspace_bytes, short_conv_bwd_workspace_size(dtype, B, T, C, W));
     if (st != KDA_OK) return st;
     kda::ConvArgs a = conv_args(x, weight, bias, activation, initial_state, cu_seqlens, num_seqs, B, T, C);
     a.dy = dy;
@@ -265,7 +266,6 @@ int short_conv_bwd(const void* x, const float* weight, const float* bias, int32_
     a.dbias = dbias;
     a.dh0 = dh0;
     a.part = static_cast<float*>(workspace);
-    a.groups = kda::short_conv_groups(B, T);
     (void)hipGetLastError();
     kda::launch_short_conv_bwd(a, W, dtype == KDA_FP32, static_cast<hipStream_t>(stream));
     return status();

@@ -35,14 +35,18 @@ struct Word<float> {
     static __device__ __forceinline__ uint32_t put(const float* f) { return __float_as_uint(f[0]); }
 };
 
-// A sigmoid 1 / (1 + e^-z) as e^min(z, 0) / (1 + e^-|z|): to a few ulps where it is
-// normal, and subnormal below z = -87.  `rest` is 1 - s.
+// A sigmoid 1 / (1 + e^-z) as e^min(z, 0) / (1 + e^-|z|), to a few ulps where it is
+// normal, and subnormal below z = -87 (2^t by the hardware is not: the exponent's whole
+// part is put in behind it).  `rest` is 1 - s.
 struct BlockSigmoid {
     float s, rest;
     __device__ __forceinline__ explicit BlockSigmoid(float z) {
-        const float e = expf(-fabsf(z)), r = 1.f / (1.f + e);
-        s = z < 0.f ? e * r : r;
-        rest = z < 0.f ? r : e * r;
+        const float t = fmaxf(-LOG2E * fabsf(z), -200.f), n = floorf(t);
+        const float e = ldexpf(__builtin_amdgcn_exp2f(t - n), (int)n), r = __builtin_amdgcn_rcpf(1.f + e);
+        const float er = e * r;
+        s = z < 0.f ? er : r;
+        rest = z < 0.f ? r : er;
+        if (z != z) s = rest = z;
     }
 };
 
@@ -60,42 +64,73 @@ __device__ __forceinline__ double sum_strided(const float* p, int64_t n, int64_t
     return s;
 }
 
-// A workgroup of 256 threads adds 8 columns of n rows, `step` apart, in a fixed order and
-// in 64 bits: thread i has column i % 8 (where p points) and every 32nd row; threads 0 to
-// 7 return the sums.
+// A workgroup of 256 threads adds 32 columns of n rows, `step` apart, in a fixed order and
+// in 64 bits: thread i has column i % 32 (where p points) and every 8th row.  Returns the
+// sum of the thread's column.
 __device__ __forceinline__ double sum_columns(const float* p, int64_t n, int64_t step) {
-    __shared__ double red[256];
-    const int tid = threadIdx.x, first = tid / 8;
-    red[tid] = sum_strided(p + first * step, (n - first + 31) / 32, 32 * step);
+    __shared__ double red[8][32];
+    const int col = threadIdx.x % 32, first = threadIdx.x / 32;
+    red[first][col] = sum_strided(p + first * step, (n - first + 7) / 8, 8 * step);
     __syncthreads();
-    for (int m = 128; m >= 8; m >>= 1) {
-        if (tid < m) red[tid] += red[tid + m];
-        __syncthreads();
-    }
-    return red[tid % 8];
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += red[i][col];
+    return s;
 }
 
-// 16 bytes of a token tensor: eight bf16 channels or four fp32 channels
-template <class T>
-struct Slice {
-    static constexpr int W = Word<T>::N, N = 4 * W;
-    static __device__ __forceinline__ void load(const void* p, int64_t at, float* f) {
-        unpack(*reinterpret_cast<const u32x4*>(static_cast<const T*>(p) + at), f);
+// the sum of both of v's lanes in each pair of lanes that differ in bit `m` (a power of
+// two), where the lower bits' sums are done
+template <int m>
+__device__ __forceinline__ float add_across(float v) {
+    const int w = __float_as_int(v);
+    if constexpr (m == 1) return v + __int_as_float(__builtin_amdgcn_update_dpp(0, w, 0xB1, 0xf, 0xf, true));
+    else if constexpr (m == 2) return v + __int_as_float(__builtin_amdgcn_update_dpp(0, w, 0x4E, 0xf, 0xf, true));
+    else if constexpr (m == 4) return v + __int_as_float(__builtin_amdgcn_update_dpp(0, w, 0x141, 0xf, 0xf, true));
+    else if constexpr (m == 8) return v + __int_as_float(__builtin_amdgcn_update_dpp(0, w, 0x140, 0xf, 0xf, true));
+    else if constexpr (m == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+        return __int_as_float(r[0]) + __int_as_float(r[1]);
+    } else {
+        const auto r = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+        return __int_as_float(r[0]) + __int_as_float(r[1]);
     }
-    static __device__ __forceinline__ void unpack(u32x4 v, float* f) {
+}
+
+// the sum over L lanes that stand together, in each of them
+template <int L>
+__device__ __forceinline__ float lane_sum(float v) {
+    if constexpr (L > 1) v = add_across<1>(v);
+    if constexpr (L > 2) v = add_across<2>(v);
+    if constexpr (L > 4) v = add_across<4>(v);
+    if constexpr (L > 8) v = add_across<8>(v);
+    if constexpr (L > 16) v = add_across<16>(v);
+    if constexpr (L > 32) v = add_across<32>(v);
+    return v;
+}
+
+// R words of a token row (8 or 16 bytes): 2 R bf16 channels or R fp32 channels
+template <class T, int R = 4>
+struct Slice {
+    static constexpr int W = Word<T>::N, N = R * W;
+    typedef __attribute__((ext_vector_type(R))) unsigned int raw;
+    static __device__ __forceinline__ raw load(const void* p, int64_t at) {
+        return *reinterpret_cast<const raw*>(static_cast<const T*>(p) + at);
+    }
+    static __device__ __forceinline__ void load(const void* p, int64_t at, float* f) { unpack(load(p, at), f); }
+    static __device__ __forceinline__ void unpack(raw v, float* f) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) Word<T>::get(v[i], f + W * i);
+        for (int i = 0; i < R; ++i) Word<T>::get(v[i], f + W * i);
     }
     static __device__ __forceinline__ void store(void* p, int64_t at, const float* f) {
-        u32x4 v;
+        raw v;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = Word<T>::put(f + W * i);
-        *reinterpret_cast<u32x4*>(static_cast<T*>(p) + at) = v;
+        for (int i = 0; i < R; ++i) v[i] = Word<T>::put(f + W * i);
+        *reinterpret_cast<raw*>(static_cast<T*>(p) + at) = v;
     }
     // f as it is when stored
     static __device__ __forceinline__ void round(const float* f, float* r) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) Word<T>::get(Word<T>::put(f + W * i), r + W * i);
+        for (int i = 0; i < R; ++i) Word<T>::get(Word<T>::put(f + W * i), r + W * i);
     }
 };
 

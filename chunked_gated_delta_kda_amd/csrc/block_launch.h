@@ -78,7 +78,8 @@ struct ConvArgs {
     float* dweight;         // [C, W]
     float* dbias;           // [C] or null
     float* part;            // [groups, W + 1, C]: a workgroup's sums
-    int64_t groups;
+    int64_t groups;         // workgroups of strips (of a block of channels), and a strip's tokens
+    int32_t strip;
 };
 
 struct ConvDecodeArgs {
@@ -121,7 +122,7 @@ void launch_short_conv_fwd(const ConvArgs& a, int W, bool fp32, hipStream_t stre
 void launch_short_conv_bwd(const ConvArgs& a, int W, bool fp32, hipStream_t stream);
 void launch_short_conv_decode(const ConvDecodeArgs& a, int W, bool fp32, hipStream_t stream);
 // rows of sums that the convolution's backward kernel leaves in part
-int64_t short_conv_groups(int32_t B, int32_t T);
+int64_t short_conv_groups(int32_t B, int32_t T, int32_t C, bool fp32);
 void launch_layer_norm_fwd(const LayerNormArgs& a, bool fp32, hipStream_t stream);
 void launch_layer_norm_bwd(const LayerNormArgs& a, bool fp32, hipStream_t stream);
 // workgroups of the norm's backward kernel, each leaving a row of sums in part

@@ -576,15 +576,15 @@ __global__ __launch_bounds__(GS_THREADS, 4) void gated_scan_bwd_kernel(ScanArgs 
     }
 }
 
-// dA_log and ddt_bias from the tiles' sums, in a fixed order and in 64 bits: a workgroup
-// for 8 channels of one of them
+// dA_log and ddt_bias from the tiles' sums: a workgroup for 32 channels of one of them
 __global__ __launch_bounds__(256) void gated_scan_sum_kernel(ScanArgs a) {
-    const int which = blockIdx.x % 2, c = blockIdx.x / 2 * 8 + threadIdx.x % 8;
-    const double s = sum_columns(a.part + (int64_t)which * a.C + c, (int64_t)a.B * tiles_of(a.T, BWD_TILE), (int64_t)2 * a.C);
-    if (threadIdx.x < 8) (which ? a.ddt_bias : a.dA_log)[c] = (float)s;
+    const int which = blockIdx.x % 2, c = blockIdx.x / 2 * 32 + threadIdx.x % 32;
+    const double s = sum_columns(a.part + (int64_t)which * a.C + min(c, a.C - 1), (int64_t)a.B * a.n_states,
+                                 (int64_t)2 * a.C);
+    if (threadIdx.x < 32 && c < a.C) (which ? a.ddt_bias : a.dA_log)[c] = (float)s;
 }
 
-// One token: 4 words of a row a lane.
+// One token: a word of a row a lane.
 template <class T>
 __global__ __launch_bounds__(256) void gated_scan_decode_kernel(ScanDecodeArgs a) {
     constexpr int V = Word<T>::N;
@@ -653,7 +653,7 @@ void launch_gated_scan_bwd(const ScanArgs& a, bool fp32, hipStream_t stream) {
                                dim3(GS_THREADS), 0, stream, a);
         });
     }
-    hipLaunchKernelGGL(gated_scan_sum_kernel, dim3((unsigned)(a.C / 4)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(gated_scan_sum_kernel, dim3((unsigned)((a.C + 31) / 32 * 2)), dim3(256), 0, stream, a);
 }
 
 void launch_gated_scan_decode(const ScanDecodeArgs& a, bool fp32, hipStream_t stream) {

@@ -14,6 +14,8 @@
 // is fp32; each output is rounded once.  The backward kernel's workgroups walk
 // over the rows and keep their lanes' channels of dweight and dbias in registers;
 // a second kernel adds the workgroups' sums in a fixed order, in 64 bits.
+#include <algorithm>
+
 #include "block_device.h"
 
 namespace kda {
@@ -21,26 +23,24 @@ namespace kda {
 namespace {
 
 constexpr int LN_THREADS = 256;  // of a workgroup whose rows are a wave's or less
-constexpr int LN_GROUPS = 1024;  // most workgroups of the backward kernel
 
-// Sums of n values over the L lanes (or threads, from 256 on) that share a row.
+// Sums of n values over the L lanes (or threads, from 256 on) that share a row.  `red`
+// belongs to this one sum: another's barrier stands between two uses of it.
 template <int L, int n>
-__device__ __forceinline__ void row_sums(float (&v)[n]) {
+__device__ __forceinline__ void row_sums(float (&v)[n], float (*red)[16]) {
 #pragma unroll
-    for (int m = 1; m < (L < 64 ? L : 64); m <<= 1)
-#pragma unroll
-        for (int i = 0; i < n; ++i) v[i] += __shfl_xor(v[i], m);
+    for (int i = 0; i < n; ++i) v[i] = lane_sum<(L < 64 ? L : 64)>(v[i]);
     if constexpr (L > 64) {
         constexpr int WAVES = L / 64;
-        __shared__ float red[n][WAVES];
-        __syncthreads();
-        if (threadIdx.x % 64 == 0)
+        if (threadIdx.x % 64 == 0) {
 #pragma unroll
             for (int i = 0; i < n; ++i) red[i][threadIdx.x / 64] = v[i];
+        }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < n; ++i) {
             v[i] = 0.f;
+#pragma unroll
             for (int w = 0; w < WAVES; ++w) v[i] += red[i][w];
         }
     }
@@ -76,6 +76,7 @@ __device__ __forceinline__ float row_scale(float m) {
 
 template <int L, int M>
 __device__ __forceinline__ Stats row_stats(float (&u)[M], int count, int D, float eps) {
+    __shared__ float red_one[1][16], red_two[2][16];
     Stats s;
     s.scale = 1.f;
     const float inv = 1.f / (float)D;
@@ -83,7 +84,7 @@ __device__ __forceinline__ Stats row_stats(float (&u)[M], int count, int D, floa
         float one[1] = {0.f};
 #pragma unroll
         for (int i = 0; i < M; ++i) one[0] += u[i];  // (zeros behind the row's end)
-        row_sums<L, 1>(one);
+        row_sums<L, 1>(one, red_one);
         s.mean = one[0] * inv;
         float two[2] = {0.f, 0.f};
 #pragma unroll
@@ -92,7 +93,7 @@ __device__ __forceinline__ Stats row_stats(float (&u)[M], int count, int D, floa
             two[0] += d;
             two[1] = fmaf(d, d, two[1]);
         }
-        row_sums<L, 2>(two);
+        row_sums<L, 2>(two, red_two);
         s.rest = two[0] * inv;
         float var = fmaf(-s.rest, s.rest, two[1] * inv);
         var = (var < 0.f ? 0.f : var) + eps * s.scale * s.scale;  // (a NaN stays)
@@ -110,47 +111,79 @@ __device__ __forceinline__ Stats row_stats(float (&u)[M], int count, int D, floa
 
 }  // namespace
 
-// K slices of a row in each of its L lanes
+// K slices of a row in each of its L lanes, the workgroup's rows one after the other.  The
+// weights stay in registers and the next row's loads are under way while this one is
+// summed, but in workgroups of 1024 threads, whose 128 registers a lane they do not fit.
 template <class T, int L, int K>
 __global__ __launch_bounds__(L > LN_THREADS ? L : LN_THREADS) void layer_norm_fwd_kernel(LayerNormArgs a) {
     constexpr int V = Slice<T>::N, THREADS = L > LN_THREADS ? L : LN_THREADS, RPW = THREADS / L;
+    constexpr bool AHEAD = THREADS < 1024;
     const int l = threadIdx.x % L;
-    const int64_t row = ((int64_t)blockIdx.z * gridDim.x + blockIdx.x) * RPW + threadIdx.x / L;
-    if (row >= a.rows) return;  // (all lanes of a row together)
-    const int64_t at = row * a.D;
-    float u[K * V];
+    float wt[K * V], bias[K * V];
     int count = 0;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int c = (k * L + l) * V;
-        if (c < a.D) {
-            Slice<T>::load(a.x, at + c, u + k * V);
-            if (a.res) {
-                float r[V];
-                Slice<T>::load(a.res, at + c, r);
-#pragma unroll
-                for (int v = 0; v < V; ++v) r[v] += u[k * V + v];
-                Slice<T>::store(a.sum, at + c, r);
-                Slice<T>::round(r, u + k * V);
-            }
-            count = (k + 1) * V;
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v) u[k * V + v] = 0.f;
-        }
-    }
-    const Stats s = row_stats<L, K * V>(u, count, a.D, a.eps);
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int c = (k * L + l) * V;
-        if (c < a.D) {
-            float y[V];
+        if (c < a.D) count = (k + 1) * V;
+        if constexpr (AHEAD) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float n = ((u[k * V + v] - s.mean) - s.rest) * s.rho;
-                y[v] = fmaf(n, a.weight[c + v], a.bias ? a.bias[c + v] : 0.f);
+                wt[k * V + v] = c < a.D ? a.weight[c + v] : 0.f;
+                bias[k * V + v] = c < a.D && a.bias ? a.bias[c + v] : 0.f;
             }
-            Slice<T>::store(a.y, at + c, y);
+        }
+    }
+    const int64_t step = (int64_t)a.groups * RPW;
+    int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / L;
+    u32x4 rx[K], rr[K];
+    const auto fetch = [&](int64_t r) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * L + l) * V;
+            if (c < a.D) {
+                rx[k] = Slice<T>::load(a.x, r * a.D + c);
+                if (a.res) rr[k] = Slice<T>::load(a.res, r * a.D + c);
+            }
+        }
+    };
+    if (AHEAD && row < a.rows) fetch(row);
+    for (; row < a.rows; row += step) {
+        const int64_t at = row * a.D;
+        float u[K * V];
+        if (!AHEAD) fetch(row);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * L + l) * V;
+            if (c < a.D) {
+                Slice<T>::unpack(rx[k], u + k * V);
+                if (a.res) {
+                    float r[V];
+                    Slice<T>::unpack(rr[k], r);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) r[v] += u[k * V + v];
+                    Slice<T>::store(a.sum, at + c, r);
+                    Slice<T>::round(r, u + k * V);
+                }
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) u[k * V + v] = 0.f;
+            }
+        }
+        if (AHEAD && row + step < a.rows) fetch(row + step);
+        const Stats s = row_stats<L, K * V>(u, count, a.D, a.eps);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * L + l) * V;
+            if (c < a.D) {
+                float y[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float n = ((u[k * V + v] - s.mean) - s.rest) * s.rho;
+                    if constexpr (AHEAD) y[v] = fmaf(n, wt[k * V + v], bias[k * V + v]);
+                    else y[v] = fmaf(n, a.weight[c + v], a.bias ? a.bias[c + v] : 0.f);
+                }
+                Slice<T>::store(a.y, at + c, y);
+            }
         }
     }
 }
@@ -158,58 +191,80 @@ __global__ __launch_bounds__(L > LN_THREADS ? L : LN_THREADS) void layer_norm_fw
 template <class T, int L, int K>
 __global__ __launch_bounds__(L > LN_THREADS ? L : LN_THREADS) void layer_norm_bwd_kernel(LayerNormArgs a) {
     constexpr int V = Slice<T>::N, THREADS = L > LN_THREADS ? L : LN_THREADS, RPW = THREADS / L;
+    constexpr bool AHEAD = THREADS < 1024;
+    __shared__ float red_t[2][16];
     const int l = threadIdx.x % L;
-    float dw[K * V], db[K * V];
+    float dw[K * V], db[K * V], wt[K * V];
+    int count = 0;
 #pragma unroll
-    for (int i = 0; i < K * V; ++i) dw[i] = db[i] = 0.f;
+    for (int k = 0; k < K; ++k) {
+        const int c = (k * L + l) * V;
+        if (c < a.D) count = (k + 1) * V;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            dw[k * V + v] = db[k * V + v] = 0.f;
+            if constexpr (AHEAD) wt[k * V + v] = c < a.D ? a.weight[c + v] : 0.f;
+        }
+    }
     const float inv = 1.f / (float)a.D;
-    for (int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / L; row < a.rows; row += (int64_t)a.groups * RPW) {
-        const int64_t at = row * a.D;
-        float u[K * V], dy[K * V];
-        int count = 0;
+    const int64_t step = (int64_t)a.groups * RPW;
+    int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / L;
+    u32x4 rx[K], ry[K], rs[K];
+    const auto fetch = [&](int64_t r) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (k * L + l) * V;
             if (c < a.D) {
-                Slice<T>::load(a.x, at + c, u + k * V);
-                Slice<T>::load(a.dy, at + c, dy + k * V);
-                count = (k + 1) * V;
+                rx[k] = Slice<T>::load(a.x, r * a.D + c);
+                ry[k] = Slice<T>::load(a.dy, r * a.D + c);
+                if (a.dsum) rs[k] = Slice<T>::load(a.dsum, r * a.D + c);
+            }
+        }
+    };
+    if (AHEAD && row < a.rows) fetch(row);
+    for (; row < a.rows; row += step) {
+        const int64_t at = row * a.D;
+        float u[K * V], dy[K * V];
+        u32x4 ds[K];
+        if (!AHEAD) fetch(row);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * L + l) * V;
+            if (c < a.D) {
+                Slice<T>::unpack(rx[k], u + k * V);
+                Slice<T>::unpack(ry[k], dy + k * V);
+                if (a.dsum) ds[k] = rs[k];
             } else {
 #pragma unroll
                 for (int v = 0; v < V; ++v) u[k * V + v] = dy[k * V + v] = 0.f;
             }
         }
+        if (AHEAD && row + step < a.rows) fetch(row + step);
         const Stats s = row_stats<L, K * V>(u, count, a.D, a.eps);
         float two[2] = {0.f, 0.f};  // sums of t and t n
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = (k * L + l) * V;
-            if (c < a.D) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const int i = k * V + v;
-                    u[i] = ((u[i] - s.mean) - s.rest) * s.rho;
-                    dw[i] = fmaf(dy[i], u[i], dw[i]);
-                    db[i] += dy[i];
-                    dy[i] *= a.weight[c + v];
-                    two[0] += dy[i];
-                    two[1] = fmaf(dy[i], u[i], two[1]);
-                }
-            }
+        for (int i = 0; i < K * V; ++i) {
+            u[i] = i < count ? ((u[i] - s.mean) - s.rest) * s.rho : 0.f;
+            dw[i] = fmaf(dy[i], u[i], dw[i]);
+            db[i] += dy[i];
+            if constexpr (AHEAD) dy[i] *= wt[i];
+            else dy[i] *= i < count ? a.weight[(i / V * L + l) * V + i % V] : 0.f;
+            two[0] += dy[i];
+            two[1] = fmaf(dy[i], u[i], two[1]);
         }
-        row_sums<L, 2>(two);
+        row_sums<L, 2>(two, red_t);
         const float mt = two[0] * inv, mtn = two[1] * inv, rho = s.rho;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (k * L + l) * V;
             if (c < a.D) {
-                float dx[V], ds[V];
-                if (a.dsum) Slice<T>::load(a.dsum, at + c, ds);
+                float dx[V], d[V];
+                if (a.dsum) Slice<T>::unpack(ds[k], d);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     const int i = k * V + v;
                     dx[v] = rho * (dy[i] - mt - u[i] * mtn) * s.scale;
-                    if (a.dsum) dx[v] += ds[v];
+                    if (a.dsum) dx[v] += d[v];
                 }
                 Slice<T>::store(a.dx, at + c, dx);
             }
@@ -250,21 +305,23 @@ __global__ __launch_bounds__(L > LN_THREADS ? L : LN_THREADS) void layer_norm_bw
     }
 }
 
-// a workgroup for 8 channels of dweight or dbias
+// a workgroup for 32 channels of dweight or dbias
 __global__ __launch_bounds__(256) void layer_norm_sum_kernel(LayerNormArgs a) {
-    const int which = blockIdx.x % 2, c = blockIdx.x / 2 * 8 + threadIdx.x % 8;
+    const int which = blockIdx.x % 2, c = blockIdx.x / 2 * 32 + threadIdx.x % 32;
     if (which && !a.dbias) return;
-    const double s = sum_columns(a.part + (int64_t)which * a.D + c, a.groups, (int64_t)2 * a.D);
-    if (threadIdx.x < 8) (which ? a.dbias : a.dweight)[c] = (float)s;
+    const double s = sum_columns(a.part + (int64_t)which * a.D + min(c, a.D - 1), a.groups, (int64_t)2 * a.D);
+    if (threadIdx.x < 32 && c < a.D) (which ? a.dbias : a.dweight)[c] = (float)s;
 }
 
 namespace {
 
-// Lanes of a row and slices in each: the fewest lanes up to a wave, then two and four
-// slices a lane, then more waves.
-template <class F>
-void by_row(int slices, F&& f) {
+// Lanes of a row and slices in each: the fewest lanes up to a wave, then two slices a lane,
+// then more waves.
+template <class T, class F>
+void by_row(int32_t D, F&& rows) {
     using std::integral_constant;
+    const int slices = D / Slice<T>::N;
+    const auto f = [&](auto l, auto k) { rows(T{}, l, k); };
     if (slices <= 8) f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
     else if (slices <= 16) f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
     else if (slices <= 32) f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
@@ -272,35 +329,44 @@ void by_row(int slices, F&& f) {
     else if (slices <= 128) f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
     else if (slices <= 256) f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
     else if (slices <= 512) f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-    else if (slices <= 1024) f(integral_constant<int, 256>{}, integral_constant<int, 4>{});
-    else if (slices <= 2048) f(integral_constant<int, 512>{}, integral_constant<int, 4>{});
-    else f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
+    else if (slices <= 1024) f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+    else if (slices <= 2048) f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+    else if constexpr (sizeof(T) == 4) f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
 }
 
 template <class F>
 void by_type_and_row(bool fp32, int32_t D, F&& f) {
-    if (fp32) by_row(D / Slice<float>::N, [&](auto l, auto k) { f(float{}, l, k); });
-    else by_row(D / Slice<uint16_t>::N, [&](auto l, auto k) { f(uint16_t{}, l, k); });
+    if (fp32) by_row<float>(D, f);
+    else by_row<uint16_t>(D, f);
 }
 
 constexpr int threads_of(int L) { return L > LN_THREADS ? L : LN_THREADS; }
 
-}  // namespace
-
-int32_t layer_norm_groups(int64_t rows, int32_t D, bool fp32) {
+// Workgroups: as many as are in flight at once, `waves` of them on each CU.
+#ifndef LN_FWD_WAVES
+#define LN_FWD_WAVES 16
+#define LN_BWD_WAVES 8
+#endif
+int32_t groups_of(int64_t rows, int32_t D, bool fp32, int waves) {
     int64_t g = 1;
     by_type_and_row(fp32, D, [&](auto, auto l, auto) {
-        constexpr int per = threads_of(decltype(l)::value) / decltype(l)::value;
-        g = (rows + per - 1) / per;
+        constexpr int L = decltype(l)::value, per = threads_of(L) / L;
+        g = std::min<int64_t>((rows + per - 1) / per, std::max(1, waves * 64 / threads_of(L)) * 256);
     });
-    return (int32_t)(g < 1 ? 1 : g > LN_GROUPS ? LN_GROUPS : g);
+    return (int32_t)std::max<int64_t>(g, 1);
 }
 
-void launch_layer_norm_fwd(const LayerNormArgs& a, bool fp32, hipStream_t stream) {
+}  // namespace
+
+int32_t layer_norm_groups(int64_t rows, int32_t D, bool fp32) { return groups_of(rows, D, fp32, LN_BWD_WAVES); }
+
+void launch_layer_norm_fwd(const LayerNormArgs& args, bool fp32, hipStream_t stream) {
+    LayerNormArgs a = args;
+    a.groups = groups_of(a.rows, a.D, fp32, LN_FWD_WAVES);
     by_type_and_row(fp32, a.D, [&](auto t, auto l, auto k) {
-        constexpr int L = decltype(l)::value, THREADS = threads_of(L), RPW = THREADS / L;
-        hipLaunchKernelGGL((layer_norm_fwd_kernel<decltype(t), L, decltype(k)::value>),
-                           wide_grid((a.rows + RPW - 1) / RPW, THREADS), dim3(THREADS), 0, stream, a);
+        constexpr int L = decltype(l)::value;
+        hipLaunchKernelGGL((layer_norm_fwd_kernel<decltype(t), L, decltype(k)::value>), dim3((unsigned)a.groups),
+                           dim3(threads_of(L)), 0, stream, a);
     });
 }
 
@@ -310,7 +376,7 @@ void launch_layer_norm_bwd(const LayerNormArgs& a, bool fp32, hipStream_t stream
         hipLaunchKernelGGL((layer_norm_bwd_kernel<decltype(t), L, decltype(k)::value>), dim3((unsigned)a.groups),
                            dim3(threads_of(L)), 0, stream, a);
     });
-    hipLaunchKernelGGL(layer_norm_sum_kernel, dim3((unsigned)(a.D / 4)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(layer_norm_sum_kernel, dim3((unsigned)((a.D + 31) / 32 * 2)), dim3(256), 0, stream, a);
 }
 
 }  // namespace kda

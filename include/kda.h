@@ -596,7 +596,7 @@ int short_conv_fwd(const void* x, const float* weight, const float* bias, int32_
  * (NULL: zero): dx [B, T, C] tokens, dweight [C, W], dbias [C] (NULL only without
  * a bias), dh0 [N, W - 1, C] tokens or NULL (not written).  No result of the
  * forward call is needed. */
-size_t short_conv_bwd_workspace_size(int32_t B, int32_t T, int32_t C, int32_t W);
+size_t short_conv_bwd_workspace_size(int32_t dtype, int32_t B, int32_t T, int32_t C, int32_t W);
 
 int short_conv_bwd(const void* x, const float* weight, const float* bias, int32_t activation,
                    const void* initial_state, const int32_t* cu_seqlens, int32_t num_seqs,

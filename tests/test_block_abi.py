@@ -132,13 +132,13 @@ def test_sizes(lib):
     for bad in ((0, 1, 64), (1, -1, 64), (1, 1, 12), (1, 1, (1 << 20) + 8), (1 << 16, 1 << 15, 64)):
         assert lib.gated_scan_states(*bad) == -1
         assert kda.gated_scan_workspace_size(*bad) == kda.gated_scan_workspace_size(*bad, backward=True) == 0
-        assert lib.short_conv_bwd_workspace_size(*bad, 4) == 0
+        assert lib.short_conv_bwd_workspace_size(0, *bad, 4) == 0
     # more tiles than tickets: 2^24 of 64 tokens, 2^7 blocks of 64 channels
     assert lib.gated_scan_states(1 << 24, 64, 1 << 13) == -1
     assert kda.gated_scan_workspace_size(1 << 24, 64, 1 << 13) == 0
     assert lib.gated_scan_states((1 << 24) - 1, 64, 1 << 13) == ((1 << 24) - 1) << 13
     assert kda.gated_scan_workspace_size(2, 100, 64) >= 256
-    assert lib.short_conv_bwd_workspace_size(1, 1, 64, 5) == 0
+    assert lib.short_conv_bwd_workspace_size(0, 1, 1, 64, 5) == lib.short_conv_bwd_workspace_size(2, 1, 1, 64, 4) == 0
     assert lib.layer_norm_bwd_workspace_size(0, 5, 12) == lib.layer_norm_bwd_workspace_size(3, 5, 64) == 0
     assert lib.layer_norm_bwd_workspace_size(0, 1 << 31, 64) == lib.layer_norm_bwd_workspace_size(1, 5, 16392) == 0
 
