@@ -45,18 +45,19 @@ bool countable_tiles(int32_t B, int32_t T, int32_t C) {
     return (int64_t)B * scan_states(T) * ((C + 63) / 64) < I31;
 }
 
-// Workspace of the recurrence: the tiles' words and the ticket, a packed batch's marks
+// Workspace of the recurrence: the counters and words of the tiles, a packed batch's marks
 // and sequences, and for the gradients the tiles' sums.  One row of a batch may be packed
 // or not.
 struct ScanSpace {
-    size_t ticket, words, marks, seq, part, total;
+    size_t tickets, words, marks, seq, part, total;
 };
 
 ScanSpace scan_space(int32_t B, int32_t T, int32_t C, bool backward) {
     const size_t groups = ((size_t)T + 15) / 16;
     ScanSpace s{};
-    s.ticket = 0;
-    s.words = ALIGN;
+    s.tickets = 0;
+    s.words = align_up((size_t)std::min<int64_t>((int64_t)B * ((C + 63) / 64), kda::GS_MAX_COUNTERS) *
+                       kda::GS_TICKET_BYTES);
     s.marks = s.words + align_up((size_t)B * scan_states(T) * C * sizeof(uint64_t));
     s.seq = s.marks + (B == 1 ? align_up(groups * sizeof(uint2)) : 0);
     s.part = s.seq + (B == 1 ? align_up(groups * 16 * sizeof(int32_t)) : 0);
@@ -96,7 +97,7 @@ kda::ScanArgs scan_args(const void* x, const void* g, const void* gate, const fl
     a.C = C;
     a.N = cu ? num_seqs : B;
     a.n_states = scan_states(T);
-    a.ticket = reinterpret_cast<uint32_t*>(ws + sp.ticket);
+    a.tickets = reinterpret_cast<uint32_t*>(ws + sp.tickets);
     a.words = reinterpret_cast<uint64_t*>(ws + sp.words);
     a.marks = reinterpret_cast<uint2*>(ws + sp.marks);
     a.seq = reinterpret_cast<int32_t*>(ws + sp.seq);

@@ -14,6 +14,8 @@ namespace kda {
 // The recurrence's tiles are 128 tokens of a row of the batch in the forward pass and 64
 // in the backward pass; the forward pass keeps the state that enters every 64th token.
 constexpr int GS_STATES = 64;
+constexpr int GS_TICKET_BYTES = 64;  // counters do not share a line
+constexpr int GS_MAX_COUNTERS = 2048;
 
 struct ScanArgs {
     const void* x;          // [B, T, C] tokens
@@ -28,10 +30,12 @@ struct ScanArgs {
     int32_t n_states;       // of a row of the batch
     void* o;                // [B, T, C] tokens
     float* states;          // [B, n_states, C] (forward: or null)
-    // what the tiles of a chain post for those behind them, and the next tile to be taken
+    // what the tiles of a chain post for those behind them, and counters of tiles taken
     // (neither is used where a row is one tile)
     uint64_t* words;        // [tiles, B, C]
-    uint32_t* ticket;
+    int32_t far;            // whether a tile looks at 32 before it, not 8 (enter_tile)
+    int32_t beside;         // chains of a counter
+    uint32_t* tickets;      // the counters, GS_TICKET_BYTES apart
     // packed batches: per 16 tokens, whether each begins a sequence,
     // belongs to one, ends one; per token, which
     uint2* marks;           // [ceil(T / 16)]

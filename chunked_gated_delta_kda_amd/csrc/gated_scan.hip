@@ -24,6 +24,7 @@ namespace {
 
 constexpr int GS_WAVES = 8;
 constexpr int GS_THREADS = 64 * GS_WAVES;
+constexpr int TICKET_WORDS = GS_TICKET_BYTES / 4;
 constexpr int FWD_STEPS = 16, BWD_STEPS = 8;  // tokens of a wave
 constexpr int FWD_TILE = GS_WAVES * FWD_STEPS, BWD_TILE = GS_WAVES * BWD_STEPS;
 static_assert(BWD_TILE == GS_STATES && FWD_TILE == 2 * GS_STATES, "the states kept are those entering a BWD_TILE");
@@ -88,13 +89,53 @@ __device__ __forceinline__ void post(uint64_t* p, float prod, float sum) {
 __device__ __forceinline__ float word_prod(uint64_t w) { return __uint_as_float((uint32_t)w); }
 __device__ __forceinline__ float word_sum(uint64_t w) { return __uint_as_float((uint32_t)(w >> 32)); }
 
+// Waits until the tiles back, back + GS_WAVES, ... (n of them) before the one that posts at
+// `own` have posted, and tile `state` before it even knows the state behind it.  The number
+// of looks is bounded all the same: a workspace that someone else writes to gives NaN, not
+// a hang.
+template <int V, int n>
+__device__ __forceinline__ void await_words(const uint64_t* own, int64_t step, int order, int back, int state,
+                                            int lane, uint64_t (*look)[64 * V]) {
+    uint64_t word[n][V];
+    for (int looks = 0;; ++looks) {
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                word[i][v] = __hip_atomic_load(own + v - (1 + min(back + i * GS_WAVES, order - 1)) * step,
+                                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        bool ready = true;
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                ready = ready && (back + i * GS_WAVES == state ? word_prod(word[i][v]) == 0.f
+                                                              : (uint32_t)word[i][v] != (uint32_t)EMPTY);
+        if (__all(ready)) break;
+        if (looks == 1 << 20) {
+#pragma unroll
+            for (int i = 0; i < n; ++i)
+#pragma unroll
+                for (int v = 0; v < V; ++v) word[i][v] = 0x7fc00000ull << 32;
+            break;
+        }
+        __builtin_amdgcn_s_sleep(1);
+    }
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) look[back + i * GS_WAVES][lane * V + v] = word[i][v];
+}
+
 // The state that enters tile `order` of a chain (0: `first`), whose own product and sum
-// are (prod, sum) in the last wave.  Wave w waits for the word of the tile w + 1 before
-// this one, the last wave until that word is a state; folded from the oldest on, this is
-// the same sum in the same order whatever each tile had posted by then, so bits do not
-// depend on time.  A tile waits only for tiles whose tickets were drawn before its own:
-// those run already and wait for earlier ones in turn.  The number of looks is bounded
-// all the same (a workspace that someone else writes to gives NaN, not a hang).
+// are (prod, sum) in the last wave.  The words of the eight tiles before this one are
+// looked at first, one by each wave; where none is a state in all channels, those of the
+// next 24, of which the oldest is waited for until it is one.  Folded from the oldest on,
+// this is the same sum in the same order whatever each tile had posted by then: bits do
+// not depend on time.  A tile waits only for tiles whose tickets were drawn before
+// its own: those run already, and wait for earlier ones in turn.
+constexpr int NEAR = GS_WAVES, FAR = 4 * GS_WAVES;
+
 template <int V>
 __device__ __forceinline__ void enter_tile(const ScanArgs& a, int tiles, int order, int64_t column, bool active, int w, int lane,
                                            const float (&prod)[V], const float (&sum)[V], const float (&first)[V],
@@ -110,37 +151,36 @@ __device__ __forceinline__ void enter_tile(const ScanArgs& a, int tiles, int ord
 #pragma unroll
             for (int v = 0; v < V; ++v) post(own + v, prod[v], sum[v]);
         }
-        if (w < order) {
-            const uint64_t* p = a.words + (order - 1 - w) * step + column;
-            uint64_t word[V];
-            for (int looks = 0;; ++looks) {
-                bool ready = true;
+        const auto fold = [&](int from) {
+            for (int j = from; j >= 0; --j) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    word[v] = __hip_atomic_load(p + v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                    ready = ready && (w == GS_WAVES - 1 ? word_prod(word[v]) == 0.f : (uint32_t)word[v] != (uint32_t)EMPTY);
+                    const uint64_t t = look[j][lane * V + v];
+                    in[v] = carry(word_prod(t), word_sum(t), in[v]);
                 }
-                if (__all(ready)) break;
-                if (looks == 1 << 20) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) word[v] = 0x7fc00000ull << 32;
-                    break;
-                }
-                __builtin_amdgcn_s_sleep(1);
             }
-#pragma unroll
-            for (int v = 0; v < V; ++v) look[w][lane * V + v] = word[v];
-        }
+        };
+        await_words<V, 1>(own, step, order, w, a.far ? -1 : NEAR - 1, lane, look);
         __syncthreads();
-#pragma unroll
-        for (int v = 0; v < V; ++v) in[v] = 0.f;
-        for (int j = min(order, GS_WAVES) - 1; j >= 0; --j) {
+        int from = min(order, NEAR) - 1;
+        if (a.far && order > NEAR) {
+            bool state = true;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const uint64_t t = look[j][lane * V + v];
-                in[v] = carry(word_prod(t), word_sum(t), in[v]);
+                bool some = false;
+#pragma unroll
+                for (int j = 0; j < NEAR; ++j) some = some || word_prod(look[j][lane * V + v]) == 0.f;
+                state = state && some;
+            }
+            if (!__all(state)) {  // (the same words in every wave)
+                await_words<V, FAR / NEAR - 1>(own, step, order, w + NEAR, FAR - 1, lane, look);
+                __syncthreads();
+                from = min(order, FAR) - 1;
             }
         }
+#pragma unroll
+        for (int v = 0; v < V; ++v) in[v] = 0.f;
+        fold(from);
     }
     if (poster && order + 1 < tiles) {
 #pragma unroll
@@ -168,14 +208,14 @@ struct Marks {
 
 }  // namespace
 
-// What a pass needs before it: words that are empty and a first ticket; of a packed batch
+// What a pass needs before it: words that are empty and tickets that are not drawn; of a packed batch
 // which sequence each token belongs to and which tokens begin and end one; and for the
 // sequences without a token, the state behind them (dst = src, or zeros).  Workgroups
 // [0, fill) have the words, the next `marks` the tokens, the others a sequence each.
 struct PrepareArgs {
     ScanArgs a;
     int64_t fill, marks;
-    int64_t n_words;
+    int64_t n_words, n_tickets;
     const float* src;
     float* dst;
 };
@@ -184,13 +224,14 @@ __global__ __launch_bounds__(256) void gated_scan_prepare_kernel(PrepareArgs q) 
     const ScanArgs& a = q.a;
     int64_t wg = (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
     if (wg < q.fill) {
-        // (8 words a thread, 2 at a time; their number is a multiple of 8)
+        // (8 words a thread, 2 at a time; their number is a multiple of 8.  There are more
+        // threads than tickets.)
         const int64_t first = wg * 2048 + threadIdx.x * 2;
+        if (wg * 256 + threadIdx.x < q.n_tickets) a.tickets[(wg * 256 + threadIdx.x) * TICKET_WORDS] = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (first + i * 512 < q.n_words)
                 *reinterpret_cast<u32x4*>(a.words + first + i * 512) = u32x4{~0u, ~0u, ~0u, ~0u};
-        if (wg == 0 && threadIdx.x == 0) *a.ticket = 0;
         return;
     }
     wg -= q.fill;
@@ -225,28 +266,39 @@ __global__ __launch_bounds__(256) void gated_scan_prepare_kernel(PrepareArgs q) 
     for (int c = threadIdx.x; c < a.C; c += 256) q.dst[n * a.C + c] = q.src ? q.src[n * a.C + c] : 0.f;
 }
 
-// The ticket of this workgroup: tiles are taken in the order of time, those of all chains
-// (a row of the batch, a block of channels) side by side.
-__device__ __forceinline__ int64_t draw(const ScanArgs& a, int tiles) {
-    __shared__ uint32_t ticket;
-    if (tiles == 1) return (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
-    if (threadIdx.x == 0) ticket = atomicAdd(a.ticket, 1u);
-    __syncthreads();
-    return ticket;
-}
+// The tile that this workgroup takes.  A counter has the tiles of a.beside chains (a row of
+// the batch and a block of channels) side by side, in the order of time; workgroup i draws
+// from counter i % counters, as many from each as it has tiles.
+struct Place {
+    int64_t chain;
+    int order;
+    __device__ __forceinline__ Place(const ScanArgs& a, int tiles, int64_t chains) {
+        __shared__ uint32_t ticket;
+        const int64_t wg = (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
+        if (tiles == 1 || wg >= chains * tiles) {
+            chain = wg % chains;
+            order = (int)(wg / chains);
+            return;
+        }
+        const int64_t counters = chains / a.beside, counter = wg % counters;
+        if (threadIdx.x == 0) ticket = atomicAdd(a.tickets + counter * TICKET_WORDS, 1u);
+        __syncthreads();
+        chain = counter * a.beside + ticket % a.beside;
+        order = ticket / a.beside;
+    }
+};
 
 template <class T, bool PACKED>
 __global__ __launch_bounds__(GS_THREADS, 4) void gated_scan_fwd_kernel(ScanArgs a) {
     constexpr int V = Word<T>::N, CB = 64 * V;
     __shared__ float s_prod[GS_WAVES][CB], s_sum[GS_WAVES][CB];
-    __shared__ uint64_t look[GS_WAVES][CB];
+    __shared__ uint64_t look[FAR][CB];
     const int tiles = tiles_of(a.T, FWD_TILE);
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int blocks = (a.C + CB - 1) / CB;
-    const int64_t chains = (int64_t)a.B * blocks, ticket = draw(a, tiles);
-    if (ticket >= chains * tiles) return;
-    const int k = (int)(ticket / chains), chain = (int)(ticket % chains);
-    const int b = chain / blocks, cb = chain % blocks;
+    const Place place(a, tiles, (int64_t)a.B * blocks);
+    const int k = place.order, b = (int)(place.chain / blocks), cb = (int)(place.chain % blocks);
+    if (k >= tiles) return;
     const int own = cb * CB + lane * V;
     const bool active = own < a.C;
     const int c = active ? own : a.C - V;
@@ -357,15 +409,14 @@ __global__ __launch_bounds__(GS_THREADS, 4) void gated_scan_bwd_kernel(ScanArgs 
     constexpr int V = Word<T>::N, CB = 64 * V;
     __shared__ float s_prod[GS_WAVES][CB], s_sum[GS_WAVES][CB];    // states, forwards
     __shared__ float s_bprod[GS_WAVES][CB], s_bsum[GS_WAVES][CB];  // gradients, backwards
-    __shared__ uint64_t look[GS_WAVES][CB];
+    __shared__ uint64_t look[FAR][CB];
     const int tiles = tiles_of(a.T, BWD_TILE);
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int blocks = (a.C + CB - 1) / CB;
-    const int64_t chains = (int64_t)a.B * blocks, ticket = draw(a, tiles);
-    if (ticket >= chains * tiles) return;
-    const int order = (int)(ticket / chains), chain = (int)(ticket % chains);
-    const int k = tiles - 1 - order;
-    const int b = chain / blocks, cb = chain % blocks;
+    const Place place(a, tiles, (int64_t)a.B * blocks);
+    const int order = place.order, k = tiles - 1 - order;
+    const int b = (int)(place.chain / blocks), cb = (int)(place.chain % blocks);
+    if (k < 0) return;
     const int own = cb * CB + lane * V;
     const bool active = own < a.C;
     const int c = active ? own : a.C - V;
@@ -608,16 +659,33 @@ __global__ __launch_bounds__(256) void gated_scan_decode_kernel(ScanDecodeArgs a
 
 namespace {
 
-void launch_prepare(const ScanArgs& a, int tiles, const float* src, float* dst, hipStream_t stream) {
+int64_t chains_of(const ScanArgs& a, bool fp32) {
+    const int per = 64 * (fp32 ? Word<float>::N : Word<uint16_t>::N);
+    return (int64_t)a.B * ((a.C + per - 1) / per);
+}
+
+void launch_prepare(const ScanArgs& a, int tiles, int64_t chains, const float* src, float* dst, hipStream_t stream) {
     PrepareArgs q{};
     q.a = a;
     q.n_words = tiles > 1 ? (int64_t)tiles * a.B * a.C : 0;
+    q.n_tickets = tiles > 1 ? chains / a.beside : 0;
     q.fill = (q.n_words + 2047) / 2048;
     q.marks = a.cu ? ((int64_t)a.T + 255) / 256 : 0;
     q.src = src;
     q.dst = a.cu || a.T == 0 ? dst : nullptr;
     const int64_t groups = q.fill + q.marks + (q.dst ? a.N : 0);
     if (groups) hipLaunchKernelGGL(gated_scan_prepare_kernel, wide_grid(groups, 256), dim3(256), 0, stream, q);
+}
+
+#ifndef FAR_GROUPS
+#define FAR_GROUPS GS_MAX_COUNTERS
+#define OWN_GROUPS GS_MAX_COUNTERS
+#endif
+int64_t set_chains(ScanArgs& a, int tiles, bool fp32) {
+    const int64_t chains = chains_of(a, fp32);
+    a.far = chains * tiles <= FAR_GROUPS;
+    a.beside = chains * tiles <= OWN_GROUPS ? 1 : (int32_t)chains;
+    return chains;
 }
 
 template <class F>
@@ -628,28 +696,30 @@ void by_type(bool fp32, bool packed, F&& f) {
 
 }  // namespace
 
-void launch_gated_scan_fwd(const ScanArgs& a, bool fp32, hipStream_t stream) {
+void launch_gated_scan_fwd(const ScanArgs& args, bool fp32, hipStream_t stream) {
+    ScanArgs a = args;
     const int tiles = tiles_of(a.T, FWD_TILE);
-    launch_prepare(a, tiles, a.h0, a.h_final, stream);
+    const int64_t chains = set_chains(a, tiles, fp32);
+    launch_prepare(a, tiles, chains, a.h0, a.h_final, stream);
     if (a.T == 0) return;
     by_type(fp32, a.cu != nullptr, [&](auto t, auto packed) {
         using T = decltype(t);
-        constexpr int CB = 64 * Word<T>::N;
         hipLaunchKernelGGL((gated_scan_fwd_kernel<T, decltype(packed)::value>),
-                           wide_grid((int64_t)a.B * tiles * ((a.C + CB - 1) / CB), GS_THREADS), dim3(GS_THREADS), 0,
+                           wide_grid(chains * tiles, GS_THREADS), dim3(GS_THREADS), 0,
                            stream, a);
     });
 }
 
-void launch_gated_scan_bwd(const ScanArgs& a, bool fp32, hipStream_t stream) {
+void launch_gated_scan_bwd(const ScanArgs& args, bool fp32, hipStream_t stream) {
+    ScanArgs a = args;
     const int tiles = tiles_of(a.T, BWD_TILE);
-    launch_prepare(a, tiles, a.d_final, a.dh0, stream);
+    const int64_t chains = set_chains(a, tiles, fp32);
+    launch_prepare(a, tiles, chains, a.d_final, a.dh0, stream);
     if (a.T > 0) {
         by_type(fp32, a.cu != nullptr, [&](auto t, auto packed) {
             using T = decltype(t);
-            constexpr int CB = 64 * Word<T>::N;
-            hipLaunchKernelGGL((gated_scan_bwd_kernel<T, decltype(packed)::value>),
-                               wide_grid((int64_t)a.B * tiles * ((a.C + CB - 1) / CB), GS_THREADS),
+                hipLaunchKernelGGL((gated_scan_bwd_kernel<T, decltype(packed)::value>),
+                               wide_grid(chains * tiles, GS_THREADS),
                                dim3(GS_THREADS), 0, stream, a);
         });
     }
