@@ -22,6 +22,10 @@ namespace kda {
 
 namespace {
 
+#ifndef GS_FWD_OCC
+#define GS_FWD_OCC 8
+#define GS_BWD_OCC 6
+#endif
 constexpr int GS_WAVES = 8;
 constexpr int GS_THREADS = 64 * GS_WAVES;
 constexpr int TICKET_WORDS = GS_TICKET_BYTES / 4;
@@ -29,43 +33,51 @@ constexpr int FWD_STEPS = 16, BWD_STEPS = 8;  // tokens of a wave
 constexpr int FWD_TILE = GS_WAVES * FWD_STEPS, BWD_TILE = GS_WAVES * BWD_STEPS;
 static_assert(BWD_TILE == GS_STATES && FWD_TILE == 2 * GS_STATES, "the states kept are those entering a BWD_TILE");
 
-// The decay's gate for one element.  e = exp(-|z|), r = 1 / (1 + e) give
-// softplus(z) = max(z, 0) + log(1 + e) and sigmoid(z) = r or e r.  1 + e rounds
-// what a slow channel's decay is made of away: the lost part (e - (u - 1)) comes
-// back to first order.
+// The decay's gate for one element: L = amount softplus(z) and a = exp(-L), with
+// softplus(z) = max(z, 0) + log(1 + e), e = exp(-|z|).  1 + e rounds away what a slow
+// channel's decay is made of: the lost part (e - (u - 1)), below 2^-24, comes back times
+// 1 / u, for which 1 - e / 2 is near enough.
 struct Decay {
-    float L, a, sig;
+    float L, a;
+    __device__ __forceinline__ Decay() {}
     __device__ __forceinline__ Decay(float z, float amount) {
-        const float e = __builtin_amdgcn_exp2f(-LOG2E * fabsf(z));
-        const float u = 1.f + e, r = __builtin_amdgcn_rcpf(u);
-        const float log1p = fmaf(__builtin_amdgcn_logf(u), LN2, (e - (u - 1.f)) * r);
+        const float e = __builtin_amdgcn_exp2f(-LOG2E * fabsf(z)), u = 1.f + e;
+        const float log1p = fmaf(__builtin_amdgcn_logf(u), LN2, (e - (u - 1.f)) * fmaf(-0.5f, e, 1.f));
         L = amount * (fmaxf(z, 0.f) + log1p);
-        a = __builtin_amdgcn_exp2f(-LOG2E * L);
-        sig = z < 0.f ? e * r : r;
+        set_a();
+    }
+    __device__ __forceinline__ void set_a() { a = __builtin_amdgcn_exp2f(-LOG2E * L); }
+    // a is computed again from here on (kept, it would take the registers of a second
+    // workgroup)
+    __device__ __forceinline__ void again() {
+        asm volatile("" : "+v"(L));
+        set_a();
+    }
+    // 1 - a^2 = 1 - exp(-2 L): where a^2 is close to one by a polynomial for (1 - e^-t) / t,
+    // t <= 1/4 (8e-9 of it at most, fitted to the function), else from a
+    __device__ __forceinline__ float one_minus_square() const {
+        const float t = 2.f * L;
+        float s = 0.007510221563279629f;
+        s = fmaf(s, t, -0.041488952934741974f);
+        s = fmaf(s, t, 0.16665081679821014f);
+        s = fmaf(s, t, -0.4999994933605194f);
+        s = fmaf(s, t, 1.f);
+        return t < 0.25f ? s * t : fmaf(-a, a, 1.f);
     }
 };
 
-// 1 - a^2 = 1 - exp(-2 L): by its series where a^2 is close to one (the next term is
-// below 2^-26 of it), else from a.
-__device__ __forceinline__ float one_minus_square(float L, float a) {
-    const float t = 2.f * L;
-    float s = 1.f / 5040.f;
-    s = fmaf(s, -t, 1.f / 720.f);
-    s = fmaf(s, -t, 1.f / 120.f);
-    s = fmaf(s, -t, 1.f / 24.f);
-    s = fmaf(s, -t, 1.f / 6.f);
-    s = fmaf(s, -t, 0.5f);
-    s = fmaf(s, -t, 1.f);
-    return t < 0.25f ? s * t : fmaf(-a, a, 1.f);
+// sigmoid(z), which counts as zero below 2^-126
+__device__ __forceinline__ float sigmoid(float z) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-LOG2E * z));
 }
 
 // A gate on the input: s and s (1 - s).
 struct InputGate {
     float s, slope;
     __device__ __forceinline__ explicit InputGate(float i) {
-        const float e = __builtin_amdgcn_exp2f(-LOG2E * fabsf(i)), r = __builtin_amdgcn_rcpf(1.f + e);
-        s = i < 0.f ? e * r : r;
-        slope = e * r * r;
+        const float e = __builtin_amdgcn_exp2f(-LOG2E * fabsf(i)), r = __builtin_amdgcn_rcpf(1.f + e), er = e * r;
+        s = i < 0.f ? er : r;
+        slope = er * r;
     }
 };
 
@@ -93,105 +105,76 @@ __device__ __forceinline__ float word_sum(uint64_t w) { return __uint_as_float((
 // `own` have posted, and tile `state` before it even knows the state behind it.  The number
 // of looks is bounded all the same: a workspace that someone else writes to gives NaN, not
 // a hang.
-template <int V, int n>
+template <int n>
 __device__ __forceinline__ void await_words(const uint64_t* own, int64_t step, int order, int back, int state,
-                                            int lane, uint64_t (*look)[64 * V]) {
-    uint64_t word[n][V];
+                                            int lane, uint64_t (*look)[64]) {
+    uint64_t word[n];
     for (int looks = 0;; ++looks) {
 #pragma unroll
         for (int i = 0; i < n; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                word[i][v] = __hip_atomic_load(own + v - (1 + min(back + i * GS_WAVES, order - 1)) * step,
-                                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            word[i] = __hip_atomic_load(own - (1 + min(back + i * GS_WAVES, order - 1)) * step, __ATOMIC_RELAXED,
+                                        __HIP_MEMORY_SCOPE_AGENT);
         bool ready = true;
 #pragma unroll
         for (int i = 0; i < n; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                ready = ready && (back + i * GS_WAVES == state ? word_prod(word[i][v]) == 0.f
-                                                              : (uint32_t)word[i][v] != (uint32_t)EMPTY);
+            ready = ready && (back + i * GS_WAVES == state ? word_prod(word[i]) == 0.f
+                                                          : (uint32_t)word[i] != (uint32_t)EMPTY);
         if (__all(ready)) break;
         if (looks == 1 << 20) {
 #pragma unroll
-            for (int i = 0; i < n; ++i)
-#pragma unroll
-                for (int v = 0; v < V; ++v) word[i][v] = 0x7fc00000ull << 32;
+            for (int i = 0; i < n; ++i) word[i] = 0x7fc00000ull << 32;
             break;
         }
         __builtin_amdgcn_s_sleep(1);
     }
 #pragma unroll
-    for (int i = 0; i < n; ++i)
-#pragma unroll
-        for (int v = 0; v < V; ++v) look[back + i * GS_WAVES][lane * V + v] = word[i][v];
+    for (int i = 0; i < n; ++i) look[back + i * GS_WAVES][lane] = word[i];
 }
 
 // The state that enters tile `order` of a chain (0: `first`), whose own product and sum
 // are (prod, sum) in the last wave.  The words of the eight tiles before this one are
-// looked at first, one by each wave; where none is a state in all channels, those of the
-// next 24, of which the oldest is waited for until it is one.  Folded from the oldest on,
-// this is the same sum in the same order whatever each tile had posted by then: bits do
-// not depend on time.  A tile waits only for tiles whose tickets were drawn before
-// its own: those run already, and wait for earlier ones in turn.
+// looked at first, one by each wave, and the oldest is waited for until it is a state; on a
+// small grid (a.far), where none of the eight is a state in all channels, those of the next
+// 24, of which the oldest is waited for.  Folded from the oldest on, this is the same sum in
+// the same order whatever each tile had posted by then: bits do not depend on time.  A tile
+// waits only for tiles whose tickets were drawn before its own: those run already, and wait
+// for earlier ones in turn.
 constexpr int NEAR = GS_WAVES, FAR = 4 * GS_WAVES;
 
-template <int V>
-__device__ __forceinline__ void enter_tile(const ScanArgs& a, int tiles, int order, int64_t column, bool active, int w, int lane,
-                                           const float (&prod)[V], const float (&sum)[V], const float (&first)[V],
-                                           uint64_t (*look)[64 * V], float (&in)[V]) {
+__device__ __forceinline__ float enter_tile(const ScanArgs& a, int tiles, int order, int64_t column, bool active,
+                                            int w, int lane, float prod, float sum, float first,
+                                            uint64_t (*look)[64]) {
     const int64_t step = (int64_t)a.B * a.C;
     uint64_t* own = a.words + order * step + column;
     const bool poster = w == GS_WAVES - 1 && active;
-    if (order == 0) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) in[v] = first[v];
-    } else {
-        if (poster) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) post(own + v, prod[v], sum[v]);
-        }
-        const auto fold = [&](int from) {
-            for (int j = from; j >= 0; --j) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const uint64_t t = look[j][lane * V + v];
-                    in[v] = carry(word_prod(t), word_sum(t), in[v]);
-                }
-            }
-        };
-        await_words<V, 1>(own, step, order, w, a.far ? -1 : NEAR - 1, lane, look);
+    float in = first;
+    if (order > 0) {
+        if (poster) post(own, prod, sum);
+        await_words<1>(own, step, order, w, a.far ? -1 : NEAR - 1, lane, look);
         __syncthreads();
         int from = min(order, NEAR) - 1;
         if (a.far && order > NEAR) {
-            bool state = true;
+            bool state = false;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                bool some = false;
-#pragma unroll
-                for (int j = 0; j < NEAR; ++j) some = some || word_prod(look[j][lane * V + v]) == 0.f;
-                state = state && some;
-            }
+            for (int j = 0; j < NEAR; ++j) state = state || word_prod(look[j][lane]) == 0.f;
             if (!__all(state)) {  // (the same words in every wave)
-                await_words<V, FAR / NEAR - 1>(own, step, order, w + NEAR, FAR - 1, lane, look);
+                await_words<FAR / NEAR - 1>(own, step, order, w + NEAR, FAR - 1, lane, look);
                 __syncthreads();
                 from = min(order, FAR) - 1;
             }
         }
-#pragma unroll
-        for (int v = 0; v < V; ++v) in[v] = 0.f;
-        fold(from);
+        in = 0.f;
+        for (int j = from; j >= 0; --j) {
+            const uint64_t t = look[j][lane];
+            in = carry(word_prod(t), word_sum(t), in);
+        }
     }
-    if (poster && order + 1 < tiles) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) post(own + v, 0.f, carry(prod[v], sum[v], in[v]));
-    }
+    if (poster && order + 1 < tiles) post(own, 0.f, carry(prod, sum, in));
+    return in;
 }
 
-// The compiler takes v for another value from here on (and computes from it anew).
-__device__ __forceinline__ void forget(uint32_t& v) { asm volatile("" : "+v"(v)); }
-
-// What a wave knows of its place: its channels and, of a packed batch, its tokens.
+// Of a packed batch, what a wave knows of its tokens: which begin a sequence, belong to
+// one, end one.
 struct Marks {
     uint32_t start, in, last;
     __device__ __forceinline__ Marks() {}
@@ -205,6 +188,35 @@ struct Marks {
     }
     static __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 };
+
+// Rows of tokens from t0 on, one after the other: the offset in bytes of each from the
+// head of a token tensor, the last row's again behind it.
+struct RowWalk {
+    int64_t at;
+    int left;
+    uint32_t stride;
+    __device__ __forceinline__ RowWalk(const ScanArgs& a, int b, int t0, uint32_t row_bytes)
+        : at(((int64_t)b * a.T + min(t0, a.T - 1)) * row_bytes), left(a.T - 1 - t0), stride(row_bytes) {}
+    __device__ __forceinline__ void next() { at += left-- > 0 ? stride : 0u; }
+};
+// A channel of a token tensor: its bits, in a register of their own (held as 16 bits, the
+// compiler puts two into one as they arrive, and waits for it: 8% slower), and its value.
+template <class T>
+__device__ __forceinline__ uint32_t load_bits(const void* p, int64_t row, uint32_t lane_bytes) {
+    const T v = *reinterpret_cast<const T*>(static_cast<const char*>(p) + row + lane_bytes);
+    if constexpr (sizeof(T) == 2) return v;
+    else return __float_as_uint(v);
+}
+template <class T>
+__device__ __forceinline__ float value(uint32_t bits) {
+    return __uint_as_float(sizeof(T) == 2 ? bits << 16 : bits);
+}
+template <class T>
+__device__ __forceinline__ void store_one(void* p, int64_t row, uint32_t lane_bytes, float f) {
+    T* at = reinterpret_cast<T*>(static_cast<char*>(p) + row + lane_bytes);
+    if constexpr (sizeof(T) == 2) *at = __builtin_bit_cast(uint16_t, (bf16)f);
+    else *at = f;
+}
 
 }  // namespace
 
@@ -270,360 +282,255 @@ __global__ __launch_bounds__(256) void gated_scan_prepare_kernel(PrepareArgs q) 
 // the batch and a block of channels) side by side, in the order of time; workgroup i draws
 // from counter i % counters, as many from each as it has tiles.
 struct Place {
-    int64_t chain;
-    int order;
-    __device__ __forceinline__ Place(const ScanArgs& a, int tiles, int64_t chains) {
+    uint32_t chain, order;
+    __device__ __forceinline__ Place(const ScanArgs& a, uint32_t tiles, uint32_t chains) {
         __shared__ uint32_t ticket;
-        const int64_t wg = (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
+        const uint32_t wg = blockIdx.z * gridDim.x + blockIdx.x;  // (fewer than 2^31 have a tile)
         if (tiles == 1 || wg >= chains * tiles) {
             chain = wg % chains;
-            order = (int)(wg / chains);
+            order = wg / chains;
             return;
         }
-        const int64_t counters = chains / a.beside, counter = wg % counters;
+        const uint32_t counters = chains / a.beside, counter = wg % counters;
         if (threadIdx.x == 0) ticket = atomicAdd(a.tickets + counter * TICKET_WORDS, 1u);
         __syncthreads();
-        chain = counter * a.beside + ticket % a.beside;
-        order = ticket / a.beside;
+        const uint32_t mine = __builtin_amdgcn_readfirstlane(ticket);
+        chain = counter * a.beside + mine % a.beside;
+        order = mine / a.beside;
     }
 };
 
 template <class T, bool PACKED>
-__global__ __launch_bounds__(GS_THREADS, 4) void gated_scan_fwd_kernel(ScanArgs a) {
-    constexpr int V = Word<T>::N, CB = 64 * V;
-    __shared__ float s_prod[GS_WAVES][CB], s_sum[GS_WAVES][CB];
-    __shared__ uint64_t look[FAR][CB];
+__global__ __launch_bounds__(GS_THREADS, GS_FWD_OCC) void gated_scan_fwd_kernel(ScanArgs a) {
+    __shared__ float s_prod[GS_WAVES][64], s_sum[GS_WAVES][64];
+    __shared__ uint64_t look[FAR][64];
     const int tiles = tiles_of(a.T, FWD_TILE);
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int blocks = (a.C + CB - 1) / CB;
-    const Place place(a, tiles, (int64_t)a.B * blocks);
-    const int k = place.order, b = (int)(place.chain / blocks), cb = (int)(place.chain % blocks);
+    const uint32_t blocks = (a.C + 63) / 64;
+    const Place place(a, tiles, a.B * blocks);
+    const int k = place.order, b = place.chain / blocks, own = place.chain % blocks * 64 + lane;
     if (k >= tiles) return;
-    const int own = cb * CB + lane * V;
     const bool active = own < a.C;
-    const int c = active ? own : a.C - V;
-    float bias[V], amount[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        bias[v] = a.dt_bias[c + v];
-        amount[v] = expf(a.A_log[c + v]);
-    }
-    const int64_t row_words = a.C / V;
-    const int at = c / V;
+    const uint32_t c = active ? own : a.C - 1;
+    const uint32_t row_bytes = a.C * (uint32_t)sizeof(T), lane_bytes = c * (uint32_t)sizeof(T);
     const int t0 = k * FWD_TILE + w * FWD_STEPS;
     uint32_t rx[FWD_STEPS], rg[FWD_STEPS], ri[FWD_STEPS];
+    {
+        RowWalk row(a, b, t0, row_bytes);
 #pragma unroll
-    for (int t = 0; t < FWD_STEPS; ++t) {
-        const int64_t row = ((int64_t)b * a.T + min(t0 + t, a.T - 1)) * row_words;
-        rx[t] = (static_cast<const uint32_t*>(a.x) + row)[at];
-        rg[t] = (static_cast<const uint32_t*>(a.g) + row)[at];
-        ri[t] = (static_cast<const uint32_t*>(a.gate) + row)[at];
+        for (int t = 0; t < FWD_STEPS; ++t, row.next()) {
+            rx[t] = load_bits<T>(a.x, row.at, lane_bytes);
+            rg[t] = load_bits<T>(a.g, row.at, lane_bytes);
+            ri[t] = load_bits<T>(a.gate, row.at, lane_bytes);
+        }
     }
+    const float bias = a.dt_bias[c], amount = expf(a.A_log[c]);
     Marks m;
     if constexpr (PACKED) m = Marks(a, t0);
-    float prod[FWD_STEPS][V], sum[FWD_STEPS][V];
-    float p[V], h[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        p[v] = 1.f;
-        h[v] = 0.f;
-    }
+    // tokens that do not go on from the one before, and those behind the first such one
+    const uint32_t fresh = PACKED ? m.start | ~m.in : 0u;
+    const auto after_fresh = [&](int t) { return (fresh & ((2u << t) - 1)) != 0; };
+    // the sequence of token t, which has one, and its state
+    const auto sequence = [&](int t) { return (int64_t)(int)Marks::uniform(a.seq[t0 + t]); };
+    const auto state_of = [&](const float* p, int t) { return p ? p[sequence(t) * a.C + c] : 0.f; };
+    float prod[FWD_STEPS], sum[FWD_STEPS];
+    float p = 1.f, h = 0.f;
+    // (rows behind the last token of a batch of fixed length only follow: what is made of
+    // them goes nowhere)
 #pragma unroll
     for (int t = 0; t < FWD_STEPS; ++t) {
-        float x[V], g[V], i[V];
-        Word<T>::get(rx[t], x);
-        Word<T>::get(rg[t], g);
-        Word<T>::get(ri[t], i);
-        const bool there = PACKED ? (m.in >> t & 1) : t0 + t < a.T;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const Decay d(g[v] + bias[v], amount[v]);
-            const float in = __builtin_amdgcn_sqrtf(one_minus_square(d.L, d.a)) * InputGate(i[v]).s * x[v];
-            if constexpr (PACKED) {
-                if (m.start >> t & 1) {
-                    const float h0 = a.h0 ? a.h0[(int64_t)a.seq[t0 + t] * a.C + c + v] : 0.f;
-                    p[v] = 0.f;
-                    h[v] = fmaf(d.a, h0, in);
-                } else {
-                    p[v] = there ? p[v] * d.a : 0.f;
-                    h[v] = there ? fmaf(d.a, h[v], in) : 0.f;
-                }
-            } else {
-                p[v] = there ? p[v] * d.a : p[v];
-                h[v] = there ? fmaf(d.a, h[v], in) : h[v];
-            }
-            prod[t][v] = p[v];
-            sum[t][v] = h[v];
+        const Decay d(value<T>(rg[t]) + bias, amount);
+        const float in = __builtin_amdgcn_sqrtf(d.one_minus_square()) * sigmoid(value<T>(ri[t])) * value<T>(rx[t]);
+        if (PACKED && fresh >> t & 1) {
+            p = 0.f;
+            h = m.start >> t & 1 ? fmaf(d.a, state_of(a.h0, t), in) : 0.f;
+        } else {
+            p *= d.a;
+            h = fmaf(d.a, h, in);
         }
+        prod[t] = p;
+        sum[t] = h;
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        s_prod[w][lane * V + v] = p[v];
-        s_sum[w][lane * V + v] = h[v];
-    }
+    // behind a fresh token nothing of the state before it is left, whatever it and the
+    // decays are
+    if (PACKED && after_fresh(FWD_STEPS - 1)) p = 0.f;
+    s_prod[w][lane] = p;
+    s_sum[w][lane] = h;
     __syncthreads();
     // what the waves before this one make of the tile's state; the last wave's is the tile's
-    float bp[V], bs[V], first[V], in[V], enter[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        bp[v] = 1.f;
-        bs[v] = 0.f;
-        for (int j = 0; j < w; ++j) {
-            bs[v] = carry(s_prod[j][lane * V + v], s_sum[j][lane * V + v], bs[v]);
-            bp[v] = join(s_prod[j][lane * V + v], bp[v]);
-        }
-        first[v] = k == 0 && !PACKED && a.h0 ? a.h0[(int64_t)b * a.C + c + v] : 0.f;
-        h[v] = carry(p[v], h[v], bs[v]);
-        p[v] = join(p[v], bp[v]);
+    float bp = 1.f, bs = 0.f;
+    for (int j = 0; j < w; ++j) {
+        bs = carry(s_prod[j][lane], s_sum[j][lane], bs);
+        bp = join(s_prod[j][lane], bp);
     }
-    enter_tile<V>(a, tiles, k, (int64_t)b * a.C + c, active, w, lane, p, h, first, look, in);
+    const float first = k == 0 && !PACKED && a.h0 ? a.h0[(int64_t)b * a.C + c] : 0.f;
+    const float in = enter_tile(a, tiles, k, (int64_t)b * a.C + c, active, w, lane, join(p, bp), carry(p, h, bs), first,
+                                look);
+    if (!active) return;
+    const float enter = carry(bp, bs, in);
+    if (w % (GS_WAVES / 2) == 0 && a.states && t0 < a.T)
+        a.states[((int64_t)b * a.n_states + t0 / GS_STATES) * a.C + c] = enter;
+    RowWalk row(a, b, t0, row_bytes);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        enter[v] = carry(bp[v], bs[v], in[v]);
-        if (w % (GS_WAVES / 2) == 0 && a.states && active && t0 < a.T)
-            a.states[((int64_t)b * a.n_states + t0 / GS_STATES) * a.C + c + v] = enter[v];
-        if (!PACKED && w == GS_WAVES - 1 && a.h_final && k == tiles - 1 && active)
-            a.h_final[(int64_t)b * a.C + c + v] = carry(p[v], h[v], in[v]);
-    }
-#pragma unroll
-    for (int t = 0; t < FWD_STEPS; ++t) {
-        if (t0 + t >= a.T || !active) break;
-        float o[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if constexpr (PACKED) o[v] = m.in >> t & 1 ? carry(prod[t][v], sum[t][v], enter[v]) : 0.f;
-            else o[v] = fmaf(prod[t][v], enter[v], sum[t][v]);
+    for (int t = 0; t < FWD_STEPS; ++t, row.next()) {
+        if (t0 + t >= a.T) break;
+        const float o = PACKED && after_fresh(t) ? sum[t] : fmaf(prod[t], enter, sum[t]);
+        if (PACKED ? m.last >> t & 1 : t0 + t == a.T - 1) {
+            if (a.h_final) a.h_final[(PACKED ? sequence(t) : (int64_t)b) * a.C + c] = o;
         }
-        if constexpr (PACKED) {
-            if (a.h_final && m.last >> t & 1) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) a.h_final[(int64_t)a.seq[t0 + t] * a.C + c + v] = o[v];
-            }
-        }
-        (static_cast<uint32_t*>(a.o) + ((int64_t)b * a.T + t0 + t) * row_words)[at] = Word<T>::put(o);
+        store_one<T>(a.o, row.at, lane_bytes, o);
     }
 }
 
 template <class T, bool PACKED>
-__global__ __launch_bounds__(GS_THREADS, 4) void gated_scan_bwd_kernel(ScanArgs a) {
-    constexpr int V = Word<T>::N, CB = 64 * V;
-    __shared__ float s_prod[GS_WAVES][CB], s_sum[GS_WAVES][CB];    // states, forwards
-    __shared__ float s_bprod[GS_WAVES][CB], s_bsum[GS_WAVES][CB];  // gradients, backwards
-    __shared__ uint64_t look[FAR][CB];
+__global__ __launch_bounds__(GS_THREADS, GS_BWD_OCC) void gated_scan_bwd_kernel(ScanArgs a) {
+    __shared__ float s_prod[GS_WAVES][64], s_sum[GS_WAVES][64];    // states, forwards
+    __shared__ float s_bprod[GS_WAVES][64], s_bsum[GS_WAVES][64];  // gradients, backwards
+    __shared__ uint64_t look[FAR][64];
     const int tiles = tiles_of(a.T, BWD_TILE);
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int blocks = (a.C + CB - 1) / CB;
-    const Place place(a, tiles, (int64_t)a.B * blocks);
+    const uint32_t blocks = (a.C + 63) / 64;
+    const Place place(a, tiles, a.B * blocks);
     const int order = place.order, k = tiles - 1 - order;
-    const int b = (int)(place.chain / blocks), cb = (int)(place.chain % blocks);
+    const int b = place.chain / blocks, own = place.chain % blocks * 64 + lane;
     if (k < 0) return;
-    const int own = cb * CB + lane * V;
     const bool active = own < a.C;
-    const int c = active ? own : a.C - V;
-    const int64_t row_words = a.C / V;
-    const int at = c / V;
+    const uint32_t c = active ? own : a.C - 1;
+    const uint32_t row_bytes = a.C * (uint32_t)sizeof(T), lane_bytes = c * (uint32_t)sizeof(T);
     const int t0 = k * BWD_TILE + w * BWD_STEPS;
-    float bias[V], amount[V], enter[V];
+    uint32_t rx[BWD_STEPS], rg[BWD_STEPS], ri[BWD_STEPS], rd[BWD_STEPS];
+    {
+        RowWalk row(a, b, t0, row_bytes);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        bias[v] = a.dt_bias[c + v];
-        amount[v] = expf(a.A_log[c + v]);
-        enter[v] = a.states[((int64_t)b * a.n_states + k) * a.C + c + v];
+        for (int t = 0; t < BWD_STEPS; ++t, row.next()) {
+            rx[t] = load_bits<T>(a.x, row.at, lane_bytes);
+            rg[t] = load_bits<T>(a.g, row.at, lane_bytes);
+            ri[t] = load_bits<T>(a.gate, row.at, lane_bytes);
+            rd[t] = load_bits<T>(a.d_o, row.at, lane_bytes);
+        }
     }
+    const float bias = a.dt_bias[c], amount = expf(a.A_log[c]);
+    float enter = a.states[((int64_t)b * a.n_states + k) * a.C + c];
     Marks m;
     if constexpr (PACKED) m = Marks(a, t0);
-    const auto there = [&](int t) { return PACKED ? (m.in >> t & 1) != 0 : t0 + t < a.T; };
-    float dec[BWD_STEPS][V], prev[BWD_STEPS][V];
-    float p[V], h[V], q[V], e[V];
-    uint32_t rx[BWD_STEPS], rg[BWD_STEPS], ri[BWD_STEPS], rd[BWD_STEPS];
+    const uint32_t fresh = PACKED ? m.start | ~m.in : 0u;  // do not go on from the token before
+    const uint32_t ended = PACKED ? m.last | ~m.in : 0u;   // nor to the next one
+    const auto after_fresh = [&](int t) { return (fresh & ((2u << t) - 1)) != 0; };
+    const auto sequence = [&](int t) { return (int64_t)(int)Marks::uniform(a.seq[t0 + t]); };
+    const auto state_of = [&](const float* p, int t) { return p ? p[sequence(t) * a.C + c] : 0.f; };
+    if constexpr (!PACKED) {
+        // rows behind the last token: no decay (g = -infinity) and no gradient, so that
+        // what comes back passes them
 #pragma unroll
-    for (int t = 0; t < BWD_STEPS; ++t) {
-        const int64_t row = ((int64_t)b * a.T + min(t0 + t, a.T - 1)) * row_words;
-        rx[t] = (static_cast<const uint32_t*>(a.x) + row)[at];
-        rg[t] = (static_cast<const uint32_t*>(a.g) + row)[at];
-        ri[t] = (static_cast<const uint32_t*>(a.gate) + row)[at];
+        for (int t = 0; t < BWD_STEPS; ++t) {
+            if (t0 + t >= a.T) {
+                rg[t] = sizeof(T) == 2 ? 0xff80u : 0xff800000u;
+                rd[t] = 0;
+            }
+        }
     }
-#pragma unroll
-    for (int t = 0; t < BWD_STEPS; ++t) {
-        const int64_t row = ((int64_t)b * a.T + min(t0 + t, a.T - 1)) * row_words;
-        rd[t] = (static_cast<const uint32_t*>(a.d_o) + row)[at];
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        p[v] = q[v] = 1.f;
-        h[v] = e[v] = 0.f;
-    }
+    Decay dec[BWD_STEPS];
+    float prev[BWD_STEPS];
+    float p = 1.f, h = 0.f, q = 1.f, e = 0.f;
     // states from zero
 #pragma unroll
     for (int t = 0; t < BWD_STEPS; ++t) {
-        float x[V], g[V], i[V];
-        Word<T>::get(rx[t], x);
-        Word<T>::get(rg[t], g);
-        Word<T>::get(ri[t], i);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const Decay d(g[v] + bias[v], amount[v]);
-            const float in = __builtin_amdgcn_sqrtf(one_minus_square(d.L, d.a)) * InputGate(i[v]).s * x[v];
-            if constexpr (PACKED) {
-                if (m.start >> t & 1) {
-                    const float h0 = a.h0 ? a.h0[(int64_t)a.seq[t0 + t] * a.C + c + v] : 0.f;
-                    p[v] = 0.f;
-                    h[v] = fmaf(d.a, h0, in);
-                } else {
-                    p[v] = there(t) ? p[v] * d.a : 0.f;
-                    h[v] = there(t) ? fmaf(d.a, h[v], in) : 0.f;
-                }
-            } else {
-                p[v] = there(t) ? p[v] * d.a : p[v];
-                h[v] = there(t) ? fmaf(d.a, h[v], in) : h[v];
-            }
-            dec[t][v] = d.a;
-            prev[t][v] = h[v];
+        dec[t] = Decay(value<T>(rg[t]) + bias, amount);
+        const float in =
+            __builtin_amdgcn_sqrtf(dec[t].one_minus_square()) * sigmoid(value<T>(ri[t])) * value<T>(rx[t]);
+        if (PACKED && fresh >> t & 1) {
+            p = 0.f;
+            h = m.start >> t & 1 ? fmaf(dec[t].a, state_of(a.h0, t), in) : 0.f;
+        } else {
+            p *= dec[t].a;
+            h = fmaf(dec[t].a, h, in);
         }
+        prev[t] = h;
     }
-    // gradients of the states, from zero, last token first: what reaches the state
-    // before a token is a (do + what reaches its own)
+    // gradients of the states, from zero, last token first: what reaches the state before a
+    // token is a (do + what reaches its own)
 #pragma unroll
     for (int t = BWD_STEPS - 1; t >= 0; --t) {
-        float d[V];
-        Word<T>::get(rd[t], d);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if constexpr (PACKED) {
-                if (m.last >> t & 1) {
-                    const float df = a.d_final ? a.d_final[(int64_t)a.seq[t0 + t] * a.C + c + v] : 0.f;
-                    q[v] = 0.f;
-                    e[v] = dec[t][v] * (d[v] + df);
-                } else {
-                    q[v] = there(t) ? q[v] * dec[t][v] : 0.f;
-                    e[v] = there(t) ? dec[t][v] * (d[v] + e[v]) : 0.f;
-                }
-            } else {
-                q[v] = there(t) ? q[v] * dec[t][v] : q[v];
-                e[v] = there(t) ? dec[t][v] * (d[v] + e[v]) : e[v];
-            }
+        if (PACKED && ended >> t & 1) {
+            q = 0.f;
+            e = m.last >> t & 1 ? dec[t].a * (value<T>(rd[t]) + state_of(a.d_final, t)) : 0.f;
+        } else {
+            q *= dec[t].a;
+            e = dec[t].a * (value<T>(rd[t]) + e);
         }
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        s_prod[w][lane * V + v] = p[v];
-        s_sum[w][lane * V + v] = h[v];
-        s_bprod[w][lane * V + v] = q[v];
-        s_bsum[w][lane * V + v] = e[v];
-    }
+    if (PACKED && after_fresh(BWD_STEPS - 1)) p = 0.f;
+    if (PACKED && (ended & ((1u << BWD_STEPS) - 1))) q = 0.f;
+    s_prod[w][lane] = p;
+    s_sum[w][lane] = h;
+    s_bprod[w][lane] = q;
+    s_bsum[w][lane] = e;
     __syncthreads();
     // (the wave that posts a tile's word is the last: it folds all waves' gradients, the
     // others those behind them)
-    float bp[V], bs[V], tp[V], ts[V], first[V], in[V], back[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        for (int j = 0; j < w; ++j) enter[v] = carry(s_prod[j][lane * V + v], s_sum[j][lane * V + v], enter[v]);
-        bp[v] = tp[v] = 1.f;
-        bs[v] = ts[v] = 0.f;
-        for (int j = GS_WAVES - 1; j > w; --j) {
-            bs[v] = carry(s_bprod[j][lane * V + v], s_bsum[j][lane * V + v], bs[v]);
-            bp[v] = join(s_bprod[j][lane * V + v], bp[v]);
-        }
-        if (w == GS_WAVES - 1) {
-            for (int j = GS_WAVES - 1; j >= 0; --j) {
-                ts[v] = carry(s_bprod[j][lane * V + v], s_bsum[j][lane * V + v], ts[v]);
-                tp[v] = join(s_bprod[j][lane * V + v], tp[v]);
-            }
-        }
-        first[v] = order == 0 && !PACKED && a.d_final ? a.d_final[(int64_t)b * a.C + c + v] : 0.f;
+    for (int j = 0; j < w; ++j) enter = carry(s_prod[j][lane], s_sum[j][lane], enter);
+    float bp = 1.f, bs = 0.f;
+    const int until = w == GS_WAVES - 1 ? 0 : w + 1;
+    for (int j = GS_WAVES - 1; j >= until; --j) {
+        bs = carry(s_bprod[j][lane], s_bsum[j][lane], bs);
+        bp = join(s_bprod[j][lane], bp);
     }
-    enter_tile<V>(a, tiles, order, (int64_t)b * a.C + c, active, w, lane, tp, ts, first, look, in);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        back[v] = carry(bp[v], bs[v], in[v]);
-        if (!PACKED && w == GS_WAVES - 1 && a.dh0 && k == 0 && active)
-            a.dh0[(int64_t)b * a.C + c + v] = carry(tp[v], ts[v], in[v]);
-    }
-    // the state before each token, from what a zero state left after it
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        float prod = 1.f, before = enter[v];
+    const float first = order == 0 && !PACKED && a.d_final ? a.d_final[(int64_t)b * a.C + c] : 0.f;
+    const float in = enter_tile(a, tiles, order, (int64_t)b * a.C + c, active, w, lane, bp, bs, first, look);
+    float back = in;
+    if (w < GS_WAVES - 1) back = carry(bp, bs, in);
+    else if (!PACKED && a.dh0 && k == 0 && active) a.dh0[(int64_t)b * a.C + c] = carry(bp, bs, in);
+    // the state before each token, from what a zero state left behind it
+    {
+        float prod = 1.f, before = enter;
 #pragma unroll
         for (int t = 0; t < BWD_STEPS; ++t) {
-            const float after = prev[t][v];
-            prev[t][v] = before;
-            if constexpr (PACKED) {
-                if (m.start >> t & 1) {
-                    prev[t][v] = a.h0 ? a.h0[(int64_t)a.seq[t0 + t] * a.C + c + v] : 0.f;
-                    prod = 0.f;
-                }
-            }
-            prod *= dec[t][v];
-            before = carry(prod, after, enter[v]);
+            const float after = prev[t];
+            prev[t] = PACKED && (m.start >> t & 1) ? state_of(a.h0, t) : before;
+            dec[t].again();
+            prod *= dec[t].a;
+            before = PACKED && after_fresh(t) ? after : fmaf(prod, enter, after);
         }
     }
-    float dA[V], db[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) dA[v] = db[v] = 0.f;
-    // the gates are computed again: kept, they would take the registers of a second
-    // workgroup
-#pragma unroll
-    for (int t = 0; t < BWD_STEPS; ++t) {
-        forget(rx[t]);
-        forget(rg[t]);
-        forget(ri[t]);
-        forget(rd[t]);
-    }
+    float dA = 0.f, db = 0.f;
+    const int64_t head = ((int64_t)b * a.T + t0) * row_bytes;
 #pragma unroll
     for (int t = BWD_STEPS - 1; t >= 0; --t) {
-        float x[V], g[V], i[V], d_o[V], dx[V], dg[V], di[V];
-        Word<T>::get(rx[t], x);
-        Word<T>::get(rg[t], g);
-        Word<T>::get(ri[t], i);
-        Word<T>::get(rd[t], d_o);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if constexpr (PACKED) {
-                if (m.last >> t & 1) back[v] = a.d_final ? a.d_final[(int64_t)a.seq[t0 + t] * a.C + c + v] : 0.f;
-            }
-            const Decay d(g[v] + bias[v], amount[v]);
-            const InputGate ig(i[v]);
-            const float m2 = one_minus_square(d.L, d.a);
+        float dx = 0.f, dg = 0.f, di = 0.f;
+        if (PACKED && m.last >> t & 1) back = state_of(a.d_final, t);
+        if (!PACKED || m.in >> t & 1) {
+            Decay& d = dec[t];
+            d.again();
+            const float x = value<T>(rx[t]);
+            const InputGate ig(value<T>(ri[t]));
+            const float m2 = d.one_minus_square();
             // (no decay at all: nothing of the input enters, and nothing comes back)
             const float inv = m2 > 0.f ? __builtin_amdgcn_rsqf(m2) : 0.f;
-            const float root = m2 * inv;
-            const float et = d_o[v] + back[v];
-            const float pt = d.a * et * (d.a * ig.s * x[v] * inv - prev[t][v]);
-            dx[v] = et * root * ig.s;
-            di[v] = et * root * x[v] * ig.slope;
-            dg[v] = pt * amount[v] * d.sig;
-            if (there(t)) {
-                dA[v] = fmaf(pt, d.L, dA[v]);
-                db[v] += dg[v];
-                back[v] = d.a * et;
-            } else {
-                dx[v] = di[v] = dg[v] = 0.f;
-            }
-            if constexpr (PACKED) {
-                if (a.dh0 && active && m.start >> t & 1) a.dh0[(int64_t)a.seq[t0 + t] * a.C + c + v] = back[v];
-            }
+            const float et = value<T>(rd[t]) + back, em = et * (m2 * inv);
+            back = d.a * et;
+            const float pt = back * (d.a * ig.s * x * inv - prev[t]);
+            dx = em * ig.s;
+            di = em * x * ig.slope;
+            dg = pt * amount * sigmoid(value<T>(rg[t]) + bias);
+            dA = fmaf(pt, d.L, dA);
+            db += dg;
         }
+        if (PACKED && a.dh0 && active && m.start >> t & 1) a.dh0[sequence(t) * a.C + c] = back;
         if (active && t0 + t < a.T) {
-            const int64_t row = ((int64_t)b * a.T + t0 + t) * row_words;
-            (static_cast<uint32_t*>(a.dx) + row)[at] = Word<T>::put(dx);
-            (static_cast<uint32_t*>(a.dg) + row)[at] = Word<T>::put(dg);
-            (static_cast<uint32_t*>(a.dgate) + row)[at] = Word<T>::put(di);
+            const int64_t row = head + (int64_t)t * row_bytes;
+            store_one<T>(a.dx, row, lane_bytes, dx);
+            store_one<T>(a.dg, row, lane_bytes, dg);
+            store_one<T>(a.dgate, row, lane_bytes, di);
         }
     }
     __syncthreads();
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        s_prod[w][lane * V + v] = dA[v];
-        s_sum[w][lane * V + v] = db[v];
-    }
+    s_prod[w][lane] = dA;
+    s_sum[w][lane] = db;
     __syncthreads();
     if (w < 2 && active) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float s = 0.f;
-            for (int j = 0; j < GS_WAVES; ++j) s += w ? s_sum[j][lane * V + v] : s_prod[j][lane * V + v];
-            a.part[(((int64_t)b * tiles + k) * 2 + w) * a.C + c + v] = s;
-        }
+        float s = 0.f;
+        for (int j = 0; j < GS_WAVES; ++j) s += w ? s_sum[j][lane] : s_prod[j][lane];
+        a.part[(((int64_t)b * tiles + k) * 2 + w) * a.C + c] = s;
     }
 }
 
@@ -650,7 +557,7 @@ __global__ __launch_bounds__(256) void gated_scan_decode_kernel(ScanDecodeArgs a
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const Decay d(g[v] + a.dt_bias[c + v], expf(a.A_log[c + v]));
-        const float in = __builtin_amdgcn_sqrtf(one_minus_square(d.L, d.a)) * InputGate(i[v]).s * x[v];
+        const float in = __builtin_amdgcn_sqrtf(d.one_minus_square()) * sigmoid(i[v]) * x[v];
         o[v] = a.state_in ? fmaf(d.a, a.state_in[word * V + v], in) : in;
         a.state_out[word * V + v] = o[v];
     }
@@ -658,11 +565,6 @@ __global__ __launch_bounds__(256) void gated_scan_decode_kernel(ScanDecodeArgs a
 }
 
 namespace {
-
-int64_t chains_of(const ScanArgs& a, bool fp32) {
-    const int per = 64 * (fp32 ? Word<float>::N : Word<uint16_t>::N);
-    return (int64_t)a.B * ((a.C + per - 1) / per);
-}
 
 void launch_prepare(const ScanArgs& a, int tiles, int64_t chains, const float* src, float* dst, hipStream_t stream) {
     PrepareArgs q{};
@@ -681,8 +583,8 @@ void launch_prepare(const ScanArgs& a, int tiles, int64_t chains, const float* s
 #define FAR_GROUPS GS_MAX_COUNTERS
 #define OWN_GROUPS GS_MAX_COUNTERS
 #endif
-int64_t set_chains(ScanArgs& a, int tiles, bool fp32) {
-    const int64_t chains = chains_of(a, fp32);
+int64_t set_chains(ScanArgs& a, int tiles) {
+    const int64_t chains = (int64_t)a.B * ((a.C + 63) / 64);
     a.far = chains * tiles <= FAR_GROUPS;
     a.beside = chains * tiles <= OWN_GROUPS ? 1 : (int32_t)chains;
     return chains;
@@ -699,7 +601,7 @@ void by_type(bool fp32, bool packed, F&& f) {
 void launch_gated_scan_fwd(const ScanArgs& args, bool fp32, hipStream_t stream) {
     ScanArgs a = args;
     const int tiles = tiles_of(a.T, FWD_TILE);
-    const int64_t chains = set_chains(a, tiles, fp32);
+    const int64_t chains = set_chains(a, tiles);
     launch_prepare(a, tiles, chains, a.h0, a.h_final, stream);
     if (a.T == 0) return;
     by_type(fp32, a.cu != nullptr, [&](auto t, auto packed) {
@@ -713,7 +615,7 @@ void launch_gated_scan_fwd(const ScanArgs& args, bool fp32, hipStream_t stream) 
 void launch_gated_scan_bwd(const ScanArgs& args, bool fp32, hipStream_t stream) {
     ScanArgs a = args;
     const int tiles = tiles_of(a.T, BWD_TILE);
-    const int64_t chains = set_chains(a, tiles, fp32);
+    const int64_t chains = set_chains(a, tiles);
     launch_prepare(a, tiles, chains, a.d_final, a.dh0, stream);
     if (a.T > 0) {
         by_type(fp32, a.cu != nullptr, [&](auto t, auto packed) {
