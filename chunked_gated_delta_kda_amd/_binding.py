@@ -140,7 +140,7 @@ def load(path: Path | str | None = None):
                                    u16p, u16p, f32p, u16p, f32p, vp, sz, vp]
     for name in ("gated_scan_fwd_workspace_size", "gated_scan_bwd_workspace_size"):
         getattr(lib, name).restype = ctypes.c_size_t
-        getattr(lib, name).argtypes = [i32] * 3
+        getattr(lib, name).argtypes = [i32] * 4
     lib.gated_scan_states.restype = i64
     lib.gated_scan_states.argtypes = [i32] * 3
     lib.gated_scan_fwd.restype = ctypes.c_int
@@ -486,7 +486,7 @@ def _check(st):
 
 
 def _nbytes(t):
-    return t.numel() * t.element_size()
+    return 0 if t is None else t.numel() * t.element_size()
 
 
 def _events(events):
@@ -931,36 +931,64 @@ def gated_norm_bwd(x, gate, weight, dy, activation="sigmoid", eps=1e-6, residual
 
 
 # ------------------------- around a block: recurrence, convolution, layer norm
-def _token_type(t, name):
-    """The dtype code of a call's token tensors."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+# What these calls cost on the host is of the size of their kernels for single tokens, so
+# checks that pass are one expression each, and torch's parts are looked up once.
+class _Torch:
+    parts = None
+
+    def __init__(self):
+        torch = _torch()
+        self.codes = {torch.bfloat16: 0, torch.float32: 1}
+        self.Tensor, self.fp32, self.int32, self.uint8 = (torch.Tensor, torch.float32, torch.int32,
+                                                          torch.uint8)
+        self.empty, self.empty_like = torch.empty, torch.empty_like
+        self.current, self.stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        self.device = torch.cuda.device
+
+
+def _parts():
+    if _Torch.parts is None:
+        _Torch.parts = _Torch()
+    return _Torch.parts
+
+
+def _need_all(named, dtype, shape, dev):
+    """_need of every (name, tensor) of ``named``; None is passed over."""
+    Tensor = _Torch.parts.Tensor
+    for name, t in named:
+        if t is None or (type(t) is Tensor and t.dtype is dtype and t.shape == shape
+                         and t.device == dev and t.is_contiguous()):
+            continue
+        _need(t, name, dtype, shape, dev)
+
+
+def _tokens(t, name, dims, what):
+    """Checks of a call's first token tensor; (dtype code, dtype, device, shape)."""
+    T = _parts()
+    if not isinstance(t, T.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype == torch.bfloat16:
-        return 0
-    if t.dtype == torch.float32:
-        return 1
-    raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    dtype = t.dtype
+    code = T.codes.get(dtype)
+    if code is None:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {dtype}")
+    if not (t.is_cuda and t.is_contiguous()):
+        _need(t, name, dtype)
+    shape = t.shape
+    if dims and len(shape) != dims:
+        raise ValueError(f"{name} must be {what}")
+    return code, dtype, t.device, shape
 
 
-def _batch(x, cu_seqlens):
-    """Checks of a batch of tokens x [B, T, C]; (dtype code, device, B, T, C, sequences)."""
-    torch = _torch()
-    code = _token_type(x, "x")
-    _need(x, "x", x.dtype)
-    if x.dim() != 3:
-        raise ValueError("x must be [B, T, C]")
-    dev = x.device
-    B, T, C = x.shape
-    N = B
-    if cu_seqlens is not None:
-        _need(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
-            raise ValueError("cu_seqlens must be 1-D with num_seqs + 1 entries")
-        if B != 1:
-            raise ValueError("cu_seqlens needs B == 1 (sequences packed along T)")
-        N = cu_seqlens.numel() - 1
-    return code, dev, B, T, C, N
+def _sequences(B, cu_seqlens, dev):
+    """Checks of cu_seqlens; the number of sequences."""
+    if cu_seqlens is None:
+        return B
+    _need(cu_seqlens, "cu_seqlens", _Torch.parts.int32, None, dev)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be 1-D with num_seqs + 1 entries")
+    if B != 1:
+        raise ValueError("cu_seqlens needs B == 1 (sequences packed along T)")
+    return cu_seqlens.numel() - 1
 
 
 def _space(workspace, need, dev):
@@ -968,7 +996,7 @@ def _space(workspace, need, dev):
     if need == 0:
         raise LibKdaError(2, status_str(2))
     if workspace is None:
-        return _torch().empty(need, dtype=_torch().uint8, device=dev)
+        return _Torch.parts.empty(need, dtype=_Torch.parts.uint8, device=dev)
     _need_workspace(workspace, need, dev)
     return workspace
 
@@ -976,49 +1004,78 @@ def _space(workspace, need, dev):
 def _given(t, name, dtype, shape, dev):
     """The caller's output, checked, or a new one."""
     if t is None:
-        return _torch().empty(shape, dtype=dtype, device=dev)
+        return _Torch.parts.empty(shape, dtype=dtype, device=dev)
     _need(t, name, dtype, shape, dev)
     return t
 
 
-def gated_scan_workspace_size(B, T, C, backward=False) -> int:
-    """Workspace bytes of gated_scan_fwd (or gated_scan_bwd).  0: unsupported sizes."""
-    fn = load().gated_scan_bwd_workspace_size if backward else load().gated_scan_fwd_workspace_size
-    return int(fn(B, T, C))
+def _like(t, name, x):
+    """The caller's output, checked, or a new one as x."""
+    if t is None:
+        return _Torch.parts.empty_like(x)
+    _need(t, name, x.dtype, x.shape, x.device)
+    return t
+
+
+def _launch(fn, dev, *args):
+    """fn(*args, stream) on the device's current stream."""
+    T, i = _Torch.parts, dev.index
+    if T.current() == i:
+        _check(fn(*args, T.stream(i)))
+    else:
+        with T.device(dev):
+            _check(fn(*args, T.stream(i)))
+
+
+def gated_scan_workspace_size(B, T, C, backward=False, packed=False) -> int:
+    """Workspace bytes of gated_scan_fwd (or gated_scan_bwd); ``packed``: with cu_seqlens.
+    0: unsupported sizes."""
+    lib = load()
+    fn = lib.gated_scan_bwd_workspace_size if backward else lib.gated_scan_fwd_workspace_size
+    return fn(B, T, C, packed)
 
 
 def _scan_prepare(x, g, input_gate, A_log, dt_bias, initial_state, cu_seqlens, workspace,
                   backward):
-    torch = _torch()
-    code, dev, B, T, C, N = _batch(x, cu_seqlens)
-    _need(g, "g", x.dtype, x.shape, dev)
-    _need(input_gate, "input_gate", x.dtype, x.shape, dev)
-    _need(A_log, "A_log", torch.float32, (C,), dev)
-    _need(dt_bias, "dt_bias", torch.float32, (C,), dev)
+    code, dtype, dev, shape = _tokens(x, "x", 3, "[B, T, C]")
+    B, T, C = shape
+    N = _sequences(B, cu_seqlens, dev)
+    fp32 = _Torch.parts.fp32
+    _need_all((("g", _some(g, "g")), ("input_gate", _some(input_gate, "input_gate"))), dtype, shape,
+              dev)
+    _need_all((("A_log", _some(A_log, "A_log")), ("dt_bias", _some(dt_bias, "dt_bias"))), fp32,
+              (C,), dev)
     if initial_state is not None:
-        _need(initial_state, "initial_state", torch.float32, (N, C), dev)
-    ws = _space(workspace, gated_scan_workspace_size(B, T, C, backward), dev)
+        _need(initial_state, "initial_state", fp32, (N, C), dev)
+    need = gated_scan_workspace_size(B, T, C, backward, cu_seqlens is not None)
+    if need == 256 and workspace is None and not backward:
+        ws = None  # (one alignment unit: rows of one tile, no workspace)
+    else:
+        ws = _space(workspace, need, dev)
     return code, dev, B, T, C, N, ws
+
+
+def _some(t, name):
+    """t, which has to be there."""
+    if t is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return t
 
 
 def _scan_fwd(x, g, input_gate, A_log, dt_bias, initial_state, output_final_state, cu_seqlens,
               workspace, out, final_out, keep):
-    torch = _torch()
     code, dev, B, T, C, N, ws = _scan_prepare(x, g, input_gate, A_log, dt_bias, initial_state,
                                               cu_seqlens, workspace, False)
-    out = _given(out, "out", x.dtype, (B, T, C), dev)
-    final = None
-    if output_final_state:
-        final = _given(final_out, "final_out", torch.float32, (N, C), dev)
+    fp32 = _Torch.parts.fp32
+    out = _like(out, "out", x)
+    final = _given(final_out, "final_out", fp32, (N, C), dev) if output_final_state else None
+    lib = load()
     states = None
     if keep:
-        states = torch.empty(int(load().gated_scan_states(B, T, C)), dtype=torch.float32,
-                             device=dev)
-    with _on(dev):
-        _check(load().gated_scan_fwd(_addr(x), _addr(g), _addr(input_gate), _addr(A_log),
-                                     _addr(dt_bias), _addr(initial_state), _addr(final),
-                                     _addr(cu_seqlens), N, code, B, T, C, _addr(out),
-                                     _addr(states), _addr(ws), _nbytes(ws), _stream(dev)))
+        states = _Torch.parts.empty(int(lib.gated_scan_states(B, T, C)), dtype=fp32, device=dev)
+    _launch(lib.gated_scan_fwd, dev, _addr(x), _addr(g), _addr(input_gate), _addr(A_log),
+            _addr(dt_bias), _addr(initial_state), _addr(final), _addr(cu_seqlens), N, code, B, T, C,
+            _addr(out), _addr(states), _addr(ws), _nbytes(ws))
     return out, final, states
 
 
@@ -1050,23 +1107,20 @@ def gated_scan_bwd(x, g, input_gate, A_log, dt_bias, do, states, initial_state=N
     ``dfinal`` [N,C] fp32 (None: zero): a dict with dx, dg, dinput_gate (as x), dA_log,
     ddt_bias [C] and dh0 [N,C] (fp32; None unless ``need_dh0``).  ``states`` is what the
     forward call on the same inputs returned."""
-    torch = _torch()
     code, dev, B, T, C, N, ws = _scan_prepare(x, g, input_gate, A_log, dt_bias, initial_state,
                                               cu_seqlens, workspace, True)
+    P, lib = _Torch.parts, load()
     _need(do, "do", x.dtype, x.shape, dev)
-    _need(states, "states", torch.float32, (int(load().gated_scan_states(B, T, C)),), dev)
+    _need(states, "states", P.fp32, (int(lib.gated_scan_states(B, T, C)),), dev)
     if dfinal is not None:
-        _need(dfinal, "dfinal", torch.float32, (N, C), dev)
-    r = {"dx": torch.empty_like(x), "dg": torch.empty_like(x), "dinput_gate": torch.empty_like(x),
-         "dA_log": torch.empty_like(A_log), "ddt_bias": torch.empty_like(dt_bias),
-         "dh0": torch.empty((N, C), dtype=torch.float32, device=dev) if need_dh0 else None}
-    with _on(dev):
-        _check(load().gated_scan_bwd(_addr(x), _addr(g), _addr(input_gate), _addr(A_log),
-                                     _addr(dt_bias), _addr(initial_state), _addr(cu_seqlens), N,
-                                     code, B, T, C, _addr(do), _addr(dfinal), _addr(states),
-                                     _addr(r["dx"]), _addr(r["dg"]), _addr(r["dinput_gate"]),
-                                     _addr(r["dA_log"]), _addr(r["ddt_bias"]), _addr(r["dh0"]),
-                                     _addr(ws), _nbytes(ws), _stream(dev)))
+        _need(dfinal, "dfinal", P.fp32, (N, C), dev)
+    r = {"dx": P.empty_like(x), "dg": P.empty_like(x), "dinput_gate": P.empty_like(x),
+         "dA_log": P.empty_like(A_log), "ddt_bias": P.empty_like(dt_bias),
+         "dh0": P.empty((N, C), dtype=P.fp32, device=dev) if need_dh0 else None}
+    _launch(lib.gated_scan_bwd, dev, _addr(x), _addr(g), _addr(input_gate), _addr(A_log),
+            _addr(dt_bias), _addr(initial_state), _addr(cu_seqlens), N, code, B, T, C, _addr(do),
+            _addr(dfinal), _addr(states), _addr(r["dx"]), _addr(r["dg"]), _addr(r["dinput_gate"]),
+            _addr(r["dA_log"]), _addr(r["ddt_bias"]), _addr(r["dh0"]), _addr(ws), _nbytes(ws))
     return r
 
 
@@ -1074,45 +1128,40 @@ def gated_scan_decode(x, g, input_gate, A_log, dt_bias, state=None, state_out=No
     """One token of the recurrence for N sequences: x, g, input_gate [N,C], all bf16 or all
     fp32; state [N,C] fp32 or None (zeros).  ``state_out`` may be ``state`` (update in
     place).  Returns (o [N,C] as x, new state [N,C] fp32)."""
-    torch = _torch()
-    code = _token_type(x, "x")
-    _need(x, "x", x.dtype)
-    if x.dim() != 2:
-        raise ValueError("x must be [N, C]")
-    dev = x.device
-    N, C = x.shape
-    _need(g, "g", x.dtype, (N, C), dev)
-    _need(input_gate, "input_gate", x.dtype, (N, C), dev)
-    _need(A_log, "A_log", torch.float32, (C,), dev)
-    _need(dt_bias, "dt_bias", torch.float32, (C,), dev)
-    if state is not None:
-        _need(state, "state", torch.float32, (N, C), dev)
-    state_out = _given(state_out, "state_out", torch.float32, (N, C), dev)
-    out = _given(out, "out", x.dtype, (N, C), dev)
-    with _on(dev):
-        _check(load().gated_scan_decode(_addr(x), _addr(g), _addr(input_gate), _addr(A_log),
-                                        _addr(dt_bias), _addr(state), _addr(state_out), code, N, C,
-                                        _addr(out), _stream(dev)))
+    code, dtype, dev, shape = _tokens(x, "x", 2, "[N, C]")
+    N, C = shape
+    fp32 = _Torch.parts.fp32
+    _need_all((("g", _some(g, "g")), ("input_gate", _some(input_gate, "input_gate")), ("out", out)),
+              dtype, shape, dev)
+    _need_all((("A_log", _some(A_log, "A_log")), ("dt_bias", _some(dt_bias, "dt_bias"))), fp32,
+              (C,), dev)
+    _need_all((("state", state), ("state_out", state_out)), fp32, shape, dev)
+    if state_out is None:
+        state_out = _Torch.parts.empty(shape, dtype=fp32, device=dev)
+    if out is None:
+        out = _Torch.parts.empty_like(x)
+    _launch(load().gated_scan_decode, dev, _addr(x), _addr(g), _addr(input_gate), _addr(A_log),
+            _addr(dt_bias), _addr(state), _addr(state_out), code, N, C, _addr(out))
     return out, state_out
 
 
 _CONV_ACTIVATIONS = {None: 0, "none": 0, "silu": 1}
 
 
-def _conv_parameters(x, C, weight, bias, activation, dev):
+def _conv_parameters(C, weight, bias, activation, dev):
     """Checks of a convolution's parameters; (taps, activation code)."""
-    torch = _torch()
-    _need(weight, "weight", torch.float32, None, dev)
-    if weight.dim() != 2 or weight.shape[0] != C:
-        raise ValueError(f"weight must be [C, W] with C = {C}, got {tuple(weight.shape)}")
+    fp32 = _Torch.parts.fp32
+    _need(weight, "weight", fp32, None, dev)
+    shape = weight.shape
+    if len(shape) != 2 or shape[0] != C:
+        raise ValueError(f"weight must be [C, W] with C = {C}, got {tuple(shape)}")
     if bias is not None:
-        _need(bias, "bias", torch.float32, (C,), dev)
+        _need(bias, "bias", fp32, (C,), dev)
     if activation not in _CONV_ACTIVATIONS:
         raise ValueError(f"activation must be 'none' or 'silu', got {activation!r}")
-    W = weight.shape[1]
-    if W not in (2, 3, 4):
+    if shape[1] not in (2, 3, 4):
         raise LibKdaError(2, status_str(2))
-    return W, _CONV_ACTIVATIONS[activation]
+    return shape[1], _CONV_ACTIVATIONS[activation]
 
 
 def short_conv_fwd(x, weight, bias=None, activation="silu", initial_state=None,
@@ -1123,18 +1172,15 @@ def short_conv_fwd(x, weight, bias=None, activation="silu", initial_state=None,
     W - 1 tokens in front of each sequence, the oldest first) or None (zeros); cu_seqlens
     int32 [N+1] or None (B must then be 1; rows outside every sequence get zeros).  Returns
     (y [B,T,C] as x, final_state [N,W-1,C] as x or None)."""
-    code, dev, B, T, C, N = _batch(x, cu_seqlens)
-    W, act = _conv_parameters(x, C, weight, bias, activation, dev)
+    code, dtype, dev, (B, T, C) = _tokens(x, "x", 3, "[B, T, C]")
+    N = _sequences(B, cu_seqlens, dev)
+    W, act = _conv_parameters(C, weight, bias, activation, dev)
     if initial_state is not None:
-        _need(initial_state, "initial_state", x.dtype, (N, W - 1, C), dev)
-    out = _given(out, "out", x.dtype, (B, T, C), dev)
-    final = None
-    if output_final_state:
-        final = _given(final_out, "final_out", x.dtype, (N, W - 1, C), dev)
-    with _on(dev):
-        _check(load().short_conv_fwd(_addr(x), _addr(weight), _addr(bias), act,
-                                     _addr(initial_state), _addr(final), _addr(cu_seqlens), N,
-                                     code, B, T, C, W, _addr(out), _stream(dev)))
+        _need(initial_state, "initial_state", dtype, (N, W - 1, C), dev)
+    out = _like(out, "out", x)
+    final = _given(final_out, "final_out", dtype, (N, W - 1, C), dev) if output_final_state else None
+    _launch(load().short_conv_fwd, dev, _addr(x), _addr(weight), _addr(bias), act,
+            _addr(initial_state), _addr(final), _addr(cu_seqlens), N, code, B, T, C, W, _addr(out))
     return out, final
 
 
@@ -1143,23 +1189,21 @@ def short_conv_bwd(x, weight, dy, bias=None, activation="silu", initial_state=No
     """Gradients of short_conv_fwd for dL/dy = ``dy`` (as x) and dL/d(final state) =
     ``dfinal`` [N,W-1,C] as x (None: zero): a dict with dx (as x), dweight [C,W], dbias [C]
     (fp32; None without a bias) and dh0 [N,W-1,C] (as x; None unless ``need_dh0``)."""
-    torch = _torch()
-    code, dev, B, T, C, N = _batch(x, cu_seqlens)
-    W, act = _conv_parameters(x, C, weight, bias, activation, dev)
-    _need(dy, "dy", x.dtype, x.shape, dev)
-    for t, name in ((initial_state, "initial_state"), (dfinal, "dfinal")):
-        if t is not None:
-            _need(t, name, x.dtype, (N, W - 1, C), dev)
-    ws = _space(workspace, int(load().short_conv_bwd_workspace_size(code, B, T, C, W)), dev)
-    r = {"dx": torch.empty_like(x), "dweight": torch.empty_like(weight),
-         "dbias": None if bias is None else torch.empty_like(bias),
-         "dh0": torch.empty((N, W - 1, C), dtype=x.dtype, device=dev) if need_dh0 else None}
-    with _on(dev):
-        _check(load().short_conv_bwd(_addr(x), _addr(weight), _addr(bias), act,
-                                     _addr(initial_state), _addr(cu_seqlens), N, code, B, T, C, W,
-                                     _addr(dy), _addr(dfinal), _addr(r["dx"]), _addr(r["dweight"]),
-                                     _addr(r["dbias"]), _addr(r["dh0"]), _addr(ws), _nbytes(ws),
-                                     _stream(dev)))
+    code, dtype, dev, shape = _tokens(x, "x", 3, "[B, T, C]")
+    B, T, C = shape
+    N = _sequences(B, cu_seqlens, dev)
+    W, act = _conv_parameters(C, weight, bias, activation, dev)
+    _need(dy, "dy", dtype, shape, dev)
+    _need_all((("initial_state", initial_state), ("dfinal", dfinal)), dtype, (N, W - 1, C), dev)
+    P, lib = _Torch.parts, load()
+    ws = _space(workspace, int(lib.short_conv_bwd_workspace_size(code, B, T, C, W)), dev)
+    r = {"dx": P.empty_like(x), "dweight": P.empty_like(weight),
+         "dbias": None if bias is None else P.empty_like(bias),
+         "dh0": P.empty((N, W - 1, C), dtype=dtype, device=dev) if need_dh0 else None}
+    _launch(lib.short_conv_bwd, dev, _addr(x), _addr(weight), _addr(bias), act,
+            _addr(initial_state), _addr(cu_seqlens), N, code, B, T, C, W, _addr(dy), _addr(dfinal),
+            _addr(r["dx"]), _addr(r["dweight"]), _addr(r["dbias"]), _addr(r["dh0"]), _addr(ws),
+            _nbytes(ws))
     return r
 
 
@@ -1167,32 +1211,26 @@ def short_conv_decode(x, weight, state, bias=None, activation="silu", state_out=
     """One token of the convolution for N sequences: x [N,C] bf16 or fp32, state [N,W-1,C]
     as x, the oldest token first.  ``state_out`` may be ``state`` (update in place).
     Returns (y [N,C], new state [N,W-1,C]), as x."""
-    code = _token_type(x, "x")
-    _need(x, "x", x.dtype)
-    if x.dim() != 2:
-        raise ValueError("x must be [N, C]")
-    dev = x.device
-    N, C = x.shape
-    W, act = _conv_parameters(x, C, weight, bias, activation, dev)
-    _need(state, "state", x.dtype, (N, W - 1, C), dev)
-    state_out = _given(state_out, "state_out", x.dtype, (N, W - 1, C), dev)
-    out = _given(out, "out", x.dtype, (N, C), dev)
-    with _on(dev):
-        _check(load().short_conv_decode(_addr(x), _addr(weight), _addr(bias), act, _addr(state),
-                                        _addr(state_out), code, N, C, W, _addr(out),
-                                        _stream(dev)))
+    code, dtype, dev, (N, C) = _tokens(x, "x", 2, "[N, C]")
+    W, act = _conv_parameters(C, weight, bias, activation, dev)
+    _need_all((("state", _some(state, "state")), ("state_out", state_out)), dtype, (N, W - 1, C),
+              dev)
+    if state_out is None:
+        state_out = _Torch.parts.empty_like(state)
+    out = _like(out, "out", x)
+    _launch(load().short_conv_decode, dev, _addr(x), _addr(weight), _addr(bias), act, _addr(state),
+            _addr(state_out), code, N, C, W, _addr(out))
     return out, state_out
 
 
 def _rows(x, name, weight):
-    """Checks of rows x [..., D] and their weight; (dtype code, device, rows, D)."""
-    code = _token_type(x, name)
-    _need(x, name, x.dtype)
-    if x.dim() < 1 or x.shape[-1] < 1:
+    """Checks of rows x [..., D] and their weight; (dtype code, dtype, device, shape, rows, D)."""
+    code, dtype, dev, shape = _tokens(x, name, 0, "")
+    if len(shape) < 1 or shape[-1] < 1:
         raise ValueError(f"{name} must be [..., D]")
-    D = x.shape[-1]
-    _need(weight, "weight", _torch().float32, (D,), x.device)
-    return code, x.device, x.numel() // D, D
+    D = shape[-1]
+    _need(weight, "weight", _Torch.parts.fp32, (D,), dev)
+    return code, dtype, dev, shape, x.numel() // D, D
 
 
 def layer_norm_fwd(x, weight, bias=None, eps=1e-5, residual=None, out=None, sum_out=None):
@@ -1201,20 +1239,19 @@ def layer_norm_fwd(x, weight, bias=None, eps=1e-5, residual=None, out=None, sum_
     sqrt(var(u) + eps) weight + bias.  residual as x; weight [D], bias [D] or None, fp32.
     ``out`` and ``sum_out`` may be ``x`` or ``residual``, one each.  Returns (y, u), both as
     x; u is ``x`` itself without a residual."""
-    code, dev, rows, D = _rows(x, "x", weight)
+    code, dtype, dev, shape, rows, D = _rows(x, "x", weight)
     if bias is not None:
-        _need(bias, "bias", _torch().float32, (D,), dev)
+        _need(bias, "bias", _Torch.parts.fp32, (D,), dev)
     total = x
+    _need_all((("residual", residual), ("out", out)), dtype, shape, dev)
     if residual is not None:
-        _need(residual, "residual", x.dtype, x.shape, dev)
-        total = _given(sum_out, "sum_out", x.dtype, x.shape, dev)
-    out = _given(out, "out", x.dtype, x.shape, dev)
-    if out is total and residual is not None:
-        raise ValueError("out and sum_out must be two tensors")
-    with _on(dev):
-        _check(load().layer_norm_fwd(_addr(x), _addr(residual), _addr(weight), _addr(bias),
-                                     float(eps), code, rows, D, _addr(out),
-                                     None if residual is None else _addr(total), _stream(dev)))
+        total = _like(sum_out, "sum_out", x)
+        if out is total:
+            raise ValueError("out and sum_out must be two tensors")
+    if out is None:
+        out = _Torch.parts.empty_like(x)
+    _launch(load().layer_norm_fwd, dev, _addr(x), _addr(residual), _addr(weight), _addr(bias),
+            float(eps), code, rows, D, _addr(out), None if residual is None else _addr(total))
     return out, total
 
 
@@ -1222,16 +1259,13 @@ def layer_norm_bwd(total, weight, dy, eps=1e-5, dsum=None, workspace=None, need_
     """Gradients of layer_norm_fwd for dL/dy = ``dy`` and dL/du = ``dsum`` (None: none), from
     the ``total`` u that it returned: a dict with dx (as u; that of x and of the residual
     alike), dweight [D] and dbias [D] (fp32; None unless ``need_dbias``)."""
-    torch = _torch()
-    code, dev, rows, D = _rows(total, "total", weight)
-    _need(dy, "dy", total.dtype, total.shape, dev)
-    if dsum is not None:
-        _need(dsum, "dsum", total.dtype, total.shape, dev)
-    ws = _space(workspace, int(load().layer_norm_bwd_workspace_size(code, rows, D)), dev)
-    r = {"dx": torch.empty_like(total), "dweight": torch.empty_like(weight),
-         "dbias": torch.empty_like(weight) if need_dbias else None}
-    with _on(dev):
-        _check(load().layer_norm_bwd(_addr(total), _addr(weight), float(eps), code, rows, D,
-                                     _addr(dy), _addr(dsum), _addr(r["dx"]), _addr(r["dweight"]),
-                                     _addr(r["dbias"]), _addr(ws), _nbytes(ws), _stream(dev)))
+    code, dtype, dev, shape, rows, D = _rows(total, "total", weight)
+    _need_all((("dy", _some(dy, "dy")), ("dsum", dsum)), dtype, shape, dev)
+    P, lib = _Torch.parts, load()
+    ws = _space(workspace, int(lib.layer_norm_bwd_workspace_size(code, rows, D)), dev)
+    r = {"dx": P.empty_like(total), "dweight": P.empty_like(weight),
+         "dbias": P.empty_like(weight) if need_dbias else None}
+    _launch(lib.layer_norm_bwd, dev, _addr(total), _addr(weight), float(eps), code, rows, D,
+            _addr(dy), _addr(dsum), _addr(r["dx"]), _addr(r["dweight"]), _addr(r["dbias"]),
+            _addr(ws), _nbytes(ws))
     return r

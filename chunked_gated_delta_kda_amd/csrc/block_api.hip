@@ -45,22 +45,22 @@ bool countable_tiles(int32_t B, int32_t T, int32_t C) {
     return (int64_t)B * scan_states(T) * ((C + 63) / 64) < I31;
 }
 
-// Workspace of the recurrence: the counters and words of the tiles, a packed batch's marks
-// and sequences, and for the gradients the tiles' sums.  One row of a batch may be packed
-// or not.
+// Workspace of the recurrence: the counters and words of the tiles (none where a row is one
+// tile), a packed batch's marks and sequences, and for the gradients the tiles' sums.
 struct ScanSpace {
     size_t tickets, words, marks, seq, part, total;
 };
 
-ScanSpace scan_space(int32_t B, int32_t T, int32_t C, bool backward) {
-    const size_t groups = ((size_t)T + 15) / 16;
+ScanSpace scan_space(int32_t B, int32_t T, int32_t C, bool packed, bool backward) {
+    const size_t groups = packed ? ((size_t)T + 15) / 16 : 0;
+    const bool one = T == 0 || (backward ? T <= kda::GS_STATES : !packed && T <= kda::GS_ONE_TILE);
+    const int64_t counters = std::min<int64_t>((int64_t)B * ((C + 63) / 64), kda::GS_MAX_COUNTERS);
     ScanSpace s{};
     s.tickets = 0;
-    s.words = align_up((size_t)std::min<int64_t>((int64_t)B * ((C + 63) / 64), kda::GS_MAX_COUNTERS) *
-                       kda::GS_TICKET_BYTES);
-    s.marks = s.words + align_up((size_t)B * scan_states(T) * C * sizeof(uint64_t));
-    s.seq = s.marks + (B == 1 ? align_up(groups * sizeof(uint2)) : 0);
-    s.part = s.seq + (B == 1 ? align_up(groups * 16 * sizeof(int32_t)) : 0);
+    s.words = one ? 0 : align_up((size_t)counters * kda::GS_TICKET_BYTES);
+    s.marks = s.words + (one ? 0 : align_up((size_t)B * scan_states(T) * C * sizeof(uint64_t)));
+    s.seq = s.marks + align_up(groups * sizeof(uint2));
+    s.part = s.seq + align_up(groups * 16 * sizeof(int32_t));
     s.total = s.part + (backward ? align_up((size_t)B * scan_states(T) * 2 * C * sizeof(float)) : 0);
     return s;
 }
@@ -77,7 +77,7 @@ int check_scan(const void* x, const void* g, const void* gate, const float* A_lo
 }
 
 int check_workspace(const void* ws, size_t bytes, size_t need) {
-    return ws && aligned(ws, ALIGN) && bytes >= need ? KDA_OK : KDA_ERR_WORKSPACE;
+    return !need || (ws && aligned(ws, ALIGN) && bytes >= need) ? KDA_OK : KDA_ERR_WORKSPACE;
 }
 
 kda::ScanArgs scan_args(const void* x, const void* g, const void* gate, const float* A_log, const float* dt_bias,
@@ -148,12 +148,14 @@ int64_t gated_scan_states(int32_t B, int32_t T, int32_t C) {
     return valid_batch(B, T, C) && countable_tiles(B, T, C) ? (int64_t)B * scan_states(T) * C : -1;
 }
 
-size_t gated_scan_fwd_workspace_size(int32_t B, int32_t T, int32_t C) {
-    return valid_batch(B, T, C) && countable_tiles(B, T, C) ? scan_space(B, T, C, false).total : 0;
+size_t gated_scan_fwd_workspace_size(int32_t B, int32_t T, int32_t C, int32_t packed) {
+    if (!valid_batch(B, T, C) || !countable_tiles(B, T, C) || (packed && B != 1)) return 0;
+    return std::max(ALIGN, scan_space(B, T, C, packed != 0, false).total);
 }
 
-size_t gated_scan_bwd_workspace_size(int32_t B, int32_t T, int32_t C) {
-    return valid_batch(B, T, C) && countable_tiles(B, T, C) ? scan_space(B, T, C, true).total : 0;
+size_t gated_scan_bwd_workspace_size(int32_t B, int32_t T, int32_t C, int32_t packed) {
+    if (!valid_batch(B, T, C) || !countable_tiles(B, T, C) || (packed && B != 1)) return 0;
+    return std::max(ALIGN, scan_space(B, T, C, packed != 0, true).total);
 }
 
 int gated_scan_fwd(const void* x, const void* g, const void* input_gate, const float* A_log, const float* dt_bias,
@@ -163,7 +165,7 @@ int gated_scan_fwd(const void* x, const void* g, const void* input_gate, const f
     int st = check_scan(x, g, input_gate, A_log, dt_bias, initial_state, cu_seqlens, num_seqs, dtype, B, T, C);
     if (st != KDA_OK) return st;
     if ((T > 0 && !o) || !aligned({o, final_state, states}, 16)) return KDA_ERR_INVALID_ARG;
-    const ScanSpace sp = scan_space(B, T, C, false);
+    const ScanSpace sp = scan_space(B, T, C, cu_seqlens != nullptr, false);
     st = check_workspace(workspace, workspace_bytes, sp.total);
     if (st != KDA_OK) return st;
     kda::ScanArgs a =
@@ -186,7 +188,7 @@ int gated_scan_bwd(const void* x, const void* g, const void* input_gate, const f
     if (T > 0 && (!d_o || !states || !dx || !dg || !dinput_gate)) return KDA_ERR_INVALID_ARG;
     if (!dA_log || !ddt_bias || !aligned({dA_log, ddt_bias}, 4)) return KDA_ERR_INVALID_ARG;
     if (!aligned({d_o, d_final, states, dx, dg, dinput_gate, dh0}, 16)) return KDA_ERR_INVALID_ARG;
-    const ScanSpace sp = scan_space(B, T, C, true);
+    const ScanSpace sp = scan_space(B, T, C, cu_seqlens != nullptr, true);
     st = check_workspace(workspace, workspace_bytes, sp.total);
     if (st != KDA_OK) return st;
     kda::ScanArgs a =

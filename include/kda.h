@@ -551,7 +551,9 @@ enum kda_dtype { KDA_BF16 = 0, KDA_FP32 = 1 };
  * supported. */
 int64_t gated_scan_states(int32_t B, int32_t T, int32_t C);
 
-size_t gated_scan_fwd_workspace_size(int32_t B, int32_t T, int32_t C);
+/* packed: whether cu_seqlens will be passed.  A call that needs no workspace (rows of up to
+ * 256 tokens, not packed) has a size of 256 bytes and accepts NULL. */
+size_t gated_scan_fwd_workspace_size(int32_t B, int32_t T, int32_t C, int32_t packed);
 
 int gated_scan_fwd(const void* x, const void* g, const void* input_gate, const float* A_log,
                    const float* dt_bias, const float* initial_state, float* final_state,
@@ -563,7 +565,7 @@ int gated_scan_fwd(const void* x, const void* g, const void* input_gate, const f
  * dx, dg, dinput_gate [B, T, C] tokens, dA_log, ddt_bias [C], dh0 [N, C] or NULL
  * (not written).  states: those of a gated_scan_fwd call on the same inputs,
  * sizes, initial_state and cu_seqlens. */
-size_t gated_scan_bwd_workspace_size(int32_t B, int32_t T, int32_t C);
+size_t gated_scan_bwd_workspace_size(int32_t B, int32_t T, int32_t C, int32_t packed);
 
 int gated_scan_bwd(const void* x, const void* g, const void* input_gate, const float* A_log,
                    const float* dt_bias, const float* initial_state, const int32_t* cu_seqlens,

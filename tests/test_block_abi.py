@@ -27,7 +27,7 @@ SIZES = [
     (dict(dtype=-1), 1), (dict(B=1 << 16, T=1 << 15), 1), (dict(cu=FAKE, B=2, N=2), 1), (dict(cu=FAKE, N=0), 1),
     (dict(cu=odd(2)), 1), (dict(x=None), 1), (dict(x=odd(8)), 1), (dict(h0=odd(8)), 1)]
 
-SCAN = dict(x=FAKE, g=FAKE, gate=FAKE, A=FAKE, b=FAKE, h0=None, hT=None, cu=None, N=1, dtype=0, B=1, T=16, C=64, o=FAKE,
+SCAN = dict(x=FAKE, g=FAKE, gate=FAKE, A=FAKE, b=FAKE, h0=None, hT=None, cu=None, N=1, dtype=0, B=1, T=300, C=64, o=FAKE,
             states=None, ws=FAKE, wsb=BIG, stream=None)
 SCAN_ONLY = [(dict(g=None), 1), (dict(gate=None), 1), (dict(A=None), 1), (dict(b=None), 1), (dict(g=odd(4)), 1),
              (dict(gate=odd(8)), 1), (dict(A=odd(2)), 1), (dict(b=odd(1)), 1), (dict(ws=None), 3),
@@ -41,7 +41,7 @@ def test_gated_scan_fwd_rejects_on_host(lib, over, code):
     assert call(lib.gated_scan_fwd, SCAN, over) == code
 
 
-SCAN_BWD = dict(x=FAKE, g=FAKE, gate=FAKE, A=FAKE, b=FAKE, h0=None, cu=None, N=1, dtype=0, B=1, T=16, C=64, do=FAKE,
+SCAN_BWD = dict(x=FAKE, g=FAKE, gate=FAKE, A=FAKE, b=FAKE, h0=None, cu=None, N=1, dtype=0, B=1, T=300, C=64, do=FAKE,
                 df=None, states=FAKE, dx=FAKE, dg=FAKE, di=FAKE, dA=FAKE, db=FAKE, dh0=None, ws=FAKE, wsb=BIG,
                 stream=None)
 
@@ -137,7 +137,12 @@ def test_sizes(lib):
     assert lib.gated_scan_states(1 << 24, 64, 1 << 13) == -1
     assert kda.gated_scan_workspace_size(1 << 24, 64, 1 << 13) == 0
     assert lib.gated_scan_states((1 << 24) - 1, 64, 1 << 13) == ((1 << 24) - 1) << 13
-    assert kda.gated_scan_workspace_size(2, 100, 64) >= 256
+    # rows of one tile need none, packed ones their tables, longer ones words for every tile
+    assert kda.gated_scan_workspace_size(2, 256, 64) == 256
+    assert kda.gated_scan_workspace_size(1, 256, 64, packed=True) > 256
+    assert kda.gated_scan_workspace_size(2, 100, 64, packed=True) == 0
+    assert kda.gated_scan_workspace_size(2, 257, 64) >= 2 * 3 * 64 * 8
+    assert kda.gated_scan_workspace_size(2, 257, 64, True) >= 2 * 5 * 64 * 8 + 2 * 5 * 2 * 64 * 4
     assert lib.short_conv_bwd_workspace_size(0, 1, 1, 64, 5) == lib.short_conv_bwd_workspace_size(2, 1, 1, 64, 4) == 0
     assert lib.layer_norm_bwd_workspace_size(0, 5, 12) == lib.layer_norm_bwd_workspace_size(3, 5, 64) == 0
     assert lib.layer_norm_bwd_workspace_size(0, 1 << 31, 64) == lib.layer_norm_bwd_workspace_size(1, 5, 16392) == 0

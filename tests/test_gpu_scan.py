@@ -51,7 +51,7 @@ def check(w):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 127, 128, 129, 300])
+@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 64, 65, 127, 128, 129, 192, 255, 256, 257, 300])
 def test_lengths(T, dtype):
     check(make(2, T, 24, seed=T, dtype=dtype))
 
