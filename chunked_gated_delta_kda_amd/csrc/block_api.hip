@@ -112,6 +112,7 @@ int check_conv(const void* x, const float* weight, const float* bias, int32_t ac
     if (W < 2 || W > 4) return KDA_ERR_UNSUPPORTED;
     if (activation != KDA_CONV_NONE && activation != KDA_CONV_SILU) return KDA_ERR_INVALID_ARG;
     if (!weight || (T > 0 && !x)) return KDA_ERR_INVALID_ARG;
+    if (kda::short_conv_workgroups(B, T, C, cu ? num_seqs : B) >= I31) return KDA_ERR_INVALID_ARG;
     if (!aligned({x, initial_state}, 16) || !aligned({weight, bias}, 4)) return KDA_ERR_INVALID_ARG;
     return KDA_OK;
 }
@@ -247,6 +248,7 @@ int short_conv_fwd(const void* x, const float* weight, const float* bias, int32_
 
 size_t short_conv_bwd_workspace_size(int32_t dtype, int32_t B, int32_t T, int32_t C, int32_t W) {
     if (!valid_batch(B, T, C) || W < 2 || W > 4 || !known_type(dtype)) return 0;
+    if (kda::short_conv_workgroups(B, T, C, B) >= I31) return 0;
     return std::max(
         ALIGN, align_up((size_t)kda::short_conv_groups(B, T, C, dtype == KDA_FP32) * (W + 1) * C * sizeof(float)));
 }

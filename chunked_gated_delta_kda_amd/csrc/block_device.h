@@ -37,7 +37,8 @@ struct Word<float> {
 
 // A sigmoid 1 / (1 + e^-z) as e^min(z, 0) / (1 + e^-|z|), to a few ulps where it is
 // normal, and subnormal below z = -87 (2^t by the hardware is not: the exponent's whole
-// part is put in behind it).  `rest` is 1 - s.
+// part is put in behind it).  `rest` is 1 - s.  For a NaN both are numbers: what they are
+// multiplied by z for is one.
 struct BlockSigmoid {
     float s, rest;
     __device__ __forceinline__ explicit BlockSigmoid(float z) {
@@ -46,7 +47,6 @@ struct BlockSigmoid {
         const float er = e * r;
         s = z < 0.f ? er : r;
         rest = z < 0.f ? r : er;
-        if (z != z) s = rest = z;
     }
 };
 
@@ -108,7 +108,7 @@ __device__ __forceinline__ float lane_sum(float v) {
     return v;
 }
 
-// R words of a token row (8 or 16 bytes): 2 R bf16 channels or R fp32 channels
+// R words of a token row (4, 8 or 16 bytes): 2 R bf16 channels or R fp32 channels
 template <class T, int R = 4>
 struct Slice {
     static constexpr int W = Word<T>::N, N = R * W;

@@ -83,7 +83,7 @@ struct ConvArgs {
     float* dweight;         // [C, W]
     float* dbias;           // [C] or null
     float* part;            // [groups, W + 1, C]: a workgroup's sums
-    int64_t groups;         // workgroups of strips (of a block of channels), and a strip's tokens
+    uint32_t groups;        // workgroups of strips (of a block of channels), and a strip's tokens
     int32_t strip;
 };
 
@@ -128,6 +128,8 @@ void launch_short_conv_bwd(const ConvArgs& a, int W, bool fp32, hipStream_t stre
 void launch_short_conv_decode(const ConvDecodeArgs& a, int W, bool fp32, hipStream_t stream);
 // rows of sums that the convolution's backward kernel leaves in part
 int64_t short_conv_groups(int32_t B, int32_t T, int32_t C, bool fp32);
+// most workgroups of its kernels (counted in 32 bits)
+int64_t short_conv_workgroups(int32_t B, int32_t T, int32_t C, int32_t N);
 void launch_layer_norm_fwd(const LayerNormArgs& a, bool fp32, hipStream_t stream);
 void launch_layer_norm_bwd(const LayerNormArgs& a, bool fp32, hipStream_t stream);
 // workgroups of the norm's backward kernel, each leaving a row of sums in part

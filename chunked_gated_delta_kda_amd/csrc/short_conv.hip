@@ -6,10 +6,12 @@
 //   dx_t = sum_j weight[c, j] dz_{t + W - 1 - j},  dbias = sum dz,
 //   dweight[c, j] = sum dz_t x_{t - W + 1 + j}.
 //
-// Bound by HBM.  A wave has a strip of tokens and 16 bytes of channels a lane, so
-// that a sequence's boundary is the same for all its lanes: the window of the last
-// W - 1 tokens and the gradients of the last W - 1 slide through registers, while the
-// loads of the next eight tokens are under way.
+// Bound by HBM.  A wave has a strip of tokens and two channels a lane, so that a
+// sequence's boundary is the same for all its lanes: the last W - 1 tokens and their
+// gradients slide through registers, while the loads of the next four tokens are
+// under way.  (Four and eight channels a lane leave too few waves, and in the
+// gradients too few registers: 4096 tokens of 4096 bf16 channels, gradients 34 us
+// with two, 42 with four, 56 with eight.)
 #include "block_device.h"
 
 namespace kda {
@@ -18,16 +20,10 @@ namespace {
 
 constexpr int SC_WAVES = 4;
 constexpr int SC_THREADS = 64 * SC_WAVES;
-#ifndef SC_FWD_BATCH
-#define SC_FWD_BATCH 8
-#define SC_BWD_BATCH 4
-#define SC_FWD_WORDS 4
-#define SC_BWD_WORDS 2
-#endif
+constexpr int SC_BATCH = 4;  // tokens whose loads are under way together; divides a strip
+
 template <class T>
-using FwdSlice = Slice<T, SC_FWD_WORDS>;
-template <class T>
-using BwdSlice = Slice<T, SC_BWD_WORDS>;
+using Pair = Slice<T, sizeof(T) / 2>;  // two channels
 
 __device__ __forceinline__ int clamp_tok(int v, int T) { return min(max(v, 0), T); }
 
@@ -62,14 +58,16 @@ struct Seq {
     }
 };
 
-// act and its slope at z
-template <bool SLOPE>
-__device__ __forceinline__ float act(bool silu, float z, float& slope) {
-    slope = 1.f;
-    if (!silu) return z;
+// act and its slope
+template <bool SILU>
+__device__ __forceinline__ float act(float z) {
+    return SILU ? z * BlockSigmoid(z).s : z;
+}
+template <bool SILU>
+__device__ __forceinline__ float slope(float z) {
+    if (!SILU) return 1.f;
     const BlockSigmoid g(z);
-    if (SLOPE) slope = g.s * (1.f + z * g.rest);
-    return z * g.s;
+    return g.s * fmaf(z, g.rest, 1.f);
 }
 
 }  // namespace
@@ -106,22 +104,23 @@ __device__ __forceinline__ void fetch(const void* p, int64_t row0, int t, int en
     for (int i = 0; i < n; ++i) r[i] = S::load(p, (row0 + min(t + i, end - 1)) * C + c);
 }
 
-template <class T, int W>
+// Four tokens that are all inside of one sequence, not its last among them, are straight
+// code over what was loaded ahead; the others go one by one, with loads of their own.
+template <class T, int W, bool SILU>
 __global__ __launch_bounds__(SC_THREADS) void short_conv_fwd_kernel(ConvArgs a) {
-    typedef FwdSlice<T> S;
+    typedef Pair<T> S;
     constexpr int V = S::N, CB = 64 * V;
-    const int blocks = (a.C + CB - 1) / CB;
-    const int64_t wg = (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
+    const uint32_t blocks = (a.C + CB - 1) / CB;
+    const uint32_t wg = blockIdx.z * gridDim.x + blockIdx.x;
     if (wg >= a.groups * blocks) return copy_empty<T>(a, wg - a.groups * blocks, W - 1, a.h0, a.h_final);
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int per_row = (a.T + a.strip - 1) / a.strip;
-    const int64_t strip = wg / blocks * SC_WAVES + w;
-    const int b = (int)(strip / per_row);
+    const uint32_t per_row = (a.T + a.strip - 1) / a.strip, strip = wg / blocks * SC_WAVES + w;
+    const int b = strip / max(per_row, 1u);
     const int c = ((int)(wg % blocks) * 64 + (threadIdx.x & 63)) * V;
     if (b >= a.B || c >= a.C) return;
-    const int t0 = (int)(strip % per_row) * a.strip, t1 = min(t0 + a.strip, a.T);
+    const int t0 = strip % per_row * a.strip, t1 = min(t0 + a.strip, a.T);
     const int64_t row0 = (int64_t)b * a.T;
-    typename S::raw next[SC_FWD_BATCH];
+    typename S::raw next[SC_BATCH];
     fetch<S>(a.x, row0, t0, t1, a.C, c, next);
     float wt[W][V], bias[V];
 #pragma unroll
@@ -132,20 +131,48 @@ __global__ __launch_bounds__(SC_THREADS) void short_conv_fwd_kernel(ConvArgs a) 
     }
     Seq q;
     q.find(a, b, t0);
-    float win[W][V];
+    float win[W - 1][V];  // x of the W - 1 tokens before
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) win[j][v] = 0.f;
     if (t0 > q.s && t0 < q.e) {
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) window_row<S, W>(a, q, row0, t0, j, c, win[j]);
     }
-    for (int tb = t0; tb < t1; tb += SC_FWD_BATCH) {
-        typename S::raw rx[SC_FWD_BATCH];
+    for (int tb = t0; tb < t1; tb += SC_BATCH) {
+        typename S::raw rx[SC_BATCH];
 #pragma unroll
-        for (int i = 0; i < SC_FWD_BATCH; ++i) rx[i] = next[i];
-        if (tb + SC_FWD_BATCH < t1) fetch<S>(a.x, row0, tb + SC_FWD_BATCH, t1, a.C, c, next);
+        for (int i = 0; i < SC_BATCH; ++i) rx[i] = next[i];
+        if (tb + SC_BATCH < t1) fetch<S>(a.x, row0, tb + SC_BATCH, t1, a.C, c, next);
+        if (tb >= q.e) q.next(a, tb);
+        if (tb > q.s && tb + SC_BATCH < q.e && tb + SC_BATCH <= t1) {
+            float x[SC_BATCH + W - 1][V];
 #pragma unroll
-        for (int i = 0; i < SC_FWD_BATCH; ++i) {
-            const int t = tb + i;
-            if (t >= t1) break;
+            for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v) x[j][v] = win[j][v];
+#pragma unroll
+            for (int i = 0; i < SC_BATCH; ++i) S::unpack(rx[i], x[W - 1 + i]);
+#pragma unroll
+            for (int i = 0; i < SC_BATCH; ++i) {
+                float y[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float z = bias[v];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) z = fmaf(wt[j][v], x[i + j][v], z);
+                    y[v] = act<SILU>(z);
+                }
+                S::store(a.y, (row0 + tb + i) * a.C + c, y);
+            }
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v) win[j][v] = x[SC_BATCH + j][v];
+            continue;
+        }
+        for (int t = tb; t < min(tb + SC_BATCH, t1); ++t) {
             if (t >= q.e) q.next(a, t);
             if (t == q.s) {
 #pragma unroll
@@ -153,15 +180,17 @@ __global__ __launch_bounds__(SC_THREADS) void short_conv_fwd_kernel(ConvArgs a) 
             }
             float y[V];
             if (t >= q.s && t < q.e) {
-                S::unpack(rx[i], win[W - 1]);
+                float x[V];
+                S::load(a.x, (row0 + t) * a.C + c, x);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    float z = bias[v], slope;
+                    float z = bias[v];
 #pragma unroll
-                    for (int j = 0; j < W; ++j) z = fmaf(wt[j][v], win[j][v], z);
-                    y[v] = act<false>(a.silu, z, slope);
+                    for (int j = 0; j < W - 1; ++j) z = fmaf(wt[j][v], win[j][v], z);
+                    y[v] = act<SILU>(fmaf(wt[W - 1][v], x[v], z));
 #pragma unroll
-                    for (int j = 0; j < W - 1; ++j) win[j][v] = win[j + 1][v];
+                    for (int j = 0; j < W - 2; ++j) win[j][v] = win[j + 1][v];
+                    win[W - 2][v] = x[v];
                 }
                 if (a.h_final && t == q.e - 1) {
 #pragma unroll
@@ -177,19 +206,17 @@ __global__ __launch_bounds__(SC_THREADS) void short_conv_fwd_kernel(ConvArgs a) 
     }
 }
 
-template <class T, int W>
-__global__ __launch_bounds__(SC_THREADS) void short_conv_bwd_kernel(ConvArgs a) {
-    typedef BwdSlice<T> S;
+template <class T, int W, bool SILU>
+__global__ __launch_bounds__(SC_THREADS, 4) void short_conv_bwd_kernel(ConvArgs a) {
+    typedef Pair<T> S;
     constexpr int V = S::N, CB = 64 * V;
     __shared__ float red[SC_WAVES][W + 1][V][64];
-    const int blocks = (a.C + CB - 1) / CB;
-    const int64_t wg = (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
-    const int64_t group = wg / blocks;
+    const uint32_t blocks = (a.C + CB - 1) / CB;
+    const uint32_t wg = blockIdx.z * gridDim.x + blockIdx.x, group = wg / blocks;
     if (group >= a.groups) return copy_empty<T>(a, wg - a.groups * blocks, W - 1, a.d_final, a.dh0);
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int per_row = (a.T + a.strip - 1) / a.strip;
-    const int64_t strip = group * SC_WAVES + w;
-    const int b = (int)(strip / per_row);
+    const uint32_t per_row = (a.T + a.strip - 1) / a.strip, strip = group * SC_WAVES + w;
+    const int b = strip / max(per_row, 1u);
     const int c = ((int)(wg % blocks) * 64 + lane) * V;
     float dw[W + 1][V];
 #pragma unroll
@@ -197,10 +224,10 @@ __global__ __launch_bounds__(SC_THREADS) void short_conv_bwd_kernel(ConvArgs a) 
 #pragma unroll
         for (int v = 0; v < V; ++v) dw[j][v] = 0.f;
     if (b < a.B && c < a.C) {
-        const int t0 = (int)(strip % per_row) * a.strip, t1 = min(t0 + a.strip, a.T);
+        const int t0 = strip % per_row * a.strip, t1 = min(t0 + a.strip, a.T);
         const int64_t row0 = (int64_t)b * a.T;
         const int end = min(t1 + W - 1, a.T);
-        typename S::raw next_x[SC_BWD_BATCH], next_y[SC_BWD_BATCH];
+        typename S::raw next_x[SC_BATCH], next_y[SC_BATCH];
         fetch<S>(a.x, row0, t0, end, a.C, c, next_x);
         fetch<S>(a.dy, row0, t0, end, a.C, c, next_y);
         float wt[W][V], bias[V];
@@ -212,11 +239,12 @@ __global__ __launch_bounds__(SC_THREADS) void short_conv_bwd_kernel(ConvArgs a) 
         }
         Seq q;
         q.find(a, b, t0);
-        float win[W][V], acc[W][V];  // acc[k]: the gradient of x_{t - k} so far
+        // of the W - 1 tokens before: x, and the gradient of x so far
+        float win[W - 1][V], pend[W - 1][V];
 #pragma unroll
-        for (int k = 0; k < W; ++k)
+        for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-            for (int v = 0; v < V; ++v) acc[k][v] = 0.f;
+            for (int v = 0; v < V; ++v) win[j][v] = pend[j][v] = 0.f;
         // the gradient of place p of the sequence: a token's, or a row of its state's
         const auto emit = [&](int p, const float* f) {
             if (p >= q.s) {
@@ -229,21 +257,74 @@ __global__ __launch_bounds__(SC_THREADS) void short_conv_bwd_kernel(ConvArgs a) 
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) window_row<S, W>(a, q, row0, t0, j, c, win[j]);
         }
-        for (int tb = t0; tb < end; tb += SC_BWD_BATCH) {
-            typename S::raw rx[SC_BWD_BATCH], ry[SC_BWD_BATCH];
+        for (int tb = t0; tb < end; tb += SC_BATCH) {
+            typename S::raw rx[SC_BATCH], ry[SC_BATCH];
 #pragma unroll
-            for (int i = 0; i < SC_BWD_BATCH; ++i) {
+            for (int i = 0; i < SC_BATCH; ++i) {
                 rx[i] = next_x[i];
                 ry[i] = next_y[i];
             }
-            if (tb + SC_BWD_BATCH < end) {
-                fetch<S>(a.x, row0, tb + SC_BWD_BATCH, end, a.C, c, next_x);
-                fetch<S>(a.dy, row0, tb + SC_BWD_BATCH, end, a.C, c, next_y);
+            if (tb + SC_BATCH < end) {
+                fetch<S>(a.x, row0, tb + SC_BATCH, end, a.C, c, next_x);
+                fetch<S>(a.dy, row0, tb + SC_BATCH, end, a.C, c, next_y);
             }
+            if (tb >= q.e) q.next(a, tb);
+            // (a batch behind the strip may have tokens from `end` on: their part is of
+            // places that are not this strip's)
+            if (tb >= q.s + W && tb + SC_BATCH < q.e && (tb >= t1 || tb + SC_BATCH <= t1)) {
+                float x[SC_BATCH + W - 1][V], dx[SC_BATCH + W - 1][V], dz[SC_BATCH][V];
 #pragma unroll
-            for (int i = 0; i < SC_BWD_BATCH; ++i) {
-                const int t = tb + i;
-                if (t >= end) break;
+                for (int v = 0; v < V; ++v) {
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j) {
+                        x[j][v] = win[j][v];
+                        dx[j][v] = pend[j][v];
+                    }
+#pragma unroll
+                    for (int j = W - 1; j < SC_BATCH + W - 1; ++j) dx[j][v] = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < SC_BATCH; ++i) {
+                    S::unpack(rx[i], x[W - 1 + i]);
+                    S::unpack(ry[i], dz[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < SC_BATCH; ++i) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        float z = bias[v];
+#pragma unroll
+                        for (int j = 0; j < W; ++j) z = fmaf(wt[j][v], x[i + j][v], z);
+                        dz[i][v] *= slope<SILU>(z);
+#pragma unroll
+                        for (int j = 0; j < W; ++j) dx[i + j][v] = fmaf(wt[j][v], dz[i][v], dx[i + j][v]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < SC_BATCH; ++i) {
+                    const int p = tb + i - (W - 1);
+                    if (p >= t0 && p < t1) S::store(a.dx, (row0 + p) * a.C + c, dx[i]);
+                }
+                if (tb < t1) {
+#pragma unroll
+                    for (int i = 0; i < SC_BATCH; ++i)
+#pragma unroll
+                        for (int v = 0; v < V; ++v) {
+#pragma unroll
+                            for (int j = 0; j < W; ++j) dw[j][v] = fmaf(dz[i][v], x[i + j][v], dw[j][v]);
+                            dw[W][v] += dz[i][v];
+                        }
+                }
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        win[j][v] = x[SC_BATCH + j][v];
+                        pend[j][v] = dx[SC_BATCH + j][v];
+                    }
+                continue;
+            }
+            for (int t = tb; t < min(tb + SC_BATCH, end); ++t) {
                 if (t >= q.e) q.next(a, t);
                 if (t == q.s) {
 #pragma unroll
@@ -256,46 +337,44 @@ __global__ __launch_bounds__(SC_THREADS) void short_conv_bwd_kernel(ConvArgs a) 
                     }
                     continue;
                 }
-                float dz[V];
-                S::unpack(rx[i], win[W - 1]);
-                S::unpack(ry[i], dz);
+                float x[V], dz[V], done[V];
+                S::load(a.x, (row0 + t) * a.C + c, x);
+                S::load(a.dy, (row0 + t) * a.C + c, dz);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    float z = bias[v], slope;
+                    float z = bias[v];
 #pragma unroll
-                    for (int j = 0; j < W; ++j) z = fmaf(wt[j][v], win[j][v], z);
-                    act<true>(a.silu, z, slope);
-                    dz[v] *= slope;
+                    for (int j = 0; j < W - 1; ++j) z = fmaf(wt[j][v], win[j][v], z);
+                    dz[v] *= slope<SILU>(fmaf(wt[W - 1][v], x[v], z));
                     if (t < t1) {
 #pragma unroll
-                        for (int j = 0; j < W; ++j) dw[j][v] = fmaf(dz[v], win[j][v], dw[j][v]);
+                        for (int j = 0; j < W - 1; ++j) dw[j][v] = fmaf(dz[v], win[j][v], dw[j][v]);
+                        dw[W - 1][v] = fmaf(dz[v], x[v], dw[W - 1][v]);
                         dw[W][v] += dz[v];
                     }
+                    done[v] = fmaf(wt[0][v], dz[v], pend[0][v]);
 #pragma unroll
-                    for (int k = 0; k < W; ++k) acc[k][v] = fmaf(wt[W - 1 - k][v], dz[v], acc[k][v]);
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j) win[j][v] = win[j + 1][v];
+                    for (int j = 0; j < W - 2; ++j) {
+                        win[j][v] = win[j + 1][v];
+                        pend[j][v] = fmaf(wt[j + 1][v], dz[v], pend[j + 1][v]);
+                    }
+                    win[W - 2][v] = x[v];
+                    pend[W - 2][v] = wt[W - 1][v] * dz[v];
                 }
-                emit(t - (W - 1), acc[W - 1]);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-#pragma unroll
-                    for (int k = W - 1; k > 0; --k) acc[k][v] = acc[k - 1][v];
-                    acc[0][v] = 0.f;
-                }
+                emit(t - (W - 1), done);
                 if (t == q.e - 1) {
                     // the last places, and what comes back through the state left behind
 #pragma unroll
-                    for (int k = W - 1; k > 0; --k) {
+                    for (int j = 0; j < W - 1; ++j) {
                         if (a.d_final) {
                             float df[V];
-                            S::load(a.d_final, ((int64_t)q.n * (W - 1) + (W - 1 - k)) * a.C + c, df);
+                            S::load(a.d_final, ((int64_t)q.n * (W - 1) + j) * a.C + c, df);
 #pragma unroll
-                            for (int v = 0; v < V; ++v) acc[k][v] += df[v];
+                            for (int v = 0; v < V; ++v) pend[j][v] += df[v];
                         }
-                        emit(t + 1 - k, acc[k]);
+                        emit(t + 1 - (W - 1) + j, pend[j]);
 #pragma unroll
-                        for (int v = 0; v < V; ++v) acc[k][v] = 0.f;
+                        for (int v = 0; v < V; ++v) pend[j][v] = 0.f;
                     }
                 }
             }
@@ -311,7 +390,7 @@ __global__ __launch_bounds__(SC_THREADS) void short_conv_bwd_kernel(ConvArgs a) 
         if (ch >= a.C) continue;
         float s = 0.f;
         for (int k = 0; k < SC_WAVES; ++k) s += red[k][j][v][l];
-        a.part[(group * (W + 1) + j) * a.C + ch] = s;
+        a.part[((int64_t)group * (W + 1) + j) * a.C + ch] = s;
     }
 }
 
@@ -325,7 +404,7 @@ __global__ __launch_bounds__(256) void short_conv_sum_kernel(ConvArgs a) {
     if (threadIdx.x < 32 && c < a.C) (j < W ? a.dweight + (int64_t)c * W + j : a.dbias + c)[0] = (float)s;
 }
 
-template <class T, int W>
+template <class T, int W, bool SILU>
 __global__ __launch_bounds__(256) void short_conv_decode_kernel(ConvDecodeArgs a) {
     constexpr int V = Slice<T>::N;
     const int64_t per_row = a.C / V;
@@ -339,10 +418,10 @@ __global__ __launch_bounds__(256) void short_conv_decode_kernel(ConvDecodeArgs a
     Slice<T>::load(a.x, n * a.C + c, win[W - 1]);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        float z = a.bias ? a.bias[c + v] : 0.f, slope;
+        float z = a.bias ? a.bias[c + v] : 0.f;
 #pragma unroll
         for (int j = 0; j < W; ++j) z = fmaf(a.weight[(int64_t)(c + v) * W + j], win[j][v], z);
-        y[v] = act<false>(a.silu, z, slope);
+        y[v] = act<SILU>(z);
     }
     Slice<T>::store(a.y, n * a.C + c, y);
 #pragma unroll
@@ -352,8 +431,11 @@ __global__ __launch_bounds__(256) void short_conv_decode_kernel(ConvDecodeArgs a
 namespace {
 
 template <class F>
-void by_taps(int W, bool fp32, F&& f) {
-    const auto with = [&](auto w) { fp32 ? f(float{}, w) : f(uint16_t{}, w); };
+void by_taps(int W, bool fp32, bool silu, F&& f) {
+    const auto with = [&](auto w) {
+        const auto type = [&](auto s) { fp32 ? f(float{}, w, s) : f(uint16_t{}, w, s); };
+        silu ? type(std::true_type{}) : type(std::false_type{});
+    };
     switch (W) {
         case 2: return with(std::integral_constant<int, 2>{});
         case 3: return with(std::integral_constant<int, 3>{});
@@ -361,69 +443,68 @@ void by_taps(int W, bool fp32, F&& f) {
     }
 }
 
-template <class S>
-int64_t channel_blocks(int32_t C) {
-    return (C + 64 * S::N - 1) / (64 * S::N);
+// Tokens of a strip, 16 or 32.  The gradients read W - 1 tokens more than a strip has, and
+// leave a row of sums for four strips; bf16 calls that fill the GPU with strips of 32 gain
+// by them (32768 tokens of 4096 channels: 185 us, 204 with 16; 2048 tokens: 24 and 22), fp32
+// calls do not (339 and 309), nor does the forward pass (113 and 106).
+int strip_of(int32_t B, int32_t T, int64_t blocks, bool fp32, bool backward) {
+    return backward && !fp32 && (int64_t)B * ((T + 31) / 32) * blocks >= 16 * 256 ? 32 : 16;
 }
 
-// Tokens of a strip: 32, or 16 where that leaves fewer than eight waves to a CU.
-#ifndef SC_LONG
-#define SC_LONG 32
-#define SC_SHORT 16
-#endif
-int strip_of(int32_t B, int32_t T, int64_t blocks) {
-    return (int64_t)B * ((T + SC_LONG - 1) / SC_LONG) * blocks < 8 * 256 ? SC_SHORT : SC_LONG;
-}
+int64_t channel_blocks(int32_t C) { return (C + 127) / 128; }
 
 int64_t groups_of(int32_t B, int32_t T, int strip) {
-    const int64_t strips = (int64_t)B * ((T + strip - 1) / strip);
+    const int64_t strips = (int64_t)B * (((int64_t)T + strip - 1) / strip);
     return (strips + SC_WAVES - 1) / SC_WAVES;
 }
 
 // strips, and the sequences that may be empty behind them
-template <class S>
-dim3 grid_of(ConvArgs& a, const void* state) {
-    const int64_t blocks = channel_blocks<S>(a.C);
-    a.strip = strip_of(a.B, a.T, blocks);
-    a.groups = groups_of(a.B, a.T, a.strip);
+dim3 grid_of(ConvArgs& a, bool fp32, bool backward, const void* state) {
+    const int64_t blocks = channel_blocks(a.C);
+    a.strip = strip_of(a.B, a.T, blocks, fp32, backward);
+    a.groups = (uint32_t)groups_of(a.B, a.T, a.strip);
     return wide_grid(a.groups * blocks + (state && (a.cu || a.T == 0) ? a.N : 0), SC_THREADS);
 }
 
 }  // namespace
 
 int64_t short_conv_groups(int32_t B, int32_t T, int32_t C, bool fp32) {
-    return groups_of(
-        B, T, strip_of(B, T, fp32 ? channel_blocks<BwdSlice<float>>(C) : channel_blocks<BwdSlice<uint16_t>>(C)));
+    return groups_of(B, T, strip_of(B, T, channel_blocks(C), fp32, true));
+}
+
+int64_t short_conv_workgroups(int32_t B, int32_t T, int32_t C, int32_t N) {
+    return groups_of(B, T, 16) * channel_blocks(C) + N;
 }
 
 void launch_short_conv_fwd(const ConvArgs& args, int W, bool fp32, hipStream_t stream) {
     ConvArgs a = args;
     if (a.T == 0 && !a.h_final) return;
-    by_taps(W, fp32, [&](auto t, auto w) {
-        using T = decltype(t);
-        const dim3 grid = grid_of<FwdSlice<T>>(a, a.h_final);
-        hipLaunchKernelGGL((short_conv_fwd_kernel<T, decltype(w)::value>), grid, dim3(SC_THREADS), 0, stream, a);
+    const dim3 grid = grid_of(a, fp32, false, a.h_final);
+    by_taps(W, fp32, a.silu, [&](auto t, auto w, auto silu) {
+        hipLaunchKernelGGL((short_conv_fwd_kernel<decltype(t), decltype(w)::value, decltype(silu)::value>), grid,
+                           dim3(SC_THREADS), 0, stream, a);
     });
 }
 
 void launch_short_conv_bwd(const ConvArgs& args, int W, bool fp32, hipStream_t stream) {
     ConvArgs a = args;
-    by_taps(W, fp32, [&](auto t, auto w) {
-        using T = decltype(t);
+    const dim3 grid = grid_of(a, fp32, true, a.dh0);
+    by_taps(W, fp32, a.silu, [&](auto t, auto w, auto silu) {
         constexpr int TAPS = decltype(w)::value;
-        const dim3 grid = grid_of<BwdSlice<T>>(a, a.dh0);
         if (a.T > 0 || a.dh0)
-            hipLaunchKernelGGL((short_conv_bwd_kernel<T, TAPS>), grid, dim3(SC_THREADS), 0, stream, a);
+            hipLaunchKernelGGL((short_conv_bwd_kernel<decltype(t), TAPS, decltype(silu)::value>), grid,
+                               dim3(SC_THREADS), 0, stream, a);
         hipLaunchKernelGGL(short_conv_sum_kernel<TAPS>, dim3((unsigned)((a.C + 31) / 32 * (TAPS + 1))), dim3(256), 0,
                            stream, a);
     });
 }
 
 void launch_short_conv_decode(const ConvDecodeArgs& a, int W, bool fp32, hipStream_t stream) {
-    by_taps(W, fp32, [&](auto t, auto w) {
+    by_taps(W, fp32, a.silu, [&](auto t, auto w, auto silu) {
+        constexpr bool SILU = decltype(silu)::value;
         using T = decltype(t);
         const int64_t lanes = (int64_t)a.N * (a.C / Slice<T>::N);
-        hipLaunchKernelGGL((short_conv_decode_kernel<T, decltype(w)::value>), wide_grid((lanes + 255) / 256, 256),
+        hipLaunchKernelGGL((short_conv_decode_kernel<T, decltype(w)::value, SILU>), wide_grid((lanes + 255) / 256, 256),
                            dim3(256), 0, stream, a);
     });
 }

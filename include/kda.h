@@ -586,7 +586,8 @@ int gated_scan_decode(const void* x, const void* g, const void* input_gate, cons
  * x, y [B, T, C] tokens; weight [C, W], bias [C] (NULL: none) fp32; states
  * [N, W - 1, C] tokens: the last W - 1 tokens, the oldest first (initial_state:
  * those in front of a sequence, NULL: zeros; final_state: those behind it, NULL:
- * not written).  activation: KDA_CONV_NONE or KDA_CONV_SILU. */
+ * not written).  activation: KDA_CONV_NONE or KDA_CONV_SILU.
+ * ceil(B ceil(T / 16) / 4) ceil(C / 128) + N < 2^31. */
 enum kda_conv_activation { KDA_CONV_NONE = 0, KDA_CONV_SILU = 1 };
 
 int short_conv_fwd(const void* x, const float* weight, const float* bias, int32_t activation,

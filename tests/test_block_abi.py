@@ -67,7 +67,7 @@ def test_gated_scan_decode_rejects_on_host(lib, over, code):
 CONV = dict(x=FAKE, w=FAKE, b=None, act=1, h0=None, hT=None, cu=None, N=1, dtype=0, B=1, T=16, C=64, W=4, y=FAKE,
             stream=None)
 CONV_ONLY = [(dict(w=None), 1), (dict(w=odd(2)), 1), (dict(b=odd(2)), 1), (dict(act=2), 1), (dict(act=-1), 1),
-             (dict(W=1), 2), (dict(W=5), 2)]
+             (dict(W=1), 2), (dict(W=5), 2), (dict(B=1 << 23, T=64, C=1 << 15), 1)]
 
 
 @pytest.mark.parametrize("over,code", SIZES + CONV_ONLY + [(dict(y=None), 1), (dict(y=odd(8)), 1),
@@ -91,7 +91,7 @@ def test_short_conv_bwd_rejects_on_host(lib, over, code):
 CONV_TOK = dict(x=FAKE, w=FAKE, b=None, act=1, s_in=FAKE, s_out=FAKE, dtype=0, N=2, C=64, W=4, y=FAKE, stream=None)
 
 
-@pytest.mark.parametrize("over,code", CONV_ONLY + [({n: None}, 1) for n in ("x", "s_in", "s_out", "y")] + [
+@pytest.mark.parametrize("over,code", CONV_ONLY[:-1] + [({n: None}, 1) for n in ("x", "s_in", "s_out", "y")] + [
     ({n: odd(8)}, 1) for n in ("x", "s_in", "s_out", "y")] + [(dict(N=0), 1), (dict(C=4), 2), (dict(dtype=2), 1)])
 def test_short_conv_decode_rejects_on_host(lib, over, code):
     assert call(lib.short_conv_decode, CONV_TOK, over) == code
@@ -143,6 +143,7 @@ def test_sizes(lib):
     assert kda.gated_scan_workspace_size(2, 100, 64, packed=True) == 0
     assert kda.gated_scan_workspace_size(2, 257, 64) >= 2 * 3 * 64 * 8
     assert kda.gated_scan_workspace_size(2, 257, 64, True) >= 2 * 5 * 64 * 8 + 2 * 5 * 2 * 64 * 4
+    assert lib.short_conv_bwd_workspace_size(0, 1 << 23, 64, 1 << 15, 4) == 0  # workgroups
     assert lib.short_conv_bwd_workspace_size(0, 1, 1, 64, 5) == lib.short_conv_bwd_workspace_size(2, 1, 1, 64, 4) == 0
     assert lib.layer_norm_bwd_workspace_size(0, 5, 12) == lib.layer_norm_bwd_workspace_size(3, 5, 64) == 0
     assert lib.layer_norm_bwd_workspace_size(0, 1 << 31, 64) == lib.layer_norm_bwd_workspace_size(1, 5, 16392) == 0
