@@ -30,7 +30,8 @@ __device__ __forceinline__ int clamp_tok(int v, int T) { return min(max(v, 0), T
 // The sequence that a strip's token belongs to: tokens [s, e) of its row of the batch.
 struct Seq {
     int n, s, e;
-    // the last sequence that begins at or before t (an empty one at T if none does)
+    // the last sequence that begins at or before t (-1: none does), 64 candidates at a time:
+    // all lanes of the wave have to be there
     __device__ __forceinline__ void find(const ConvArgs& a, int b, int t) {
         if (!a.cu) {
             n = b;
@@ -38,13 +39,20 @@ struct Seq {
             e = a.T;
             return;
         }
-        int lo = 0, hi = a.N;
-        while (lo < hi) {
-            const int mid = lo + (hi - lo) / 2;
-            if (clamp_tok(a.cu[mid], a.T) <= t) lo = mid + 1;
-            else hi = mid;
-        }
-        set(a, lo - 1);
+        const int lane = threadIdx.x & 63;
+        int lo = 0, count = a.N, step;
+        do {
+            step = (count + 63) / 64;
+            const int i = lane * step;
+            const int before = __popcll(__ballot(i < count && clamp_tok(a.cu[min(lo + i, a.N)], a.T) <= t));
+            if (before == 0) {
+                lo = -1;
+                break;
+            }
+            lo += (before - 1) * step;
+            count = min(step, count - (before - 1) * step);
+        } while (step > 1);
+        set(a, lo);
     }
     __device__ __forceinline__ void set(const ConvArgs& a, int i) {
         n = i;
@@ -117,8 +125,11 @@ __global__ __launch_bounds__(SC_THREADS) void short_conv_fwd_kernel(ConvArgs a) 
     const uint32_t per_row = (a.T + a.strip - 1) / a.strip, strip = wg / blocks * SC_WAVES + w;
     const int b = strip / max(per_row, 1u);
     const int c = ((int)(wg % blocks) * 64 + (threadIdx.x & 63)) * V;
-    if (b >= a.B || c >= a.C) return;
+    if (b >= a.B) return;
     const int t0 = strip % per_row * a.strip, t1 = min(t0 + a.strip, a.T);
+    Seq q;
+    q.find(a, b, t0);
+    if (c >= a.C) return;
     const int64_t row0 = (int64_t)b * a.T;
     typename S::raw next[SC_BATCH];
     fetch<S>(a.x, row0, t0, t1, a.C, c, next);
@@ -129,8 +140,6 @@ __global__ __launch_bounds__(SC_THREADS) void short_conv_fwd_kernel(ConvArgs a) 
 #pragma unroll
         for (int j = 0; j < W; ++j) wt[j][v] = a.weight[(int64_t)(c + v) * W + j];
     }
-    Seq q;
-    q.find(a, b, t0);
     float win[W - 1][V];  // x of the W - 1 tokens before
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
@@ -223,8 +232,10 @@ __global__ __launch_bounds__(SC_THREADS, 4) void short_conv_bwd_kernel(ConvArgs 
     for (int j = 0; j <= W; ++j)
 #pragma unroll
         for (int v = 0; v < V; ++v) dw[j][v] = 0.f;
+    const int t0 = strip % max(per_row, 1u) * a.strip, t1 = min(t0 + a.strip, a.T);
+    Seq q;
+    if (b < a.B) q.find(a, b, t0);
     if (b < a.B && c < a.C) {
-        const int t0 = strip % per_row * a.strip, t1 = min(t0 + a.strip, a.T);
         const int64_t row0 = (int64_t)b * a.T;
         const int end = min(t1 + W - 1, a.T);
         typename S::raw next_x[SC_BATCH], next_y[SC_BATCH];
@@ -237,8 +248,6 @@ __global__ __launch_bounds__(SC_THREADS, 4) void short_conv_bwd_kernel(ConvArgs 
 #pragma unroll
             for (int j = 0; j < W; ++j) wt[j][v] = a.weight[(int64_t)(c + v) * W + j];
         }
-        Seq q;
-        q.find(a, b, t0);
         // of the W - 1 tokens before: x, and the gradient of x so far
         float win[W - 1][V], pend[W - 1][V];
 #pragma unroll
@@ -445,10 +454,10 @@ void by_taps(int W, bool fp32, bool silu, F&& f) {
 
 // Tokens of a strip, 16 or 32.  The gradients read W - 1 tokens more than a strip has, and
 // leave a row of sums for four strips; bf16 calls that fill the GPU with strips of 32 gain
-// by them (32768 tokens of 4096 channels: 185 us, 204 with 16; 2048 tokens: 24 and 22), fp32
-// calls do not (339 and 309), nor does the forward pass (113 and 106).
+// by them (32768 tokens of 4096 channels: 182 us, 204 with 16; 2048 tokens: 24 and 22), fp32
+// calls do not (338 and 311), nor does the forward pass (109 and 108).
 int strip_of(int32_t B, int32_t T, int64_t blocks, bool fp32, bool backward) {
-    return backward && !fp32 && (int64_t)B * ((T + 31) / 32) * blocks >= 16 * 256 ? 32 : 16;
+        return backward && !fp32 && (int64_t)B * ((T + 31) / 32) * blocks >= 16 * 256 ? 32 : 16;
 }
 
 int64_t channel_blocks(int32_t C) { return (C + 127) / 128; }
