@@ -111,27 +111,66 @@ __device__ __forceinline__ Stats row_stats(float (&u)[M], int count, int D, floa
 
 }  // namespace
 
+// The weights of a lane's slices of V channels: in registers, or read again for every row
+// (from L2) where a lane has more than 16 channels, or a workgroup of 1024 threads leaves it
+// 128 registers.
+template <int K, int V, bool KEEP>
+struct Weights {
+    float w[KEEP ? K * V : 1];
+    const float* p;
+    __device__ __forceinline__ explicit Weights(const float* q) : p(q) {}
+    __device__ __forceinline__ void read(int c, float* f) const {
+        typedef float four __attribute__((ext_vector_type(4), aligned(4)));
+#pragma unroll
+        for (int v = 0; v < V; v += 4) {
+            const four q = *reinterpret_cast<const four*>(p + c + v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[v + e] = q[e];
+        }
+    }
+    // slice k, which begins at channel c
+    __device__ __forceinline__ void keep(int k, int c, bool there) {
+        if constexpr (KEEP) {
+            if (there && p) {
+                read(c, w + k * V);
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) w[k * V + v] = 0.f;
+            }
+        }
+    }
+    // (the compiler would read them ahead of the rows, and spill them)
+    __device__ __forceinline__ void next_row() {
+        if constexpr (!KEEP) asm volatile("" : "+s"(p));
+    }
+    __device__ __forceinline__ void get(int k, int c, float* f) const {
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) f[v] = w[k * V + v];
+        } else if (p) {
+            read(c, f);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) f[v] = 0.f;
+        }
+    }
+};
+
 // K slices of a row in each of its L lanes, the workgroup's rows one after the other.  The
-// weights stay in registers and the next row's loads are under way while this one is
-// summed, but in workgroups of 1024 threads, whose 128 registers a lane they do not fit.
+// next row's loads are under way while this one is summed.
 template <class T, int L, int K>
 __global__ __launch_bounds__(L > LN_THREADS ? L : LN_THREADS) void layer_norm_fwd_kernel(LayerNormArgs a) {
     constexpr int V = Slice<T>::N, THREADS = L > LN_THREADS ? L : LN_THREADS, RPW = THREADS / L;
-    constexpr bool AHEAD = THREADS < 1024;
+    constexpr bool KEEP = K * V <= 16 && THREADS < 1024;
     const int l = threadIdx.x % L;
-    float wt[K * V], bias[K * V];
+    Weights<K, V, KEEP> wt(a.weight), bias(a.bias);
     int count = 0;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int c = (k * L + l) * V;
         if (c < a.D) count = (k + 1) * V;
-        if constexpr (AHEAD) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                wt[k * V + v] = c < a.D ? a.weight[c + v] : 0.f;
-                bias[k * V + v] = c < a.D && a.bias ? a.bias[c + v] : 0.f;
-            }
-        }
+        wt.keep(k, c, c < a.D);
+        bias.keep(k, c, c < a.D);
     }
     const int64_t step = (int64_t)a.groups * RPW;
     int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / L;
@@ -146,11 +185,12 @@ __global__ __launch_bounds__(L > LN_THREADS ? L : LN_THREADS) void layer_norm_fw
             }
         }
     };
-    if (AHEAD && row < a.rows) fetch(row);
+    if (row < a.rows) fetch(row);
     for (; row < a.rows; row += step) {
         const int64_t at = row * a.D;
         float u[K * V];
-        if (!AHEAD) fetch(row);
+        wt.next_row();
+        bias.next_row();
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (k * L + l) * V;
@@ -169,42 +209,41 @@ __global__ __launch_bounds__(L > LN_THREADS ? L : LN_THREADS) void layer_norm_fw
                 for (int v = 0; v < V; ++v) u[k * V + v] = 0.f;
             }
         }
-        if (AHEAD && row + step < a.rows) fetch(row + step);
+        if (row + step < a.rows) fetch(row + step);
         const Stats s = row_stats<L, K * V>(u, count, a.D, a.eps);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (k * L + l) * V;
             if (c < a.D) {
-                float y[V];
+                float y[V], q[V], d[V];
+                wt.get(k, c, q);
+                bias.get(k, c, d);
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float n = ((u[k * V + v] - s.mean) - s.rest) * s.rho;
-                    if constexpr (AHEAD) y[v] = fmaf(n, wt[k * V + v], bias[k * V + v]);
-                    else y[v] = fmaf(n, a.weight[c + v], a.bias ? a.bias[c + v] : 0.f);
-                }
+                for (int v = 0; v < V; ++v)
+                    y[v] = fmaf(((u[k * V + v] - s.mean) - s.rest) * s.rho, q[v], d[v]);
                 Slice<T>::store(a.y, at + c, y);
             }
         }
     }
 }
 
+// (In workgroups of 1024 threads the next row's loads do not fit beside the sums.)
 template <class T, int L, int K>
 __global__ __launch_bounds__(L > LN_THREADS ? L : LN_THREADS) void layer_norm_bwd_kernel(LayerNormArgs a) {
     constexpr int V = Slice<T>::N, THREADS = L > LN_THREADS ? L : LN_THREADS, RPW = THREADS / L;
-    constexpr bool AHEAD = THREADS < 1024;
+    constexpr bool KEEP = K * V <= 16 && THREADS < 1024, AHEAD = THREADS < 1024;
     __shared__ float red_t[2][16];
     const int l = threadIdx.x % L;
-    float dw[K * V], db[K * V], wt[K * V];
+    float dw[K * V], db[K * V];
+    Weights<K, V, KEEP> wt(a.weight);
     int count = 0;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int c = (k * L + l) * V;
         if (c < a.D) count = (k + 1) * V;
+        wt.keep(k, c, c < a.D);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            dw[k * V + v] = db[k * V + v] = 0.f;
-            if constexpr (AHEAD) wt[k * V + v] = c < a.D ? a.weight[c + v] : 0.f;
-        }
+        for (int v = 0; v < V; ++v) dw[k * V + v] = db[k * V + v] = 0.f;
     }
     const float inv = 1.f / (float)a.D;
     const int64_t step = (int64_t)a.groups * RPW;
@@ -217,40 +256,52 @@ __global__ __launch_bounds__(L > LN_THREADS ? L : LN_THREADS) void layer_norm_bw
             if (c < a.D) {
                 rx[k] = Slice<T>::load(a.x, r * a.D + c);
                 ry[k] = Slice<T>::load(a.dy, r * a.D + c);
-                if (a.dsum) rs[k] = Slice<T>::load(a.dsum, r * a.D + c);
+                if (AHEAD && a.dsum) rs[k] = Slice<T>::load(a.dsum, r * a.D + c);
             }
         }
     };
     if (AHEAD && row < a.rows) fetch(row);
     for (; row < a.rows; row += step) {
         const int64_t at = row * a.D;
-        float u[K * V], dy[K * V];
-        u32x4 ds[K];
+        float u[K * V];
+        u32x4 gy[K], gs[K];
         if (!AHEAD) fetch(row);
+        wt.next_row();
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (k * L + l) * V;
             if (c < a.D) {
                 Slice<T>::unpack(rx[k], u + k * V);
-                Slice<T>::unpack(ry[k], dy + k * V);
-                if (a.dsum) ds[k] = rs[k];
+                gy[k] = ry[k];
+                if (a.dsum) gs[k] = rs[k];
             } else {
 #pragma unroll
-                for (int v = 0; v < V; ++v) u[k * V + v] = dy[k * V + v] = 0.f;
+                for (int v = 0; v < V; ++v) u[k * V + v] = 0.f;
             }
         }
         if (AHEAD && row + step < a.rows) fetch(row + step);
         const Stats s = row_stats<L, K * V>(u, count, a.D, a.eps);
-        float two[2] = {0.f, 0.f};  // sums of t and t n
+        float two[2] = {0.f, 0.f};  // sums of t = dy weight and of t n
+        float t[KEEP ? K * V : 1];  // (kept, too, where the weights are)
 #pragma unroll
-        for (int i = 0; i < K * V; ++i) {
-            u[i] = i < count ? ((u[i] - s.mean) - s.rest) * s.rho : 0.f;
-            dw[i] = fmaf(dy[i], u[i], dw[i]);
-            db[i] += dy[i];
-            if constexpr (AHEAD) dy[i] *= wt[i];
-            else dy[i] *= i < count ? a.weight[(i / V * L + l) * V + i % V] : 0.f;
-            two[0] += dy[i];
-            two[1] = fmaf(dy[i], u[i], two[1]);
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * L + l) * V;
+            if (c < a.D) {
+                float dy[V], q[V];
+                Slice<T>::unpack(gy[k], dy);
+                wt.get(k, c, q);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const int i = k * V + v;
+                    u[i] = ((u[i] - s.mean) - s.rest) * s.rho;
+                    dw[i] = fmaf(dy[v], u[i], dw[i]);
+                    db[i] += dy[v];
+                    dy[v] *= q[v];
+                    two[0] += dy[v];
+                    two[1] = fmaf(dy[v], u[i], two[1]);
+                    if constexpr (KEEP) t[i] = dy[v];
+                }
+            }
         }
         row_sums<L, 2>(two, red_t);
         const float mt = two[0] * inv, mtn = two[1] * inv, rho = s.rho;
@@ -258,12 +309,20 @@ __global__ __launch_bounds__(L > LN_THREADS ? L : LN_THREADS) void layer_norm_bw
         for (int k = 0; k < K; ++k) {
             const int c = (k * L + l) * V;
             if (c < a.D) {
-                float dx[V], d[V];
-                if (a.dsum) Slice<T>::unpack(ds[k], d);
+                float dx[V], dy[V], q[V], d[V];
+                if constexpr (!KEEP) {
+                    Slice<T>::unpack(gy[k], dy);
+                    wt.get(k, c, q);
+                }
+                if (a.dsum) {
+                    if (!AHEAD) gs[k] = Slice<T>::load(a.dsum, at + c);
+                    Slice<T>::unpack(gs[k], d);
+                }
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     const int i = k * V + v;
-                    dx[v] = rho * (dy[i] - mt - u[i] * mtn) * s.scale;
+                    if constexpr (KEEP) dx[v] = rho * (t[i] - mt - u[i] * mtn) * s.scale;
+                    else dx[v] = rho * (dy[v] * q[v] - mt - u[i] * mtn) * s.scale;
                     if (a.dsum) dx[v] += d[v];
                 }
                 Slice<T>::store(a.dx, at + c, dx);
@@ -330,7 +389,7 @@ void by_row(int32_t D, F&& rows) {
     else if (slices <= 256) f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
     else if (slices <= 512) f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
     else if (slices <= 1024) f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
-    else if (slices <= 2048) f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+    else if (slices <= 2048) f(integral_constant<int, 512>{}, integral_constant<int, 4>{});
     else if constexpr (sizeof(T) == 4) f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
 }
 
