@@ -39,10 +39,11 @@ bool valid_batch(int32_t B, int32_t T, int32_t C) {
 }
 
 int32_t scan_states(int32_t T) { return (int32_t)(((int64_t)T + kda::GS_STATES - 1) / kda::GS_STATES); }
+int32_t scan_tiles(int32_t T) { return (int32_t)(((int64_t)T + kda::GS_TILE - 1) / kda::GS_TILE); }
 
 // Tiles of all rows, of 64 channels and more, are counted in 32 bits (their tickets).
 bool countable_tiles(int32_t B, int32_t T, int32_t C) {
-    return (int64_t)B * scan_states(T) * ((C + 63) / 64) < I31;
+    return (int64_t)B * scan_tiles(T) * ((C + 63) / 64) < I31;
 }
 
 // Workspace of the recurrence: the counters and words of the tiles (none where a row is one
@@ -53,15 +54,15 @@ struct ScanSpace {
 
 ScanSpace scan_space(int32_t B, int32_t T, int32_t C, bool packed, bool backward) {
     const size_t groups = packed ? ((size_t)T + 15) / 16 : 0;
-    const bool one = T == 0 || (backward ? T <= kda::GS_STATES : !packed && T <= kda::GS_ONE_TILE);
+    const bool one = T == 0 || (backward ? T <= kda::GS_TILE : !packed && T <= kda::GS_ONE_TILE);
     const int64_t counters = std::min<int64_t>((int64_t)B * ((C + 63) / 64), kda::GS_MAX_COUNTERS);
     ScanSpace s{};
     s.tickets = 0;
     s.words = one ? 0 : align_up((size_t)counters * kda::GS_TICKET_BYTES);
-    s.marks = s.words + (one ? 0 : align_up((size_t)B * scan_states(T) * C * sizeof(uint64_t)));
+    s.marks = s.words + (one ? 0 : align_up((size_t)B * scan_tiles(T) * C * sizeof(uint64_t)));
     s.seq = s.marks + align_up(groups * sizeof(uint2));
     s.part = s.seq + align_up(groups * 16 * sizeof(int32_t));
-    s.total = s.part + (backward ? align_up((size_t)B * scan_states(T) * 2 * C * sizeof(float)) : 0);
+    s.total = s.part + (backward ? align_up((size_t)B * scan_tiles(T) * 2 * C * sizeof(float)) : 0);
     return s;
 }
 

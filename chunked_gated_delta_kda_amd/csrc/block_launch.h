@@ -12,8 +12,9 @@
 namespace kda {
 
 // The recurrence's tiles are 128 tokens of a row of the batch in the forward pass and 64
-// in the backward pass; the forward pass keeps the state that enters every 64th token.
-constexpr int GS_STATES = 64;
+// in the backward pass; the forward pass keeps the state that enters every 8th token.
+constexpr int GS_TILE = 64;
+constexpr int GS_STATES = 8;
 constexpr int GS_ONE_TILE = 256;  // most tokens of a row that the forward pass has as one tile
 constexpr int GS_TICKET_BYTES = 64;  // counters do not share a line
 constexpr int GS_MAX_COUNTERS = 2048;
@@ -50,7 +51,7 @@ struct ScanArgs {
     float* dA_log;          // [C]
     float* ddt_bias;        // [C]
     float* dh0;             // [N, C] or null
-    float* part;            // [B, n_states, 2, C]: a tile's sums for dA_log and ddt_bias
+    float* part;            // [B, tiles, 2, C]: a tile's sums for dA_log and ddt_bias
 };
 
 struct ScanDecodeArgs {

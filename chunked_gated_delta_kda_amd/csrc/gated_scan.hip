@@ -14,8 +14,8 @@
 // state) are joined through LDS, the tiles of a chain through memory
 // (enter_tile), and each output is then one fused multiply-add from the state that
 // enters the wave.  Gradients run the same way from the last token to the first,
-// in tiles of 64 tokens; the states they need are scanned again from those that
-// the forward pass kept at the head of each.
+// eight tokens a wave, in tiles of 64; the states they need are scanned again from
+// those that the forward pass kept of every eighth token.
 #include "block_device.h"
 
 namespace kda {
@@ -27,7 +27,8 @@ constexpr int GS_THREADS = 64 * GS_WAVES;
 constexpr int TICKET_WORDS = GS_TICKET_BYTES / 4;
 constexpr int FWD_STEPS = 16, BWD_STEPS = 8;  // tokens of a wave
 constexpr int FWD_TILE = GS_WAVES * FWD_STEPS, BWD_TILE = GS_WAVES * BWD_STEPS;
-static_assert(BWD_TILE == GS_STATES && FWD_TILE == 2 * GS_STATES, "the states kept are those entering a BWD_TILE");
+static_assert(BWD_STEPS == GS_STATES && FWD_STEPS == 2 * GS_STATES, "the states kept are those entering BWD_STEPS tokens");
+static_assert(BWD_TILE == GS_TILE, "the smallest tile");
 
 // The decay's gate for one element: L = amount softplus(z) and a = exp(-L), with
 // softplus(z) = max(z, 0) + log(1 + e), e = exp(-|z|).  1 + e rounds away what a slow
@@ -35,19 +36,11 @@ static_assert(BWD_TILE == GS_STATES && FWD_TILE == 2 * GS_STATES, "the states ke
 // 1 / u, for which 1 - e / 2 is near enough.
 struct Decay {
     float L, a;
-    __device__ __forceinline__ Decay() {}
     __device__ __forceinline__ Decay(float z, float amount) {
         const float e = __builtin_amdgcn_exp2f(-LOG2E * fabsf(z)), u = 1.f + e;
         const float log1p = fmaf(__builtin_amdgcn_logf(u), LN2, (e - (u - 1.f)) * fmaf(-0.5f, e, 1.f));
         L = amount * (fmaxf(z, 0.f) + log1p);
-        set_a();
-    }
-    __device__ __forceinline__ void set_a() { a = __builtin_amdgcn_exp2f(-LOG2E * L); }
-    // a is computed again from here on (kept, it would take the registers of a second
-    // workgroup)
-    __device__ __forceinline__ void again() {
-        asm volatile("" : "+v"(L));
-        set_a();
+        a = __builtin_amdgcn_exp2f(-LOG2E * L);
     }
     // 1 - a^2 = 1 - exp(-2 L): where a^2 is close to one by a polynomial for (1 - e^-t) / t,
     // t <= 1/4 (8e-9 of it at most, fitted to the function), else from a
@@ -368,8 +361,8 @@ __global__ __launch_bounds__(64 * WAVES, 8) void gated_scan_fwd_kernel(ScanArgs 
     }
     if (!active) return;
     const float enter = carry(bp, bs, in);
-    if (w % (GS_STATES / FWD_STEPS) == 0 && a.states && t0 < a.T)
-        a.states[((int64_t)b * a.n_states + t0 / GS_STATES) * a.C + c] = enter;
+    float* states = a.states ? a.states + ((int64_t)b * a.n_states + t0 / GS_STATES) * a.C + c : nullptr;
+    if (states && t0 < a.T) states[0] = enter;
     RowWalk row(a, b, t0, row_bytes);
 #pragma unroll
     for (int t = 0; t < FWD_STEPS; ++t, row.next()) {
@@ -378,14 +371,17 @@ __global__ __launch_bounds__(64 * WAVES, 8) void gated_scan_fwd_kernel(ScanArgs 
         if (PACKED ? m.last >> t & 1 : t0 + t == a.T - 1) {
             if (a.h_final) a.h_final[(PACKED ? sequence(t) : (int64_t)b) * a.C + c] = o;
         }
+        if (t == GS_STATES - 1 && states && t0 + GS_STATES < a.T) states[a.C] = o;
         store_one<T>(a.o, row.at, lane_bytes, o);
     }
 }
 
+// A wave knows the state that enters its eight tokens, and so everything but the gradients
+// that come back to them: what each gradient is of those is made ready before they are
+// known, and there is little to do behind enter_tile.
 template <class T, bool PACKED>
 __global__ __launch_bounds__(GS_THREADS, 6) void gated_scan_bwd_kernel(ScanArgs a) {
-    __shared__ float s_prod[GS_WAVES][64], s_sum[GS_WAVES][64];    // states, forwards
-    __shared__ float s_bprod[GS_WAVES][64], s_bsum[GS_WAVES][64];  // gradients, backwards
+    __shared__ float s_prod[GS_WAVES][64], s_sum[GS_WAVES][64];
     __shared__ uint64_t look[FAR][64];
     const int tiles = tiles_of(a.T, BWD_TILE);
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -410,12 +406,11 @@ __global__ __launch_bounds__(GS_THREADS, 6) void gated_scan_bwd_kernel(ScanArgs 
         }
     }
     const float bias = a.dt_bias[c], amount = expf(a.A_log[c]);
-    float enter = a.states[((int64_t)b * a.n_states + k) * a.C + c];
+    // (tokens behind the last one have none, and need none)
+    float h = a.states[((int64_t)b * a.n_states + min(t0 / GS_STATES, a.n_states - 1)) * a.C + c];
     Marks m;
     if constexpr (PACKED) m = Marks(a, t0);
-    const uint32_t fresh = PACKED ? m.start | ~m.in : 0u;  // do not go on from the token before
-    const uint32_t ended = PACKED ? m.last | ~m.in : 0u;   // nor to the next one
-    const auto after_fresh = [&](int t) { return (fresh & ((2u << t) - 1)) != 0; };
+    const uint32_t ended = PACKED ? m.last | ~m.in : 0u;  // nothing comes back from the token behind
     const auto sequence = [&](int t) { return (int64_t)(int)Marks::uniform(a.seq[t0 + t]); };
     const auto state_of = [&](const float* p, int t) { return p ? p[sequence(t) * a.C + c] : 0.f; };
     if constexpr (!PACKED) {
@@ -429,69 +424,58 @@ __global__ __launch_bounds__(GS_THREADS, 6) void gated_scan_bwd_kernel(ScanArgs 
             }
         }
     }
-    Decay dec[BWD_STEPS];
-    float prev[BWD_STEPS];
-    float p = 1.f, h = 0.f, q = 1.f, e = 0.f;
-    // states from zero
+    // With e the gradient of h_t: dx = e fx, di = e fi, dL/dL_t = (a e) fp, and
+    // dg = (a e) fp fg
+    float dec[BWD_STEPS], L[BWD_STEPS], fx[BWD_STEPS], fi[BWD_STEPS], fp[BWD_STEPS], fg[BWD_STEPS], d_o[BWD_STEPS];
 #pragma unroll
     for (int t = 0; t < BWD_STEPS; ++t) {
-        dec[t] = Decay(value<T>(rg[t]) + bias, amount);
-        const float in =
-            __builtin_amdgcn_sqrtf(dec[t].one_minus_square()) * sigmoid(value<T>(ri[t])) * value<T>(rx[t]);
-        if (PACKED && fresh >> t & 1) {
-            p = 0.f;
-            h = m.start >> t & 1 ? fmaf(dec[t].a, state_of(a.h0, t), in) : 0.f;
-        } else {
-            p *= dec[t].a;
-            h = fmaf(dec[t].a, h, in);
-        }
-        prev[t] = h;
+        const float z = value<T>(rg[t]) + bias, x = value<T>(rx[t]);
+        const Decay d(z, amount);
+        const InputGate ig(value<T>(ri[t]));
+        const float root = __builtin_amdgcn_sqrtf(d.one_minus_square());
+        if (PACKED && (m.start >> t & 1)) h = state_of(a.h0, t);
+        dec[t] = d.a;
+        L[t] = d.L;
+        fx[t] = root * ig.s;
+        fi[t] = root * x * ig.slope;
+        // (no decay at all: nothing of the input enters, and sigmoid(z) is zero)
+        fp[t] = fmaf(d.a * ig.s * x, __builtin_amdgcn_rcpf(fmaxf(root, 0x1p-70f)), -h);
+        fg[t] = amount * sigmoid(z);
+        d_o[t] = value<T>(rd[t]);
+        h = fmaf(d.a, h, fx[t] * x);
+        // (here, and not where they are used: what they are made of would stay in registers)
+        asm volatile("" : "+v"(fx[t]), "+v"(fi[t]), "+v"(fp[t]), "+v"(fg[t]));
     }
     // gradients of the states, from zero, last token first: what reaches the state before a
     // token is a (do + what reaches its own)
+    float q = 1.f, e = 0.f;
 #pragma unroll
     for (int t = BWD_STEPS - 1; t >= 0; --t) {
         if (PACKED && ended >> t & 1) {
             q = 0.f;
-            e = m.last >> t & 1 ? dec[t].a * (value<T>(rd[t]) + state_of(a.d_final, t)) : 0.f;
+            e = m.last >> t & 1 ? dec[t] * (d_o[t] + state_of(a.d_final, t)) : 0.f;
         } else {
-            q *= dec[t].a;
-            e = dec[t].a * (value<T>(rd[t]) + e);
+            q *= dec[t];
+            e = dec[t] * (d_o[t] + e);
         }
     }
-    if (PACKED && after_fresh(BWD_STEPS - 1)) p = 0.f;
     if (PACKED && (ended & ((1u << BWD_STEPS) - 1))) q = 0.f;
-    s_prod[w][lane] = p;
-    s_sum[w][lane] = h;
-    s_bprod[w][lane] = q;
-    s_bsum[w][lane] = e;
+    s_prod[w][lane] = q;
+    s_sum[w][lane] = e;
     __syncthreads();
     // (the wave that posts a tile's word is the last: it folds all waves' gradients, the
     // others those behind them)
-    for (int j = 0; j < w; ++j) enter = carry(s_prod[j][lane], s_sum[j][lane], enter);
     float bp = 1.f, bs = 0.f;
     const int until = w == GS_WAVES - 1 ? 0 : w + 1;
     for (int j = GS_WAVES - 1; j >= until; --j) {
-        bs = carry(s_bprod[j][lane], s_bsum[j][lane], bs);
-        bp = join(s_bprod[j][lane], bp);
+        bs = carry(s_prod[j][lane], s_sum[j][lane], bs);
+        bp = join(s_prod[j][lane], bp);
     }
     const float first = order == 0 && !PACKED && a.d_final ? a.d_final[(int64_t)b * a.C + c] : 0.f;
     const float in = enter_tile(a, tiles, order, (int64_t)b * a.C + c, active, w, lane, bp, bs, first, look);
     float back = in;
     if (w < GS_WAVES - 1) back = carry(bp, bs, in);
     else if (!PACKED && a.dh0 && k == 0 && active) a.dh0[(int64_t)b * a.C + c] = carry(bp, bs, in);
-    // the state before each token, from what a zero state left behind it
-    {
-        float prod = 1.f, before = enter;
-#pragma unroll
-        for (int t = 0; t < BWD_STEPS; ++t) {
-            const float after = prev[t];
-            prev[t] = PACKED && (m.start >> t & 1) ? state_of(a.h0, t) : before;
-            dec[t].again();
-            prod *= dec[t].a;
-            before = PACKED && after_fresh(t) ? after : fmaf(prod, enter, after);
-        }
-    }
     float dA = 0.f, db = 0.f;
     const int64_t head = ((int64_t)b * a.T + t0) * row_bytes;
 #pragma unroll
@@ -499,20 +483,13 @@ __global__ __launch_bounds__(GS_THREADS, 6) void gated_scan_bwd_kernel(ScanArgs 
         float dx = 0.f, dg = 0.f, di = 0.f;
         if (PACKED && m.last >> t & 1) back = state_of(a.d_final, t);
         if (!PACKED || m.in >> t & 1) {
-            Decay& d = dec[t];
-            d.again();
-            const float x = value<T>(rx[t]);
-            const InputGate ig(value<T>(ri[t]));
-            const float m2 = d.one_minus_square();
-            // (no decay at all: nothing of the input enters, and nothing comes back)
-            const float inv = m2 > 0.f ? __builtin_amdgcn_rsqf(m2) : 0.f;
-            const float et = value<T>(rd[t]) + back, em = et * (m2 * inv);
-            back = d.a * et;
-            const float pt = back * (d.a * ig.s * x * inv - prev[t]);
-            dx = em * ig.s;
-            di = em * x * ig.slope;
-            dg = pt * amount * sigmoid(value<T>(rg[t]) + bias);
-            dA = fmaf(pt, d.L, dA);
+            const float et = d_o[t] + back;
+            back = dec[t] * et;
+            const float pt = back * fp[t];
+            dx = et * fx[t];
+            di = et * fi[t];
+            dg = pt * fg[t];
+            dA = fmaf(pt, L[t], dA);
             db += dg;
         }
         if (PACKED && a.dh0 && active && m.start >> t & 1) a.dh0[sequence(t) * a.C + c] = back;
@@ -537,7 +514,7 @@ __global__ __launch_bounds__(GS_THREADS, 6) void gated_scan_bwd_kernel(ScanArgs 
 // dA_log and ddt_bias from the tiles' sums: a workgroup for 32 channels of one of them
 __global__ __launch_bounds__(256) void gated_scan_sum_kernel(ScanArgs a) {
     const int which = blockIdx.x % 2, c = blockIdx.x / 2 * 32 + threadIdx.x % 32;
-    const double s = sum_columns(a.part + (int64_t)which * a.C + min(c, a.C - 1), (int64_t)a.B * a.n_states,
+    const double s = sum_columns(a.part + (int64_t)which * a.C + min(c, a.C - 1), (int64_t)a.B * tiles_of(a.T, BWD_TILE),
                                  (int64_t)2 * a.C);
     if (threadIdx.x < 32 && c < a.C) (which ? a.ddt_bias : a.dA_log)[c] = (float)s;
 }

@@ -546,7 +546,7 @@ enum kda_dtype { KDA_BF16 = 0, KDA_FP32 = 1 };
  * without a token returns its initial state.  exp(A_log[c]) has to be finite.
  * B ceil(T / 64) ceil(C / 64) < 2^31.
  * states (NULL: not kept): gated_scan_states(B, T, C) fp32 numbers, what
- * gated_scan_bwd needs of the forward pass (the state that enters every 64th
+ * gated_scan_bwd needs of the forward pass (the state that enters every 8th
  * token of a row of the batch).  gated_scan_states is -1 for sizes that are not
  * supported. */
 int64_t gated_scan_states(int32_t B, int32_t T, int32_t C);

@@ -127,7 +127,7 @@ def test_no_rows_is_no_call(lib):
 
 
 def test_sizes(lib):
-    assert lib.gated_scan_states(2, 129, 64) == 2 * 3 * 64
+    assert lib.gated_scan_states(2, 129, 64) == 2 * 17 * 64
     assert lib.gated_scan_states(1, 0, 64) == 0
     for bad in ((0, 1, 64), (1, -1, 64), (1, 1, 12), (1, 1, (1 << 20) + 8), (1 << 16, 1 << 15, 64)):
         assert lib.gated_scan_states(*bad) == -1
@@ -136,7 +136,7 @@ def test_sizes(lib):
     # more tiles than tickets: 2^24 of 64 tokens, 2^7 blocks of 64 channels
     assert lib.gated_scan_states(1 << 24, 64, 1 << 13) == -1
     assert kda.gated_scan_workspace_size(1 << 24, 64, 1 << 13) == 0
-    assert lib.gated_scan_states((1 << 24) - 1, 64, 1 << 13) == ((1 << 24) - 1) << 13
+    assert lib.gated_scan_states((1 << 24) - 1, 64, 1 << 13) == ((1 << 24) - 1) << 16
     # rows of one tile need none, packed ones their tables, longer ones words for every tile
     assert kda.gated_scan_workspace_size(2, 256, 64) == 256
     assert kda.gated_scan_workspace_size(1, 256, 64, packed=True) > 256
