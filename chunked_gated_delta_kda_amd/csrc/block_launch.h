@@ -17,7 +17,7 @@ constexpr int GS_TILE = 64;
 constexpr int GS_STATES = 8;
 constexpr int GS_ONE_TILE = 256;  // most tokens of a row that the forward pass has as one tile
 constexpr int GS_TICKET_BYTES = 64;  // counters do not share a line
-constexpr int GS_MAX_COUNTERS = 2048;
+constexpr int GS_MAX_COUNTERS = 8192;
 
 struct ScanArgs {
     const void* x;          // [B, T, C] tokens

@@ -7,15 +7,21 @@
 //   dx = e m s,  di = e m x s (1 - s),  dg = p exp(A_log) sigmoid(g + dt_bias),
 //   dA_log = sum p L,  ddt_bias = sum dg,  dh0 = a_0 e_0.
 //
-// One pass over the data.  A wave has 64 words of a token row (128 bf16 channels,
-// 64 of fp32) for 16 tokens, a workgroup eight such waves one behind the other: a
-// tile of 128 tokens.  Every wave scans its own tokens from a zero state, keeping
-// the state and the product of the decays at each; the eight pairs (product,
-// state) are joined through LDS, the tiles of a chain through memory
-// (enter_tile), and each output is then one fused multiply-add from the state that
-// enters the wave.  Gradients run the same way from the last token to the first,
-// eight tokens a wave, in tiles of 64; the states they need are scanned again from
-// those that the forward pass kept of every eighth token.
+// One pass over the data, bound by HBM.  A lane has a channel of 16 tokens of a row
+// (gradients: 8), a workgroup eight such waves one behind the other: a tile of 64
+// channels and 128 tokens (64).  Every wave scans its own tokens from a zero state,
+// keeping the state and the product of the decays at each; the eight pairs (product,
+// state) are joined through LDS, the tiles of a chain through memory (enter_tile), and
+// each output is then one fused multiply-add from the state that enters the wave.
+// Gradients run the same way from the last token to the first, in tiles of half the
+// tokens, since a token has twice the values to keep; the states they need are scanned
+// again from those that the forward pass kept of every eighth token.  One channel a lane
+// keeps a forward wave within 64 registers, so that eight fit on a SIMD; two channels a
+// lane (rows of 256 bytes) gain nothing: 131072 x 4096 bf16 tokens 501 us, 468 with one,
+// and the gradients of 2 x 2048 x 4096 the same to 1%.
+// Measured (bf16, 4096 channels): 131072 tokens 468 us, 4.6 TB/s; 2 x 2048 tokens with
+// the states kept 39 us, 3.9 TB/s; their gradients 79 us with the launches before and
+// behind, 3.2 TB/s.
 #include "block_device.h"
 
 namespace kda {
@@ -209,10 +215,11 @@ __device__ __forceinline__ void store_one(void* p, int64_t row, uint32_t lane_by
 
 }  // namespace
 
-// What a pass needs before it: words that are empty and tickets that are not drawn; of a packed batch
-// which sequence each token belongs to and which tokens begin and end one; and for the
-// sequences without a token, the state behind them (dst = src, or zeros).  Workgroups
-// [0, fill) have the words, the next `marks` the tokens, the others a sequence each.
+// What a pass needs before it: words that are empty and tickets that are not drawn; of a
+// packed batch which sequence each token belongs to and which tokens begin and end one; and
+// for the sequences without a token, the state behind them (dst = src, or zeros).
+// Workgroups [0, fill) have the words, the next `marks` the tokens, the others a sequence
+// each.
 struct PrepareArgs {
     ScanArgs a;
     int64_t fill, marks;
@@ -378,9 +385,10 @@ __global__ __launch_bounds__(64 * WAVES, 8) void gated_scan_fwd_kernel(ScanArgs 
 
 // A wave knows the state that enters its eight tokens, and so everything but the gradients
 // that come back to them: what each gradient is of those is made ready before they are
-// known, and there is little to do behind enter_tile.
+// known, and there is little to do behind enter_tile.  (Bounded to six waves a SIMD it
+// spills: 2 x 2048 x 4096 with its forward pass 127.6 us, 122.3 with five.)
 template <class T, bool PACKED>
-__global__ __launch_bounds__(GS_THREADS, 6) void gated_scan_bwd_kernel(ScanArgs a) {
+__global__ __launch_bounds__(GS_THREADS, 4) void gated_scan_bwd_kernel(ScanArgs a) {
     __shared__ float s_prod[GS_WAVES][64], s_sum[GS_WAVES][64];
     __shared__ uint64_t look[FAR][64];
     const int tiles = tiles_of(a.T, BWD_TILE);
@@ -426,7 +434,7 @@ __global__ __launch_bounds__(GS_THREADS, 6) void gated_scan_bwd_kernel(ScanArgs 
     }
     // With e the gradient of h_t: dx = e fx, di = e fi, dL/dL_t = (a e) fp, and
     // dg = (a e) fp fg
-    float dec[BWD_STEPS], L[BWD_STEPS], fx[BWD_STEPS], fi[BWD_STEPS], fp[BWD_STEPS], fg[BWD_STEPS], d_o[BWD_STEPS];
+    float dec[BWD_STEPS], L[BWD_STEPS], fx[BWD_STEPS], fi[BWD_STEPS], fp[BWD_STEPS], fg[BWD_STEPS];
 #pragma unroll
     for (int t = 0; t < BWD_STEPS; ++t) {
         const float z = value<T>(rg[t]) + bias, x = value<T>(rx[t]);
@@ -439,9 +447,8 @@ __global__ __launch_bounds__(GS_THREADS, 6) void gated_scan_bwd_kernel(ScanArgs 
         fx[t] = root * ig.s;
         fi[t] = root * x * ig.slope;
         // (no decay at all: nothing of the input enters, and sigmoid(z) is zero)
-        fp[t] = fmaf(d.a * ig.s * x, __builtin_amdgcn_rcpf(fmaxf(root, 0x1p-70f)), -h);
+        fp[t] = fmaf(d.a * ig.s * x, root == 0.f ? 0.f : __builtin_amdgcn_rcpf(root), -h);
         fg[t] = amount * sigmoid(z);
-        d_o[t] = value<T>(rd[t]);
         h = fmaf(d.a, h, fx[t] * x);
         // (here, and not where they are used: what they are made of would stay in registers)
         asm volatile("" : "+v"(fx[t]), "+v"(fi[t]), "+v"(fp[t]), "+v"(fg[t]));
@@ -453,10 +460,10 @@ __global__ __launch_bounds__(GS_THREADS, 6) void gated_scan_bwd_kernel(ScanArgs 
     for (int t = BWD_STEPS - 1; t >= 0; --t) {
         if (PACKED && ended >> t & 1) {
             q = 0.f;
-            e = m.last >> t & 1 ? dec[t] * (d_o[t] + state_of(a.d_final, t)) : 0.f;
+            e = m.last >> t & 1 ? dec[t] * (value<T>(rd[t]) + state_of(a.d_final, t)) : 0.f;
         } else {
             q *= dec[t];
-            e = dec[t] * (d_o[t] + e);
+            e = dec[t] * (value<T>(rd[t]) + e);
         }
     }
     if (PACKED && (ended & ((1u << BWD_STEPS) - 1))) q = 0.f;
@@ -483,7 +490,7 @@ __global__ __launch_bounds__(GS_THREADS, 6) void gated_scan_bwd_kernel(ScanArgs 
         float dx = 0.f, dg = 0.f, di = 0.f;
         if (PACKED && m.last >> t & 1) back = state_of(a.d_final, t);
         if (!PACKED || m.in >> t & 1) {
-            const float et = d_o[t] + back;
+            const float et = value<T>(rd[t]) + back;
             back = dec[t] * et;
             const float pt = back * fp[t];
             dx = et * fx[t];
@@ -556,14 +563,19 @@ void launch_prepare(const ScanArgs& a, int tiles, int64_t chains, const float* s
     if (groups) hipLaunchKernelGGL(gated_scan_prepare_kernel, wide_grid(groups, 256), dim3(256), 0, stream, q);
 }
 
-#ifndef FAR_GROUPS
-#define FAR_GROUPS GS_MAX_COUNTERS
-#define OWN_GROUPS GS_MAX_COUNTERS
-#endif
-int64_t set_chains(ScanArgs& a, int tiles) {
+// Where all tiles are at work within a few rounds, a chain has a counter of its own: one
+// counter for all is a queue at the start (forward 2048 tokens of 4096 channels, 1024 tiles:
+// 21.7 us, 32.3 with one; 8192 tokens: 66, 76), but keeps the chains of a longer call side
+// by side in memory (131072 tokens, 65536 tiles: 468 us, 543 with one each; gradients of
+// 8192 tokens, 8192 tiles: 144 and 148).  And where they all start at about the same time,
+// a tile looks far (odd packed batch with gradients: 60 us, 67 without; gradients of 32768
+// tokens of 1024 channels, 8192 tiles: 174, 151 without).
+constexpr int64_t FAR_TILES = 2048, OWN_TILES_BWD = 2048, OWN_TILES_FWD = GS_MAX_COUNTERS;
+
+int64_t set_chains(ScanArgs& a, int tiles, int64_t own_tiles) {
     const int64_t chains = (int64_t)a.B * ((a.C + 63) / 64);
-    a.far = chains * tiles <= FAR_GROUPS;
-    a.beside = chains * tiles <= OWN_GROUPS ? 1 : (int32_t)chains;
+    a.far = chains * tiles <= FAR_TILES;
+    a.beside = chains * tiles <= own_tiles ? 1 : (int32_t)chains;
     return chains;
 }
 
@@ -581,7 +593,7 @@ void launch_gated_scan_fwd(const ScanArgs& args, bool fp32, hipStream_t stream) 
     // launch before this one (256 tokens of 256 channels: 11.0 us a call, 15.6 in two tiles).
     const bool one = !a.cu && a.T > FWD_TILE && a.T <= GS_ONE_TILE;
     const int tiles = one ? 1 : tiles_of(a.T, FWD_TILE);
-    const int64_t chains = set_chains(a, tiles);
+    const int64_t chains = set_chains(a, tiles, OWN_TILES_FWD);
     launch_prepare(a, tiles, chains, a.h0, a.h_final, stream);
     if (a.T == 0) return;
     by_type(fp32, a.cu != nullptr, [&](auto t, auto packed) {
@@ -603,14 +615,13 @@ void launch_gated_scan_fwd(const ScanArgs& args, bool fp32, hipStream_t stream) 
 void launch_gated_scan_bwd(const ScanArgs& args, bool fp32, hipStream_t stream) {
     ScanArgs a = args;
     const int tiles = tiles_of(a.T, BWD_TILE);
-    const int64_t chains = set_chains(a, tiles);
+    const int64_t chains = set_chains(a, tiles, OWN_TILES_BWD);
     launch_prepare(a, tiles, chains, a.d_final, a.dh0, stream);
     if (a.T > 0) {
         by_type(fp32, a.cu != nullptr, [&](auto t, auto packed) {
             using T = decltype(t);
-                hipLaunchKernelGGL((gated_scan_bwd_kernel<T, decltype(packed)::value>),
-                               wide_grid(chains * tiles, GS_THREADS),
-                               dim3(GS_THREADS), 0, stream, a);
+            hipLaunchKernelGGL((gated_scan_bwd_kernel<T, decltype(packed)::value>),
+                               wide_grid(chains * tiles, GS_THREADS), dim3(GS_THREADS), 0, stream, a);
         });
     }
     hipLaunchKernelGGL(gated_scan_sum_kernel, dim3((unsigned)((a.C + 31) / 32 * 2)), dim3(256), 0, stream, a);

@@ -291,3 +291,32 @@ def test_two_streams_at_once():
     for i in range(2):
         for o, f in got[i]:
             assert torch.equal(o, want[i][0]) and torch.equal(f, want[i][1])
+
+
+def test_large_values_in_the_last_row():
+    """Rows behind the last token are read as the last one, without a decay: nothing of
+    them, however large, reaches the sums over tokens."""
+    w = make(2, 70, 24, seed=47, dtype="fp32")
+    w["x"][:, -1] *= 2.0 ** 90
+    check(w)
+
+
+@pytest.mark.parametrize("B,T", [(11, 260), (1, 4300), (300, 4000)])
+def test_counters_and_looks(B, T):
+    """Tiles in 33 chains or one, each with a counter of its own, and 9600 tiles (forward)
+    drawn from one counter; few enough that a tile looks at 32 before it, or at 8: the same
+    sums in the same order."""
+    C = 136 if B == 11 else 64
+    gen = torch.Generator(device=DEV).manual_seed(B)
+    n = lambda *s: torch.randn(*s, generator=gen, device=DEV)  # noqa: E731
+    x, g, i, do = (n(B, T, C) for _ in range(4))
+    A, bias, h0, df = n(C), 2 * n(C) - 5, n(B, C), n(B, C)
+    o, f, s = kda.gated_scan_fwd_save(x, g, i, A, bias, h0)
+    r = kda.gated_scan_bwd(x, g, i, A, bias, do, s, h0, df)
+    for b in sorted({0, B // 2, B - 1}):
+        one = [t[b:b + 1].contiguous() for t in (x, g, i, do, h0, df)]
+        o1, f1, s1 = kda.gated_scan_fwd_save(*one[:3], A, bias, one[4])
+        r1 = kda.gated_scan_bwd(*one[:3], A, bias, one[3], s1, one[4], one[5])
+        assert torch.equal(o[b], o1[0]) and torch.equal(f[b], f1[0])
+        for k in ("dx", "dg", "dinput_gate", "dh0"):
+            assert torch.equal(r[k][b], r1[k][0]), k
