@@ -1246,7 +1246,7 @@ def layer_norm_fwd(x, weight, bias=None, eps=1e-5, residual=None, out=None, sum_
     _need_all((("residual", residual), ("out", out)), dtype, shape, dev)
     if residual is not None:
         total = _like(sum_out, "sum_out", x)
-        if out is total:
+        if out is not None and rows and out.data_ptr() == total.data_ptr():
             raise ValueError("out and sum_out must be two tensors")
     if out is None:
         out = _Torch.parts.empty_like(x)

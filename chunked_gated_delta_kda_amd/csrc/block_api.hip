@@ -305,6 +305,7 @@ int layer_norm_fwd(const void* x, const void* residual, const float* weight, con
     if (rows > 0 && (!x || !y || (residual && !sum))) return KDA_ERR_INVALID_ARG;
     if (!aligned({x, residual, y, sum}, 16) || !aligned(bias, 4)) return KDA_ERR_INVALID_ARG;
     if (rows == 0) return KDA_OK;
+    if (residual && y == sum) return KDA_ERR_INVALID_ARG;
     kda::LayerNormArgs a{};
     a.x = x;
     a.res = residual;

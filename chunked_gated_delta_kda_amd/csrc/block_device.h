@@ -9,7 +9,6 @@ namespace kda {
 
 namespace {
 
-
 // One 4-byte word of a token tensor: two bf16 channels or one fp32 channel.
 template <class T>
 struct Word;

@@ -40,19 +40,17 @@ struct Seq {
             return;
         }
         const int lane = threadIdx.x & 63;
-        int lo = 0, count = a.N, step;
+        uint32_t lo = 0, count = a.N, step;  // (N + 63 may pass 31 bits)
         do {
             step = (count + 63) / 64;
-            const int i = lane * step;
-            const int before = __popcll(__ballot(i < count && clamp_tok(a.cu[min(lo + i, a.N)], a.T) <= t));
-            if (before == 0) {
-                lo = -1;
-                break;
-            }
+            const uint32_t i = lane * step;
+            const int before =
+                __popcll(__ballot(i < count && clamp_tok(a.cu[min(lo + i, (uint32_t)a.N)], a.T) <= t));
+            if (before == 0) return set(a, -1);
             lo += (before - 1) * step;
             count = min(step, count - (before - 1) * step);
         } while (step > 1);
-        set(a, lo);
+        set(a, (int)lo);
     }
     __device__ __forceinline__ void set(const ConvArgs& a, int i) {
         n = i;
@@ -484,7 +482,7 @@ void by_taps(int W, bool fp32, bool silu, F&& f) {
 // by them (32768 tokens of 4096 channels: 182 us, 204 with 16; 2048 tokens: 24 and 22), fp32
 // calls do not (338 and 311), nor does the forward pass (109 and 108).
 int strip_of(int32_t B, int32_t T, int64_t blocks, bool fp32, bool backward) {
-        return backward && !fp32 && (int64_t)B * ((T + 31) / 32) * blocks >= 16 * 256 ? 32 : 16;
+    return backward && !fp32 && (int64_t)B * ((T + 31) / 32) * blocks >= 16 * 256 ? 32 : 16;
 }
 
 int64_t channel_blocks(int32_t C) { return (C + 127) / 128; }

@@ -105,7 +105,8 @@ NORM_ONLY = [(dict(rows=-1), 1), (dict(rows=1 << 31), 1), (dict(D=0), 1), (dict(
 
 @pytest.mark.parametrize("over,code", NORM_ONLY + [
     (dict(x=None), 1), (dict(y=None), 1), (dict(res=FAKE), 1), (dict(x=odd(8)), 1), (dict(y=odd(8)), 1),
-    (dict(res=odd(8), sum=FAKE), 1), (dict(res=FAKE, sum=odd(8)), 1), (dict(b=odd(2)), 1)])
+    (dict(res=odd(8), sum=FAKE), 1), (dict(res=FAKE, sum=odd(8)), 1), (dict(b=odd(2)), 1),
+    (dict(res=FAKE, sum=FAKE), 1)])
 def test_layer_norm_fwd_rejects_on_host(lib, over, code):
     assert call(lib.layer_norm_fwd, NORM, over) == code
 
