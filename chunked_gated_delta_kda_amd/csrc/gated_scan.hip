@@ -17,9 +17,9 @@
 // tokens, since a token has twice the values to keep; the states they need are scanned
 // again from those that the forward pass kept of every eighth token.  One channel a lane
 // keeps a forward wave within 64 registers, so that eight fit on a SIMD; two channels a
-// lane (rows of 256 bytes) gain nothing: 131072 x 4096 bf16 tokens 501 us, 468 with one,
+// lane (rows of 256 bytes) gain nothing: 131072 x 2048 bf16 tokens 501 us, 468 with one,
 // and the gradients of 2 x 2048 x 4096 the same to 1%.
-// Measured (bf16, 4096 channels): 131072 tokens 468 us, 4.6 TB/s; 2 x 2048 tokens with
+// Measured (bf16): 131072 x 2048 468 us, 4.6 TB/s; 2 x 2048 x 4096 with
 // the states kept 39 us, 3.9 TB/s; their gradients 79 us with the launches before and
 // behind, 3.2 TB/s.
 #include "block_device.h"
@@ -566,8 +566,8 @@ void launch_prepare(const ScanArgs& a, int tiles, int64_t chains, const float* s
 // Where all tiles are at work within a few rounds, a chain has a counter of its own: one
 // counter for all is a queue at the start (forward 2048 tokens of 4096 channels, 1024 tiles:
 // 21.7 us, 32.3 with one; 8192 tokens: 66, 76), but keeps the chains of a longer call side
-// by side in memory (131072 tokens, 65536 tiles: 468 us, 543 with one each; gradients of
-// 8192 tokens, 8192 tiles: 144 and 148).  And where they all start at about the same time,
+// by side in memory (131072 tokens of 2048, 32768 tiles: 468 us, 543 with one each; gradients
+// of 8192 tokens of 4096, 8192 tiles: 144 and 148).  And where they all start at about the same time,
 // a tile looks far (odd packed batch with gradients: 60 us, 67 without; gradients of 32768
 // tokens of 1024 channels, 8192 tiles: 174, 151 without).
 constexpr int64_t FAR_TILES = 2048, OWN_TILES_BWD = 2048, OWN_TILES_FWD = GS_MAX_COUNTERS;

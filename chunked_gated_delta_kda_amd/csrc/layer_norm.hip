@@ -14,6 +14,9 @@
 // is fp32; each output is rounded once.  The backward kernel's workgroups walk
 // over the rows and keep their lanes' channels of dweight and dbias in registers;
 // a second kernel adds the workgroups' sums in a fixed order, in 64 bits.
+// Measured (16384 x 4096 bf16): forward with a residual 102 us, 5.3 TB/s, gradients 114 us,
+// 4.7 TB/s; 3001 x 1000 fp32 forward 7.3 us, gradients 13.1 and their sum 4.4 (its 24 MB
+// are in flight for too short a time: six rows a workgroup, one after the other).
 #include <algorithm>
 
 #include "block_device.h"
@@ -375,7 +378,8 @@ __global__ __launch_bounds__(256) void layer_norm_sum_kernel(LayerNormArgs a) {
 namespace {
 
 // Lanes of a row and slices in each: the fewest lanes up to a wave, then two slices a lane,
-// then more waves.
+// then more waves.  (256 slices in one wave, four a lane, need no barrier but registers:
+// gradients of 3001 x 1000 fp32 21.1 us, 17.5 in four waves; 16384 x 2048 bf16 73 and 66.)
 template <class T, class F>
 void by_row(int32_t D, F&& rows) {
     using std::integral_constant;

@@ -12,6 +12,9 @@
 // under way.  (Four and eight channels a lane leave too few waves, and in the
 // gradients too few registers: 4096 tokens of 4096 bf16 channels, gradients 34 us
 // with two, 42 with four, 56 with eight.)
+// Measured (bf16, 4 taps, silu): 35862 packed tokens of 12288 channels 358 us, 4.9 TB/s;
+// 2 x 2048 tokens of 4096 channels 15.6 us, 4.3 TB/s, their gradients 27 us and 4.4 for the
+// sums over strips.
 #include "block_device.h"
 
 namespace kda {
