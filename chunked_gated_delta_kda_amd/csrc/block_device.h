@@ -34,18 +34,17 @@ struct Word<float> {
     static __device__ __forceinline__ uint32_t put(const float* f) { return __float_as_uint(f[0]); }
 };
 
-// A sigmoid 1 / (1 + e^-z) as e^min(z, 0) / (1 + e^-|z|), to a few ulps where it is
-// normal, and subnormal below z = -87 (2^t by the hardware is not: the exponent's whole
-// part is put in behind it).  `rest` is 1 - s.  For a NaN both are numbers: what they are
-// multiplied by z for is one.
+// A sigmoid s = 1 / (1 + e^-z) as e^min(z, 0) / (1 + e^-|z|), to a few ulps where it is
+// normal, and subnormal below z = -87: 2^t by the hardware is not, the square of 2^(t / 2)
+// is.  `side` is s (1 - s).  For a NaN both are numbers: what they are multiplied by z for
+// is one.
 struct BlockSigmoid {
-    float s, rest;
+    float s, side;
     __device__ __forceinline__ explicit BlockSigmoid(float z) {
-        const float t = fmaxf(-LOG2E * fabsf(z), -200.f), n = floorf(t);
-        const float e = ldexpf(__builtin_amdgcn_exp2f(t - n), (int)n), r = __builtin_amdgcn_rcpf(1.f + e);
-        const float er = e * r;
+        const float h = __builtin_amdgcn_exp2f(-0.5f * LOG2E * fabsf(z)), e = h * h;
+        const float r = __builtin_amdgcn_rcpf(1.f + e), er = e * r;
         s = z < 0.f ? er : r;
-        rest = z < 0.f ? r : er;
+        side = er * r;
     }
 };
 

@@ -36,29 +36,32 @@ constexpr int FWD_TILE = GS_WAVES * FWD_STEPS, BWD_TILE = GS_WAVES * BWD_STEPS;
 static_assert(BWD_STEPS == GS_STATES && FWD_STEPS == 2 * GS_STATES, "the states kept are those entering BWD_STEPS tokens");
 static_assert(BWD_TILE == GS_TILE, "the smallest tile");
 
-// The decay's gate for one element: L = amount softplus(z) and a = exp(-L), with
-// softplus(z) = max(z, 0) + log(1 + e), e = exp(-|z|).  1 + e rounds away what a slow
-// channel's decay is made of: the lost part (e - (u - 1)), below 2^-24, comes back times
-// 1 / u, for which 1 - e / 2 is near enough.
+// The decay's gate for one element, in powers of two: L = amount softplus(z) log2(e) and
+// a = 2^-L.  With y = z log2(e) and e = 2^-|y|, softplus(z) log2(e) = max(y, 0) +
+// log2(1 + e).  1 + e rounds away what a slow channel's decay is made of: the lost part
+// e - (u - 1), below 2^-24, comes back (it would have to be divided by u: what that leaves
+// out is 2^-24 of the logarithm).
 struct Decay {
-    float L, a;
+    float y, log, L, a;
     __device__ __forceinline__ Decay(float z, float amount) {
-        const float e = __builtin_amdgcn_exp2f(-LOG2E * fabsf(z)), u = 1.f + e;
-        const float log1p = fmaf(__builtin_amdgcn_logf(u), LN2, (e - (u - 1.f)) * fmaf(-0.5f, e, 1.f));
-        L = amount * (fmaxf(z, 0.f) + log1p);
-        a = __builtin_amdgcn_exp2f(-LOG2E * L);
+        y = LOG2E * z;
+        const float e = __builtin_amdgcn_exp2f(-fabsf(y)), u = 1.f + e;
+        log = fmaf(e - (u - 1.f), LOG2E, __builtin_amdgcn_logf(u));
+        L = amount * (fmaxf(y, 0.f) + log);
+        a = __builtin_amdgcn_exp2f(-L);
     }
-    // 1 - a^2 = 1 - exp(-2 L): where a^2 is close to one by a polynomial for (1 - e^-t) / t,
-    // t <= 1/4 (8e-9 of it at most, fitted to the function), else from a
+    // 1 - a^2 = 1 - 2^-2L: where a^2 is close to one by a polynomial for (1 - 2^-2L) / L,
+    // L <= 0.18 (1e-8 of it at most, fitted to the function), else from a
     __device__ __forceinline__ float one_minus_square() const {
-        const float t = 2.f * L;
-        float s = 0.007510221563279629f;
-        s = fmaf(s, t, -0.041488952934741974f);
-        s = fmaf(s, t, 0.16665081679821014f);
-        s = fmaf(s, t, -0.4999994933605194f);
-        s = fmaf(s, t, 1.f);
-        return t < 0.25f ? s * t : fmaf(-a, a, 1.f);
+        float s = 0.038452982902526855f;
+        s = fmaf(s, L, -0.15323370695114136f);
+        s = fmaf(s, L, 0.44399064779281616f);
+        s = fmaf(s, L, -0.9609050750732422f);
+        s = fmaf(s, L, 1.3862943649291992f);
+        return L < 0.18f ? s * L : fmaf(-a, a, 1.f);
     }
+    // sigmoid(z) = 2^(y - softplus(z) log2(e))
+    __device__ __forceinline__ float sigmoid() const { return __builtin_amdgcn_exp2f(fminf(y, 0.f) - log); }
 };
 
 // sigmoid(z), which counts as zero below 2^-126
@@ -448,7 +451,7 @@ __global__ __launch_bounds__(GS_THREADS, 4) void gated_scan_bwd_kernel(ScanArgs 
         fi[t] = root * x * ig.slope;
         // (no decay at all: nothing of the input enters, and sigmoid(z) is zero)
         fp[t] = fmaf(d.a * ig.s * x, root == 0.f ? 0.f : __builtin_amdgcn_rcpf(root), -h);
-        fg[t] = amount * sigmoid(z);
+        fg[t] = amount * d.sigmoid();
         h = fmaf(d.a, h, fx[t] * x);
         // (here, and not where they are used: what they are made of would stay in registers)
         asm volatile("" : "+v"(fx[t]), "+v"(fi[t]), "+v"(fp[t]), "+v"(fg[t]));
@@ -508,7 +511,7 @@ __global__ __launch_bounds__(GS_THREADS, 4) void gated_scan_bwd_kernel(ScanArgs 
         }
     }
     __syncthreads();
-    s_prod[w][lane] = dA;
+    s_prod[w][lane] = LN2 * dA;
     s_sum[w][lane] = db;
     __syncthreads();
     if (w < 2 && active) {

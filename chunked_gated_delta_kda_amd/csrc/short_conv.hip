@@ -76,7 +76,7 @@ template <bool SILU>
 __device__ __forceinline__ float slope(float z) {
     if (!SILU) return 1.f;
     const BlockSigmoid g(z);
-    return g.s * fmaf(z, g.rest, 1.f);
+    return fmaf(z, g.side, g.s);
 }
 
 }  // namespace
