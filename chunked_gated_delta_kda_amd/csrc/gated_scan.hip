@@ -20,8 +20,10 @@
 // lane (rows of 256 bytes) gain nothing: 131072 x 2048 bf16 tokens 501 us, 468 with one,
 // and the gradients of 2 x 2048 x 4096 the same to 1%.
 // Measured (bf16): 131072 x 2048 468 us, 4.6 TB/s; 2 x 2048 x 4096 with
-// the states kept 39 us, 3.9 TB/s; their gradients 79 us with the launches before and
-// behind, 3.2 TB/s.
+// the states kept 38 us, 3.7 TB/s; their gradients 78 us with the launches before and
+// behind, 3.2 TB/s.  Rows of 128 bytes are what bounds the long call: a kernel that only
+// moves the same rows the same way reaches 4.7 TB/s (256 bytes: 5.1).  The gradients lose
+// 13 us to three launches, and a wave waits between its loads and its stores.
 #include "block_device.h"
 
 namespace kda {

@@ -10,11 +10,12 @@
 // sequence's boundary is the same for all its lanes: the last W - 1 tokens and their
 // gradients slide through registers, while the loads of the next four tokens are
 // under way.  (Four and eight channels a lane leave too few waves, and in the
-// gradients too few registers: 4096 tokens of 4096 bf16 channels, gradients 34 us
-// with two, 42 with four, 56 with eight.)
-// Measured (bf16, 4 taps, silu): 35862 packed tokens of 12288 channels 358 us, 4.9 TB/s;
-// 2 x 2048 tokens of 4096 channels 15.6 us, 4.3 TB/s, their gradients 27 us and 4.4 for the
-// sums over strips.
+// gradients too few registers: with the gates of the time, 4096 tokens of 4096 bf16
+// channels took 34 us with two, 42 with four, 56 with eight.)  The arithmetic is not far
+// behind: a gradient is some 40 instructions a channel, nine tenths of the time.
+// Measured (bf16, 4 taps, silu): 35862 packed tokens of 12288 channels 345 us, 5.1 TB/s;
+// 2 x 2048 tokens of 4096 channels 14.2 us, 4.7 TB/s, their gradients 26 us, 3.9 TB/s, and
+// 4.4 for the sums over strips.
 #include "block_device.h"
 
 namespace kda {
@@ -482,8 +483,8 @@ void by_taps(int W, bool fp32, bool silu, F&& f) {
 
 // Tokens of a strip, 16 or 32.  The gradients read W - 1 tokens more than a strip has, and
 // leave a row of sums for four strips; bf16 calls that fill the GPU with strips of 32 gain
-// by them (32768 tokens of 4096 channels: 182 us, 204 with 16; 2048 tokens: 24 and 22), fp32
-// calls do not (338 and 311), nor does the forward pass (109 and 108).
+// by them (32768 tokens of 4096 channels: 173 us, 194 with 16; 2048 tokens: 22.6 and 21.5),
+// fp32 calls do not (338 and 309), nor does the forward pass (109 and 106).
 int strip_of(int32_t B, int32_t T, int64_t blocks, bool fp32, bool backward) {
     return backward && !fp32 && (int64_t)B * ((T + 31) / 32) * blocks >= 16 * 256 ? 32 : 16;
 }
