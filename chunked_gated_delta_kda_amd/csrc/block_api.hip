@@ -55,7 +55,7 @@ struct ScanSpace {
 ScanSpace scan_space(int32_t B, int32_t T, int32_t C, bool packed, bool backward) {
     const size_t groups = packed ? ((size_t)T + 15) / 16 : 0;
     const bool one = T == 0 || (backward ? T <= kda::GS_TILE : !packed && T <= kda::GS_ONE_TILE);
-    const int64_t counters = std::min<int64_t>((int64_t)B * ((C + 63) / 64), kda::GS_MAX_COUNTERS);
+    const int64_t counters = (int64_t)B * ((C + 63) / 64);
     ScanSpace s{};
     s.tickets = 0;
     s.words = one ? 0 : align_up((size_t)counters * kda::GS_TICKET_BYTES);

@@ -17,7 +17,6 @@ constexpr int GS_TILE = 64;
 constexpr int GS_STATES = 8;
 constexpr int GS_ONE_TILE = 256;  // most tokens of a row that the forward pass has as one tile
 constexpr int GS_TICKET_BYTES = 64;  // counters do not share a line
-constexpr int GS_MAX_COUNTERS = 8192;
 
 struct ScanArgs {
     const void* x;          // [B, T, C] tokens
@@ -36,8 +35,7 @@ struct ScanArgs {
     // (neither is used where a row is one tile)
     uint64_t* words;        // [tiles, B, C]
     int32_t far;            // whether a tile looks at 32 before it, not 8 (enter_tile)
-    int32_t beside;         // chains of a counter
-    uint32_t* tickets;      // the counters, GS_TICKET_BYTES apart
+    uint32_t* tickets;      // a counter for each chain, GS_TICKET_BYTES apart
     // packed batches: per 16 tokens, whether each begins a sequence,
     // belongs to one, ends one; per token, which
     uint2* marks;           // [ceil(T / 16)]

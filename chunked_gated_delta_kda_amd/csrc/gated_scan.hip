@@ -17,13 +17,13 @@
 // tokens, since a token has twice the values to keep; the states they need are scanned
 // again from those that the forward pass kept of every eighth token.  One channel a lane
 // keeps a forward wave within 64 registers, so that eight fit on a SIMD; two channels a
-// lane (rows of 256 bytes) gain nothing: 131072 x 2048 bf16 tokens 501 us, 468 with one,
-// and the gradients of 2 x 2048 x 4096 the same to 1%.
-// Measured (bf16): 131072 x 2048 468 us, 4.6 TB/s; 2 x 2048 x 4096 with
-// the states kept 38 us, 3.7 TB/s; their gradients 78 us with the launches before and
-// behind, 3.2 TB/s.  Rows of 128 bytes are what bounds the long call: a kernel that only
-// moves the same rows the same way reaches 4.7 TB/s (256 bytes: 5.1).  The gradients lose
-// 13 us to three launches, and a wave waits between its loads and its stores.
+// lane (rows of 256 bytes) are slower: 131072 x 2048 bf16 tokens took 501 us with two when
+// they took 468 with one, and the gradients of 2 x 2048 x 4096 the same to 1%.
+// Measured (bf16): 131072 x 2048 454 us, 4.7 TB/s; 2 x 2048 x 4096 with the states kept
+// 38 us, 3.7 TB/s; their gradients 76 us with the launches before and behind, 3.3 TB/s.
+// What bounds the long call is the memory: a kernel that only moves such rows reaches
+// 4.7 TB/s (of 256 bytes: 5.1).  The gradients lose 13 us to three launches, and a wave
+// waits between its loads and its stores.
 #include "block_device.h"
 
 namespace kda {
@@ -279,25 +279,27 @@ __global__ __launch_bounds__(256) void gated_scan_prepare_kernel(PrepareArgs q) 
     for (int c = threadIdx.x; c < a.C; c += 256) q.dst[n * a.C + c] = q.src ? q.src[n * a.C + c] : 0.f;
 }
 
-// The tile that this workgroup takes.  A counter has the tiles of a.beside chains (a row of
-// the batch and a block of channels) side by side, in the order of time; workgroup i draws
-// from counter i % counters, as many from each as it has tiles.
+// The tile that this workgroup takes: of a chain (a row of the batch and a block of
+// channels) the next in the order of time, by the chain's counter, so that the tiles that it
+// waits for run already, whatever the order in which workgroups start.  Workgroups go to the
+// chains one after the other, as many to each as it has tiles.  They also go to the XCDs one
+// after the other: where the number of chains is a multiple of 8, the eight change places
+// from one round to the next, or an XCD would read the same columns of every row, which
+// share few of its L2's channels (131072 x 2048 454 us, 543 without; 32768 x 1024 66 and
+// 76).  One counter for all chains deals them out well enough, but is a queue: 467 and 75
+// us, and 2048 x 4096 32 us, not 22.
 struct Place {
     uint32_t chain, order;
     __device__ __forceinline__ Place(const ScanArgs& a, uint32_t tiles, uint32_t chains) {
         __shared__ uint32_t ticket;
         const uint32_t wg = blockIdx.z * gridDim.x + blockIdx.x;  // (fewer than 2^31 have a tile)
-        if (tiles == 1 || wg >= chains * tiles) {
-            chain = wg % chains;
-            order = wg / chains;
-            return;
-        }
-        const uint32_t counters = chains / a.beside, counter = wg % counters;
-        if (threadIdx.x == 0) ticket = atomicAdd(a.tickets + counter * TICKET_WORDS, 1u);
+        order = wg / chains;
+        chain = wg % chains;
+        if (tiles == 1 || order >= tiles) return;
+        if (chains % 8 == 0) chain = (chain & ~7u) + ((chain + order) & 7);
+        if (threadIdx.x == 0) ticket = atomicAdd(a.tickets + (int64_t)chain * TICKET_WORDS, 1u);
         __syncthreads();
-        const uint32_t mine = __builtin_amdgcn_readfirstlane(ticket);
-        chain = counter * a.beside + mine % a.beside;
-        order = mine / a.beside;
+        order = __builtin_amdgcn_readfirstlane(ticket);
     }
 };
 
@@ -559,7 +561,7 @@ void launch_prepare(const ScanArgs& a, int tiles, int64_t chains, const float* s
     PrepareArgs q{};
     q.a = a;
     q.n_words = tiles > 1 ? (int64_t)tiles * a.B * a.C : 0;
-    q.n_tickets = tiles > 1 ? chains / a.beside : 0;
+    q.n_tickets = tiles > 1 ? chains : 0;
     q.fill = (q.n_words + 2047) / 2048;
     q.marks = a.cu ? ((int64_t)a.T + 255) / 256 : 0;
     q.src = src;
@@ -568,19 +570,14 @@ void launch_prepare(const ScanArgs& a, int tiles, int64_t chains, const float* s
     if (groups) hipLaunchKernelGGL(gated_scan_prepare_kernel, wide_grid(groups, 256), dim3(256), 0, stream, q);
 }
 
-// Where all tiles are at work within a few rounds, a chain has a counter of its own: one
-// counter for all is a queue at the start (forward 2048 tokens of 4096 channels, 1024 tiles:
-// 21.7 us, 32.3 with one; 8192 tokens: 66, 76), but keeps the chains of a longer call side
-// by side in memory (131072 tokens of 2048, 32768 tiles: 468 us, 543 with one each; gradients
-// of 8192 tokens of 4096, 8192 tiles: 144 and 148).  And where they all start at about the same time,
-// a tile looks far (odd packed batch with gradients: 60 us, 67 without; gradients of 32768
-// tokens of 1024 channels, 8192 tiles: 174, 151 without).
-constexpr int64_t FAR_TILES = 2048, OWN_TILES_BWD = 2048, OWN_TILES_FWD = GS_MAX_COUNTERS;
+// Where all tiles start at about the same time, a tile looks far (odd packed batch with
+// gradients: 60 us, 67 without; gradients of 32768 tokens of 1024 channels, 8192 tiles: 174,
+// 151 without).
+constexpr int64_t FAR_TILES = 2048;
 
-int64_t set_chains(ScanArgs& a, int tiles, int64_t own_tiles) {
+int64_t set_chains(ScanArgs& a, int tiles) {
     const int64_t chains = (int64_t)a.B * ((a.C + 63) / 64);
     a.far = chains * tiles <= FAR_TILES;
-    a.beside = chains * tiles <= own_tiles ? 1 : (int32_t)chains;
     return chains;
 }
 
@@ -598,7 +595,7 @@ void launch_gated_scan_fwd(const ScanArgs& args, bool fp32, hipStream_t stream) 
     // launch before this one (256 tokens of 256 channels: 11.0 us a call, 15.6 in two tiles).
     const bool one = !a.cu && a.T > FWD_TILE && a.T <= GS_ONE_TILE;
     const int tiles = one ? 1 : tiles_of(a.T, FWD_TILE);
-    const int64_t chains = set_chains(a, tiles, OWN_TILES_FWD);
+    const int64_t chains = set_chains(a, tiles);
     launch_prepare(a, tiles, chains, a.h0, a.h_final, stream);
     if (a.T == 0) return;
     by_type(fp32, a.cu != nullptr, [&](auto t, auto packed) {
@@ -620,7 +617,7 @@ void launch_gated_scan_fwd(const ScanArgs& args, bool fp32, hipStream_t stream) 
 void launch_gated_scan_bwd(const ScanArgs& args, bool fp32, hipStream_t stream) {
     ScanArgs a = args;
     const int tiles = tiles_of(a.T, BWD_TILE);
-    const int64_t chains = set_chains(a, tiles, OWN_TILES_BWD);
+    const int64_t chains = set_chains(a, tiles);
     launch_prepare(a, tiles, chains, a.d_final, a.dh0, stream);
     if (a.T > 0) {
         by_type(fp32, a.cu != nullptr, [&](auto t, auto packed) {
