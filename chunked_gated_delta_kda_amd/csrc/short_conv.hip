@@ -13,7 +13,7 @@
 // gradients too few registers: with the gates of the time, 4096 tokens of 4096 bf16
 // channels took 34 us with two, 42 with four, 56 with eight.)  The arithmetic is not far
 // behind: a gradient is some 40 instructions a channel, nine tenths of the time.
-// Measured (bf16, 4 taps, silu): 35862 packed tokens of 12288 channels 345 us, 5.1 TB/s;
+// Measured (bf16, 4 taps, silu): 35862 packed tokens of 12288 channels 334 us, 5.3 TB/s;
 // 2 x 2048 tokens of 4096 channels 14.2 us, 4.7 TB/s, their gradients 26 us, 3.9 TB/s, and
 // 4.4 for the sums over strips.
 #include "block_device.h"
@@ -82,6 +82,16 @@ __device__ __forceinline__ float slope(float z) {
 
 }  // namespace
 
+// The block of channels of workgroup wg, of those of a group of strips.  Workgroups go to
+// the XCDs one after the other: where the number of blocks is a multiple of 8, the eight
+// change places from one group to the next, or an XCD would read the same columns of every
+// row, which share few of its L2's channels (35862 packed tokens of 12288 channels 334 us,
+// 345 without; 32768 of 4096 100 and 105).
+__device__ __forceinline__ uint32_t column_of(uint32_t wg, uint32_t blocks) {
+    const uint32_t c = wg % blocks;
+    return blocks % 8 ? c : (c & ~7u) + ((c + wg / blocks) & 7);
+}
+
 // row j of the window in front of token t of sequence q: x_{t - W + 1 + j}
 template <class S, int W>
 __device__ __forceinline__ void window_row(const ConvArgs& a, const Seq& q, int64_t row0, int t, int j, int c,
@@ -126,7 +136,7 @@ __global__ __launch_bounds__(SC_THREADS) void short_conv_fwd_kernel(ConvArgs a) 
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t per_row = (a.T + a.strip - 1) / a.strip, strip = wg / blocks * SC_WAVES + w;
     const int b = strip / max(per_row, 1u);
-    const int c = ((int)(wg % blocks) * 64 + (threadIdx.x & 63)) * V;
+    const int c = ((int)column_of(wg, blocks) * 64 + (threadIdx.x & 63)) * V;
     if (b >= a.B) return;
     const int t0 = strip % per_row * a.strip, t1 = min(t0 + a.strip, a.T);
     Seq q;
@@ -228,7 +238,7 @@ __global__ __launch_bounds__(SC_THREADS, 4) void short_conv_bwd_kernel(ConvArgs 
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const uint32_t per_row = (a.T + a.strip - 1) / a.strip, strip = group * SC_WAVES + w;
     const int b = strip / max(per_row, 1u);
-    const int c = ((int)(wg % blocks) * 64 + lane) * V;
+    const int c = ((int)column_of(wg, blocks) * 64 + lane) * V;
     float dw[W + 1][V];
 #pragma unroll
     for (int j = 0; j <= W; ++j)
@@ -397,7 +407,7 @@ __global__ __launch_bounds__(SC_THREADS, 4) void short_conv_bwd_kernel(ConvArgs 
         for (int v = 0; v < V; ++v) red[w][j][v][lane] = dw[j][v];
     __syncthreads();
     for (int i = threadIdx.x; i < (W + 1) * CB; i += SC_THREADS) {
-        const int j = i / CB, l = i % CB / V, v = i % V, ch = (int)(wg % blocks) * CB + i % CB;
+        const int j = i / CB, l = i % CB / V, v = i % V, ch = (int)column_of(wg, blocks) * CB + i % CB;
         if (ch >= a.C) continue;
         float s = 0.f;
         for (int k = 0; k < SC_WAVES; ++k) s += red[k][j][v][l];
