@@ -374,7 +374,11 @@ def gated_scan(x, g, input_gate, A_log, dt_bias, initial_state=None, output_fina
                cu_seqlens=None):
     """Differentiable gated linear recurrence over channels (see gated_scan_fwd).  Returns
     (o, final_state); final_state is None unless ``output_final_state``.  Gradients reach x,
-    g, input_gate, A_log, dt_bias and initial_state."""
+    g, input_gate, A_log, dt_bias and initial_state; where none is asked for, the states
+    that they need are not kept."""
+    leaves = (x, g, input_gate, A_log, dt_bias, initial_state)
+    if not (_torch().is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in leaves)):
+        return _b.gated_scan_fwd(*leaves, output_final_state, cu_seqlens)
     out = _GatedScan.get().apply(x, g, input_gate, A_log, dt_bias, initial_state, cu_seqlens,
                                  bool(output_final_state))
     return out if output_final_state else (out, None)

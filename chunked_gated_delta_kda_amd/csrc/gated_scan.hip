@@ -18,7 +18,9 @@
 // again from those that the forward pass kept of every eighth token.  One channel a lane
 // keeps a forward wave within 64 registers, so that eight fit on a SIMD; two channels a
 // lane (rows of 256 bytes) are slower: 131072 x 2048 bf16 tokens took 501 us with two when
-// they took 468 with one, and the gradients of 2 x 2048 x 4096 the same to 1%.
+// they took 468 with one, 571 and 448 with eight tokens a wave, and the gradients of
+// 2 x 2048 x 4096 the same to 1%.  Tiles of 256 tokens halve what tiles exchange, and end
+// later: 443 and 448 us, packed prompts 268 and 254.
 // Measured (bf16): 131072 x 2048 454 us, 4.7 TB/s; 2 x 2048 x 4096 with the states kept
 // 38 us, 3.7 TB/s; their gradients 76 us with the launches before and behind, 3.3 TB/s.
 // What bounds the long call is the memory: a kernel that only moves such rows reaches

@@ -130,6 +130,21 @@ def test_convolution_of_single_tokens_has_the_prompts_bits(dtype):
     assert torch.equal(s, state)
 
 
+@pytest.mark.parametrize("final", [True, False])
+def test_recurrence_without_gradients_keeps_no_states(final):
+    w = make(2, 300, 64, "bf16", seed=79)
+    d = {k: t.to(DEV).requires_grad_(k in LEAVES) for k, t in w.items()}
+    names = ("x", "g", "gate", "A_log", "dt_bias")
+    o, f = kda.gated_scan(*(d[k] for k in names), output_final_state=final)
+    assert o.requires_grad
+    with torch.no_grad():
+        got = kda.gated_scan(*(d[k] for k in names), output_final_state=final)
+    plain = kda.gated_scan(*(d[k].detach() for k in names), output_final_state=final)
+    for q in (got, plain):
+        assert torch.equal(q[0], o) and not q[0].requires_grad
+        assert torch.equal(q[1], f) if final else q[1] is None
+
+
 def test_refusals_on_a_gpu():
     x = torch.zeros(2, 300, 64, dtype=torch.bfloat16, device=DEV)
     p = torch.zeros(64, device=DEV)

@@ -139,3 +139,27 @@ def test_layer_norm_of_2_to_the_32_elements():
         p = x[i:i + 10].contiguous()
         assert torch.equal(y[i:i + 10], kda.layer_norm_fwd(p, w, w)[0])
         assert torch.equal(r["dx"][i:i + 10], kda.layer_norm_bwd(p, w, p)["dx"])
+
+
+def test_rows_of_2_to_the_20_channels():
+    """The widest rows, 2^31 bytes and more of them: as their blocks of channels alone."""
+    T, C = 1100, 1 << 20
+    x = normal(22, 1, T, C)
+    A, bias = normal(23, C, dtype=torch.float32), normal(24, C, dtype=torch.float32)
+    taps = normal(25, C, 4, dtype=torch.float32)
+    say(f"[scan] {T} tokens of {C}")
+    o, f, s = kda.gated_scan_fwd_save(x, x, x, A, bias)
+    r = kda.gated_scan_bwd(x, x, x, A, bias, x, s)
+    say(f"[conv] {T} tokens of {C}")
+    y, _ = kda.short_conv_fwd(x, taps)
+    g = kda.short_conv_bwd(x, taps, x)
+    for c in (0, C // 2 + 128, C - 128):
+        cut = slice(c, c + 128)
+        p, a, b, w = x[..., cut].contiguous(), A[cut].contiguous(), bias[cut].contiguous(), taps[cut].contiguous()
+        o1, f1, s1 = kda.gated_scan_fwd_save(p, p, p, a, b)
+        assert torch.equal(o[..., cut], o1) and torch.equal(f[:, cut], f1)
+        r1 = kda.gated_scan_bwd(p, p, p, a, b, p, s1)
+        for k in ("dx", "dg", "dinput_gate", "dA_log", "ddt_bias", "dh0"):
+            assert torch.equal(r[k][..., cut], r1[k]), k
+        assert torch.equal(y[..., cut], kda.short_conv_fwd(p, w)[0])
+        assert torch.equal(g["dx"][..., cut], kda.short_conv_bwd(p, w, p)["dx"])
