@@ -22,7 +22,8 @@
 // 2 x 2048 x 4096 the same to 1%.  Tiles of 256 tokens halve what tiles exchange, and end
 // later: 443 and 448 us, packed prompts 268 and 254.
 // Measured (bf16): 131072 x 2048 454 us, 4.7 TB/s; 2 x 2048 x 4096 with the states kept
-// 38 us, 3.7 TB/s; their gradients 76 us with the launches before and behind, 3.3 TB/s.
+// 38 us, 3.7 TB/s; their gradients 70 us with the launches before and behind, 3.6 TB/s;
+// those of 16384 x 4096 242 us, 4.0 TB/s.
 // What bounds the long call is the memory: a kernel that only moves such rows reaches
 // 4.7 TB/s (of 256 bytes: 5.1).  The gradients lose 13 us to three launches, and a wave
 // waits between its loads and its stores.
@@ -394,10 +395,11 @@ __global__ __launch_bounds__(64 * WAVES, 8) void gated_scan_fwd_kernel(ScanArgs 
 
 // A wave knows the state that enters its eight tokens, and so everything but the gradients
 // that come back to them: what each gradient is of those is made ready before they are
-// known, and there is little to do behind enter_tile.  (Bounded to six waves a SIMD it
-// spills: 2 x 2048 x 4096 with its forward pass 127.6 us, 122.3 with five.)
+// known, and there is little to do behind enter_tile.  Behind it the decays are formed again:
+// eight registers less, and six waves a SIMD, not five (16384 x 4096 bf16: 242 us, 267 with
+// the decays kept; 270 with seven waves, which spill).
 template <class T, bool PACKED>
-__global__ __launch_bounds__(GS_THREADS, 4) void gated_scan_bwd_kernel(ScanArgs a) {
+__global__ __launch_bounds__(GS_THREADS, 6) void gated_scan_bwd_kernel(ScanArgs a) {
     __shared__ float s_prod[GS_WAVES][64], s_sum[GS_WAVES][64];
     __shared__ uint64_t look[FAR][64];
     const int tiles = tiles_of(a.T, BWD_TILE);
@@ -500,7 +502,8 @@ __global__ __launch_bounds__(GS_THREADS, 4) void gated_scan_bwd_kernel(ScanArgs 
         if (PACKED && m.last >> t & 1) back = state_of(a.d_final, t);
         if (!PACKED || m.in >> t & 1) {
             const float et = value<T>(rd[t]) + back;
-            back = dec[t] * et;
+            asm volatile("" : "+v"(L[t]));  // (or the decay of before would be kept)
+            back = __builtin_amdgcn_exp2f(-L[t]) * et;
             const float pt = back * fp[t];
             dx = et * fx[t];
             di = et * fi[t];
