@@ -34,7 +34,6 @@ struct ScanArgs {
     // what the tiles of a chain post for those behind them, and counters of tiles taken
     // (neither is used where a row is one tile)
     uint64_t* words;        // [tiles, B, C]
-    int32_t far;            // whether a tile looks at 32 before it, not 8 (enter_tile)
     uint32_t* tickets;      // a counter for each chain, GS_TICKET_BYTES apart
     // packed batches: per 16 tokens, whether each begins a sequence,
     // belongs to one, ends one; per token, which

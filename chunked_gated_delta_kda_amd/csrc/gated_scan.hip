@@ -22,11 +22,10 @@
 // 2 x 2048 x 4096 the same to 1%.  Tiles of 256 tokens halve what tiles exchange, and end
 // later: 443 and 448 us, packed prompts 268 and 254.
 // Measured (bf16): 131072 x 2048 454 us, 4.7 TB/s; 2 x 2048 x 4096 with the states kept
-// 38 us, 3.7 TB/s; their gradients 70 us with the launches before and behind, 3.6 TB/s;
-// those of 16384 x 4096 242 us, 4.0 TB/s.
+// 38 us, 3.7 TB/s; their gradients 64 us with the launches before and behind, 3.9 TB/s;
+// those of 16384 x 4096 230 us, 4.2 TB/s.
 // What bounds the long call is the memory: a kernel that only moves such rows reaches
-// 4.7 TB/s (of 256 bytes: 5.1).  The gradients lose 13 us to three launches, and a wave
-// waits between its loads and its stores.
+// 4.7 TB/s (of 256 bytes: 5.1).  The gradients lose 13 us to three launches.
 #include "block_device.h"
 
 namespace kda {
@@ -137,13 +136,14 @@ __device__ __forceinline__ void await_words(const uint64_t* own, int64_t step, i
 // The state that enters tile `order` of a chain (0: `first`), whose own product and sum
 // are (prod, sum) in the last wave.  The words of the eight tiles before this one are
 // looked at first, one by each wave, and the oldest is waited for until it is a state; on a
-// small grid (a.far), where none of the eight is a state in all channels, those of the next
+// small grid (far), where none of the eight is a state in all channels, those of the next
 // 24, of which the oldest is waited for.  Folded from the oldest on, this is the same sum in
 // the same order whatever each tile had posted by then: bits do not depend on time.  A tile
 // waits only for tiles whose tickets were drawn before its own: those run already, and wait
 // for earlier ones in turn.
 constexpr int NEAR = GS_WAVES, FAR = 4 * GS_WAVES;
 
+template <bool far>
 __device__ __forceinline__ float enter_tile(const ScanArgs& a, int tiles, int order, int64_t column, bool active,
                                             int w, int lane, float prod, float sum, float first,
                                             uint64_t (*look)[64]) {
@@ -153,10 +153,10 @@ __device__ __forceinline__ float enter_tile(const ScanArgs& a, int tiles, int or
     float in = first;
     if (order > 0) {
         if (poster) post(own, prod, sum);
-        await_words<1>(own, step, order, w, a.far ? -1 : NEAR - 1, lane, look);
+        await_words<1>(own, step, order, w, far ? -1 : NEAR - 1, lane, look);
         __syncthreads();
         int from = min(order, NEAR) - 1;
-        if (a.far && order > NEAR) {
+        if (far && order > NEAR) {
             bool state = false;
 #pragma unroll
             for (int j = 0; j < NEAR; ++j) state = state || word_prod(look[j][lane]) == 0.f;
@@ -293,28 +293,30 @@ __global__ __launch_bounds__(256) void gated_scan_prepare_kernel(PrepareArgs q) 
 // us, and 2048 x 4096 32 us, not 22.
 struct Place {
     uint32_t chain, order;
-    __device__ __forceinline__ Place(const ScanArgs& a, uint32_t tiles, uint32_t chains) {
-        __shared__ uint32_t ticket;
+    // lds: a place for the ticket, written to only behind the next barrier
+    __device__ __forceinline__ Place(const ScanArgs& a, uint32_t tiles, uint32_t chains, void* lds) {
+        uint32_t* ticket = static_cast<uint32_t*>(lds);
         const uint32_t wg = blockIdx.z * gridDim.x + blockIdx.x;  // (fewer than 2^31 have a tile)
         order = wg / chains;
         chain = wg % chains;
         if (tiles == 1 || order >= tiles) return;
         if (chains % 8 == 0) chain = (chain & ~7u) + ((chain + order) & 7);
-        if (threadIdx.x == 0) ticket = atomicAdd(a.tickets + (int64_t)chain * TICKET_WORDS, 1u);
+        if (threadIdx.x == 0) *ticket = atomicAdd(a.tickets + (int64_t)chain * TICKET_WORDS, 1u);
         __syncthreads();
-        order = __builtin_amdgcn_readfirstlane(ticket);
+        order = __builtin_amdgcn_readfirstlane(*ticket);
     }
 };
 
 // WAVES: 8, or 16 where that makes a row one tile (then nothing is posted).
-template <class T, bool PACKED, int WAVES>
+template <class T, bool PACKED, bool far, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 8) void gated_scan_fwd_kernel(ScanArgs a) {
     constexpr int TILE = WAVES * FWD_STEPS;
     __shared__ float s_prod[WAVES][64], s_sum[WAVES][64];
+    __shared__ uint64_t look[far ? FAR : NEAR][64];
     const int tiles = tiles_of(a.T, TILE);
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t blocks = (a.C + 63) / 64;
-    const Place place(a, tiles, a.B * blocks);
+    const Place place(a, tiles, a.B * blocks, look);
     const int k = place.order, b = place.chain / blocks, own = place.chain % blocks * 64 + lane;
     if (k >= tiles) return;
     const bool active = own < a.C;
@@ -373,8 +375,7 @@ __global__ __launch_bounds__(64 * WAVES, 8) void gated_scan_fwd_kernel(ScanArgs 
     const float first = k == 0 && !PACKED && a.h0 ? a.h0[(int64_t)b * a.C + c] : 0.f;
     float in = first;
     if constexpr (WAVES == GS_WAVES) {
-        __shared__ uint64_t look[FAR][64];
-        in = enter_tile(a, tiles, k, (int64_t)b * a.C + c, active, w, lane, join(p, bp), carry(p, h, bs), first, look);
+            in = enter_tile<far>(a, tiles, k, (int64_t)b * a.C + c, active, w, lane, join(p, bp), carry(p, h, bs), first, look);
     }
     if (!active) return;
     const float enter = carry(bp, bs, in);
@@ -395,17 +396,20 @@ __global__ __launch_bounds__(64 * WAVES, 8) void gated_scan_fwd_kernel(ScanArgs 
 
 // A wave knows the state that enters its eight tokens, and so everything but the gradients
 // that come back to them: what each gradient is of those is made ready before they are
-// known, and there is little to do behind enter_tile.  Behind it the decays are formed again:
-// eight registers less, and six waves a SIMD, not five (16384 x 4096 bf16: 242 us, 267 with
-// the decays kept; 270 with seven waves, which spill).
-template <class T, bool PACKED>
-__global__ __launch_bounds__(GS_THREADS, 6) void gated_scan_bwd_kernel(ScanArgs a) {
+// known, and there is little to do behind enter_tile.  A wave waits between its loads and
+// its stores, so that many of them are needed: two of the factors wait in LDS, and the decays
+// are formed again behind it, for 64 registers and four workgroups on a CU (16384 x 4096
+// bf16: 230 us; 246 with all factors in registers, three workgroups; 267 with the decays,
+// too, two).  Looking far takes 12 KB more of LDS, and leaves three.
+template <class T, bool PACKED, bool far>
+__global__ __launch_bounds__(GS_THREADS, far ? 6 : 8) void gated_scan_bwd_kernel(ScanArgs a) {
     __shared__ float s_prod[GS_WAVES][64], s_sum[GS_WAVES][64];
-    __shared__ uint64_t look[FAR][64];
+    __shared__ uint64_t look[far ? FAR : NEAR][64];
+    __shared__ float2 park[BWD_STEPS][GS_THREADS];
     const int tiles = tiles_of(a.T, BWD_TILE);
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t blocks = (a.C + 63) / 64;
-    const Place place(a, tiles, a.B * blocks);
+    const Place place(a, tiles, a.B * blocks, look);
     const int order = place.order, k = tiles - 1 - order;
     const int b = place.chain / blocks, own = place.chain % blocks * 64 + lane;
     if (k < 0) return;
@@ -445,7 +449,7 @@ __global__ __launch_bounds__(GS_THREADS, 6) void gated_scan_bwd_kernel(ScanArgs 
     }
     // With e the gradient of h_t: dx = e fx, di = e fi, dL/dL_t = (a e) fp, and
     // dg = (a e) fp fg
-    float dec[BWD_STEPS], L[BWD_STEPS], fx[BWD_STEPS], fi[BWD_STEPS], fp[BWD_STEPS], fg[BWD_STEPS];
+    float dec[BWD_STEPS], L[BWD_STEPS], fp[BWD_STEPS], fg[BWD_STEPS];
 #pragma unroll
     for (int t = 0; t < BWD_STEPS; ++t) {
         const float z = value<T>(rg[t]) + bias, x = value<T>(rx[t]);
@@ -455,14 +459,14 @@ __global__ __launch_bounds__(GS_THREADS, 6) void gated_scan_bwd_kernel(ScanArgs 
         if (PACKED && (m.start >> t & 1)) h = state_of(a.h0, t);
         dec[t] = d.a;
         L[t] = d.L;
-        fx[t] = root * ig.s;
-        fi[t] = root * x * ig.slope;
+        const float fx = root * ig.s;
+        park[t][threadIdx.x] = make_float2(fx, root * x * ig.slope);
         // (no decay at all: nothing of the input enters, and sigmoid(z) is zero)
         fp[t] = fmaf(d.a * ig.s * x, root == 0.f ? 0.f : __builtin_amdgcn_rcpf(root), -h);
         fg[t] = amount * d.sigmoid();
-        h = fmaf(d.a, h, fx[t] * x);
+        h = fmaf(d.a, h, fx * x);
         // (here, and not where they are used: what they are made of would stay in registers)
-        asm volatile("" : "+v"(fx[t]), "+v"(fi[t]), "+v"(fp[t]), "+v"(fg[t]));
+        asm volatile("" : "+v"(fp[t]), "+v"(fg[t]));
     }
     // gradients of the states, from zero, last token first: what reaches the state before a
     // token is a (do + what reaches its own)
@@ -490,7 +494,7 @@ __global__ __launch_bounds__(GS_THREADS, 6) void gated_scan_bwd_kernel(ScanArgs 
         bp = join(s_prod[j][lane], bp);
     }
     const float first = order == 0 && !PACKED && a.d_final ? a.d_final[(int64_t)b * a.C + c] : 0.f;
-    const float in = enter_tile(a, tiles, order, (int64_t)b * a.C + c, active, w, lane, bp, bs, first, look);
+    const float in = enter_tile<far>(a, tiles, order, (int64_t)b * a.C + c, active, w, lane, bp, bs, first, look);
     float back = in;
     if (w < GS_WAVES - 1) back = carry(bp, bs, in);
     else if (!PACKED && a.dh0 && k == 0 && active) a.dh0[(int64_t)b * a.C + c] = carry(bp, bs, in);
@@ -505,8 +509,9 @@ __global__ __launch_bounds__(GS_THREADS, 6) void gated_scan_bwd_kernel(ScanArgs 
             asm volatile("" : "+v"(L[t]));  // (or the decay of before would be kept)
             back = __builtin_amdgcn_exp2f(-L[t]) * et;
             const float pt = back * fp[t];
-            dx = et * fx[t];
-            di = et * fi[t];
+            const float2 f = park[t][threadIdx.x];
+            dx = et * f.x;
+            di = et * f.y;
             dg = pt * fg[t];
             dA = fmaf(pt, L[t], dA);
             db += dg;
@@ -580,54 +585,51 @@ void launch_prepare(const ScanArgs& a, int tiles, int64_t chains, const float* s
 // 32768 x 1024, 8192 tiles: 148, 137 without).
 constexpr int64_t FAR_TILES = 2048;
 
-int64_t set_chains(ScanArgs& a, int tiles) {
-    const int64_t chains = (int64_t)a.B * ((a.C + 63) / 64);
-    a.far = chains * tiles <= FAR_TILES;
-    return chains;
-}
+int64_t chains_of(const ScanArgs& a) { return (int64_t)a.B * ((a.C + 63) / 64); }
 
 template <class F>
-void by_type(bool fp32, bool packed, F&& f) {
-    if (fp32) packed ? f(float{}, std::true_type{}) : f(float{}, std::false_type{});
-    else packed ? f(uint16_t{}, std::true_type{}) : f(uint16_t{}, std::false_type{});
+void by_type(bool fp32, bool packed, bool far, F&& f) {
+    const auto with = [&](auto t) {
+        const auto looks = [&](auto p) { far ? f(t, p, std::true_type{}) : f(t, p, std::false_type{}); };
+        packed ? looks(std::true_type{}) : looks(std::false_type{});
+    };
+    fp32 ? with(float{}) : with(uint16_t{});
 }
 
 }  // namespace
 
-void launch_gated_scan_fwd(const ScanArgs& args, bool fp32, hipStream_t stream) {
-    ScanArgs a = args;
+void launch_gated_scan_fwd(const ScanArgs& a, bool fp32, hipStream_t stream) {
     // Rows of 129 to 256 tokens in one tile of sixteen waves need no words, and so no
     // launch before this one (256 tokens of 256 channels: 11.0 us a call, 15.6 in two tiles).
     const bool one = !a.cu && a.T > FWD_TILE && a.T <= GS_ONE_TILE;
     const int tiles = one ? 1 : tiles_of(a.T, FWD_TILE);
-    const int64_t chains = set_chains(a, tiles);
+    const int64_t chains = chains_of(a);
     launch_prepare(a, tiles, chains, a.h0, a.h_final, stream);
     if (a.T == 0) return;
-    by_type(fp32, a.cu != nullptr, [&](auto t, auto packed) {
+    by_type(fp32, a.cu != nullptr, !one && chains * tiles <= FAR_TILES, [&](auto t, auto packed, auto far) {
         using T = decltype(t);
-        constexpr bool PACKED = decltype(packed)::value;
-        const dim3 grid = wide_grid(chains * tiles, GS_THREADS);
-        if constexpr (!PACKED) {
+        constexpr bool PACKED = decltype(packed)::value, LOOKS = decltype(far)::value;
+        if constexpr (!PACKED && !LOOKS) {
             constexpr int WAVES = GS_ONE_TILE / FWD_STEPS;
             if (one) {
-                hipLaunchKernelGGL((gated_scan_fwd_kernel<T, false, WAVES>), wide_grid(chains, 64 * WAVES),
+                hipLaunchKernelGGL((gated_scan_fwd_kernel<T, false, false, WAVES>), wide_grid(chains, 64 * WAVES),
                                    dim3(64 * WAVES), 0, stream, a);
                 return;
             }
         }
-        hipLaunchKernelGGL((gated_scan_fwd_kernel<T, PACKED, GS_WAVES>), grid, dim3(GS_THREADS), 0, stream, a);
+        hipLaunchKernelGGL((gated_scan_fwd_kernel<T, PACKED, LOOKS, GS_WAVES>), wide_grid(chains * tiles, GS_THREADS),
+                           dim3(GS_THREADS), 0, stream, a);
     });
 }
 
-void launch_gated_scan_bwd(const ScanArgs& args, bool fp32, hipStream_t stream) {
-    ScanArgs a = args;
+void launch_gated_scan_bwd(const ScanArgs& a, bool fp32, hipStream_t stream) {
     const int tiles = tiles_of(a.T, BWD_TILE);
-    const int64_t chains = set_chains(a, tiles);
+    const int64_t chains = chains_of(a);
     launch_prepare(a, tiles, chains, a.d_final, a.dh0, stream);
     if (a.T > 0) {
-        by_type(fp32, a.cu != nullptr, [&](auto t, auto packed) {
+        by_type(fp32, a.cu != nullptr, chains * tiles <= FAR_TILES, [&](auto t, auto packed, auto far) {
             using T = decltype(t);
-            hipLaunchKernelGGL((gated_scan_bwd_kernel<T, decltype(packed)::value>),
+            hipLaunchKernelGGL((gated_scan_bwd_kernel<T, decltype(packed)::value, decltype(far)::value>),
                                wide_grid(chains * tiles, GS_THREADS), dim3(GS_THREADS), 0, stream, a);
         });
     }
