@@ -135,8 +135,8 @@ __device__ __forceinline__ void await_words(const uint64_t* own, int64_t step, i
 
 // The state that enters tile `order` of a chain (0: `first`), whose own product and sum
 // are (prod, sum) in the last wave.  The words of the eight tiles before this one are
-// looked at first, one by each wave, and the oldest is waited for until it is a state; on a
-// small grid (far), where none of the eight is a state in all channels, those of the next
+// looked at first, one by each wave, and the oldest is waited for until it is a state; with
+// few chains (far), where none of the eight is a state in all channels, those of the next
 // 24, of which the oldest is waited for.  Folded from the oldest on, this is the same sum in
 // the same order whatever each tile had posted by then: bits do not depend on time.  A tile
 // waits only for tiles whose tickets were drawn before its own: those run already, and wait
@@ -580,10 +580,11 @@ void launch_prepare(const ScanArgs& a, int tiles, int64_t chains, const float* s
     if (groups) hipLaunchKernelGGL(gated_scan_prepare_kernel, wide_grid(groups, 256), dim3(256), 0, stream, q);
 }
 
-// Where all tiles start at about the same time, a tile looks far (odd packed batch with
-// gradients: 59 us, 68 without; 131072 x 2048, 32768 tiles: 488, 458 without; gradients of
-// 32768 x 1024, 8192 tiles: 148, 137 without).
-constexpr int64_t FAR_TILES = 2048;
+// Few chains are short of tiles that can end, and a tile looks far; with more of them the
+// words that it reads cost more (bf16, 131072 x 512, 8 chains: forward 138 us, 176 without,
+// gradients 301 and 359; 65536 x 640, 10 chains: 89 and 103, 196 and 206; 32768 x 768, 12
+// chains: 57 and 61, 123 and 118; 16384 x 1024: 39 and 38, 79 and 67).
+constexpr int64_t FAR_CHAINS = 10;
 
 int64_t chains_of(const ScanArgs& a) { return (int64_t)a.B * ((a.C + 63) / 64); }
 
@@ -606,7 +607,7 @@ void launch_gated_scan_fwd(const ScanArgs& a, bool fp32, hipStream_t stream) {
     const int64_t chains = chains_of(a);
     launch_prepare(a, tiles, chains, a.h0, a.h_final, stream);
     if (a.T == 0) return;
-    by_type(fp32, a.cu != nullptr, !one && chains * tiles <= FAR_TILES, [&](auto t, auto packed, auto far) {
+    by_type(fp32, a.cu != nullptr, !one && chains <= FAR_CHAINS, [&](auto t, auto packed, auto far) {
         using T = decltype(t);
         constexpr bool PACKED = decltype(packed)::value, LOOKS = decltype(far)::value;
         if constexpr (!PACKED && !LOOKS) {
@@ -627,7 +628,7 @@ void launch_gated_scan_bwd(const ScanArgs& a, bool fp32, hipStream_t stream) {
     const int64_t chains = chains_of(a);
     launch_prepare(a, tiles, chains, a.d_final, a.dh0, stream);
     if (a.T > 0) {
-        by_type(fp32, a.cu != nullptr, chains * tiles <= FAR_TILES, [&](auto t, auto packed, auto far) {
+        by_type(fp32, a.cu != nullptr, chains <= FAR_CHAINS, [&](auto t, auto packed, auto far) {
             using T = decltype(t);
             hipLaunchKernelGGL((gated_scan_bwd_kernel<T, decltype(packed)::value, decltype(far)::value>),
                                wide_grid(chains * tiles, GS_THREADS), dim3(GS_THREADS), 0, stream, a);

@@ -87,6 +87,31 @@ def test_packed(lens, tail, dtype):
         assert not t[:, int(cu[-1]):].any()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens", [[700], [16, 112, 128, 1, 0, 300, 3, 77], [1] * 150 + [250]])
+def test_packed_in_many_chains(lens, dtype):
+    """More than ten chains: a tile waits for the eighth before it."""
+    cu = offsets(lens)
+    w = make(1, int(cu[-1]) + 5, 712, seed=len(lens), dtype=dtype, cu=cu)
+    for n in ("x", "g", "gate", "do"):
+        w[n][:, int(cu[-1]):] = float("nan")
+    o, f, r = check(w)
+    d = to_gpu(w)
+    cut = slice(640, 712)
+    part = [t[..., cut].contiguous() for t in args(d)]
+    o1, f1, s1 = kda.gated_scan_fwd_save(*part, d["h0"][:, cut].contiguous(), cu_seqlens=d["cu"])
+    r1 = kda.gated_scan_bwd(*part, d["do"][..., cut].contiguous(), s1, d["h0"][:, cut].contiguous(),
+                            d["dfinal"][:, cut].contiguous(), d["cu"])
+    assert torch.equal(o[..., cut], o1) and torch.equal(f[:, cut], f1)
+    for k, v in r1.items():
+        assert torch.equal(r[k][..., cut], v), k
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_long_in_many_chains(dtype):
+    check(make(3, 1500, 264, seed=5, dtype=dtype, slow=-7.0))
+
+
 def test_packed_that_begins_late():
     """Rows in front of the first sequence are outside every one, too."""
     cu = torch.tensor([20, 150, 150, 290], dtype=torch.int32)
@@ -303,8 +328,8 @@ def test_large_values_in_the_last_row():
 
 @pytest.mark.parametrize("B,T", [(11, 260), (1, 4300), (300, 4000), (16, 1400)])
 def test_counters_and_looks(B, T):
-    """Tiles in 33 chains, one or 300, the last too many for a tile to look at 32 before it:
-    it looks at 8, and finds the same sums in the same order."""
+    """Tiles in 33 chains, one, 300 or 16: where they are more than ten a tile looks at 8
+    before it, not at 32, and finds the same sums in the same order."""
     C = 136 if B == 11 else 64
     gen = torch.Generator(device=DEV).manual_seed(B)
     n = lambda *s: torch.randn(*s, generator=gen, device=DEV)  # noqa: E731
