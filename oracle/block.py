@@ -19,6 +19,7 @@ from .linear import spans
 # their product and of L / ln 2, at most 4 L 2^-24 together, and a by as much of itself:
 # L / 4 times STEP.
 STEP = 2.0 ** -20
+TINY = 2.0 ** -126  # the smallest normal number of fp32
 
 
 def _d(t):
@@ -106,7 +107,11 @@ def scan_all(x, g, i, A_log, dt_bias, h0=None, cu=None, do=None, dfinal=None):
     few = 4 * STEP  # the factors that a gradient is multiplied by at the end
     side = a * s * x.abs() * inv + pabs
     p_abs = a * eabs * side
-    p_err = a * (eerr * side + eabs * perr) + few * (1 + L / 4) * p_abs
+    # A decay below fp32's normal numbers counts as zero there: with a off by TINY, p = a e
+    # (a s x / m - h) is off by TINY e (a s x / m + h) (and the second a by as much of s x / m,
+    # again times a, which is then below TINY itself).  Times exp(A_log) sigmoid(z), or L,
+    # of a hundred it is above the floor that the tests allow by themselves.
+    p_err = a * (eerr * side + eabs * perr) + few * (1 + L / 4) * p_abs + TINY * eabs * side
     slope = torch.exp(A_log.detach()) * torch.sigmoid(g + dt_bias.detach())
     out.update(x=(grads["x"], (eerr + few * eabs) * m * s),
                i=(grads["i"], (eerr + few * eabs) * m * x.abs() * s * (1 - s)),
