@@ -48,23 +48,33 @@ struct BlockSigmoid {
     }
 };
 
-// sum of n values, `step` apart, 32 loads in flight at a time
-__device__ __forceinline__ double sum_strided(const float* p, int64_t n, int64_t step) {
-    double s = 0.0;
-    for (int64_t i = 0; i < n; i += 32) {
-        float v[32];
+// adds b values at a time to s, while there are any (all: while there are b)
+template <int b, bool all>
+__device__ __forceinline__ void add_batches(const float* p, int64_t& i, int64_t n, int64_t step, double& s) {
+    for (; all ? i + b <= n : i < n; i += b) {
+        float v[b];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = p[(i + k < n ? i + k : n - 1) * step];
+        for (int k = 0; k < b; ++k) v[k] = p[(all || i + k < n ? i + k : n - 1) * step];
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) s += i + k < n ? v[k] : 0.f;
+        for (int k = 0; k < b; ++k) s += all || i + k < n ? v[k] : 0.f;
     }
+}
+
+// sum of n values, `step` apart: 32 loads in flight at a time, 4 where fewer are left (the
+// convolution's gradients of 2 x 2048 x 4096 end with sums over 32 rows, 4 for a thread: a
+// call took 30.9 us with 32 loads there, too, and 28.7 with these)
+__device__ __forceinline__ double sum_strided(const float* p, int64_t n, int64_t step) {
+    double s = 0.0;
+    int64_t i = 0;
+    add_batches<32, true>(p, i, n, step, s);
+    add_batches<4, false>(p, i, n, step, s);
     return s;
 }
 
 // A workgroup of 256 threads adds 32 columns of n rows, `step` apart, in a fixed order and
 // in 64 bits: thread i has column i % 32 (where p points) and every 8th row.  Returns the
-// sum of the thread's column.
+// sum of the thread's column.  (512 threads: the same to 1%.)
 __device__ __forceinline__ double sum_columns(const float* p, int64_t n, int64_t step) {
     __shared__ double red[8][32];
     const int col = threadIdx.x % 32, first = threadIdx.x / 32;

@@ -15,7 +15,7 @@
 // over the rows and keep their lanes' channels of dweight and dbias in registers;
 // a second kernel adds the workgroups' sums in a fixed order, in 64 bits.
 // Measured (16384 x 4096 bf16): forward with a residual 102 us, 5.3 TB/s, gradients 114 us,
-// 4.7 TB/s; 3001 x 1000 fp32 forward 7.3 us, gradients 13.1 and their sum 4.4 (its 24 MB
+// 4.7 TB/s; 3001 x 1000 fp32 forward 7.3 us, gradients 13.1 and their sum 3.9 (its 24 MB
 // are in flight for too short a time: six rows a workgroup, one after the other).
 #include <algorithm>
 

@@ -15,7 +15,7 @@
 // behind: a gradient is some 40 instructions a channel, nine tenths of the time.
 // Measured (bf16, 4 taps, silu): 35862 packed tokens of 12288 channels 334 us, 5.3 TB/s;
 // 2 x 2048 tokens of 4096 channels 14.2 us, 4.7 TB/s, their gradients 26 us, 3.9 TB/s, and
-// 4.4 for the sums over strips.
+// 4 for the sums over strips.
 #include "block_device.h"
 
 namespace kda {
