@@ -22,8 +22,8 @@
 // 2 x 2048 x 4096 the same to 1%.  Tiles of 256 tokens halve what tiles exchange, and end
 // later: 443 and 448 us, packed prompts 268 and 254.
 // Measured (bf16): 131072 x 2048 454 us, 4.7 TB/s; 2 x 2048 x 4096 with the states kept
-// 38 us, 3.7 TB/s; their gradients 64 us with the launches before and behind, 3.9 TB/s;
-// those of 16384 x 4096 230 us, 4.2 TB/s.
+// 38 us, 3.7 TB/s; their gradients 61 us with the launches before and behind, 4.1 TB/s;
+// those of 16384 x 4096 210 us, 4.6 TB/s.
 // What bounds the long call is the memory: a kernel that only moves such rows reaches
 // 4.7 TB/s (of 256 bytes: 5.1).  The gradients lose 13 us to three launches.
 #include "block_device.h"
@@ -202,11 +202,31 @@ struct RowWalk {
         : at(((int64_t)b * a.T + min(t0, a.T - 1)) * row_bytes), left(a.T - 1 - t0), stride(row_bytes) {}
     __device__ __forceinline__ void next() { at += left-- > 0 ? stride : 0u; }
 };
+
+// The same with a lane's channel, for stores and for the gradients' loads: offsets in bytes
+// from `head`, which is the same for all lanes, so that an access takes one 32-bit addition
+// for all tensors of a row (gradients of 16384 x 4096 bf16: 212 us; 219 for the stores
+// alone, 226 without).  Loads of a packed batch are slower for it (15605 x 4096: 254 us, 230
+// for the stores alone, 234 without), and the forward pass, whose loads the compiler spreads
+// over the arithmetic to hold 64 registers, would spill.
+struct Rows {
+    int64_t head;
+    int last;
+    uint32_t stride, lane;
+    __device__ __forceinline__ Rows(const ScanArgs& a, int b, int t0, uint32_t row_bytes, uint32_t lane_bytes)
+        : head(((int64_t)b * a.T + min(t0, a.T - 1)) * row_bytes), last(max(a.T - 1 - t0, 0)), stride(row_bytes),
+          lane(lane_bytes) {}
+    __device__ __forceinline__ uint32_t at(int i) const {
+        uint32_t o = lane + (uint32_t)min(i, last) * stride;
+        asm volatile("" : "+v"(o));  // (or it would be made part of 64-bit sums, or kept)
+        return o;
+    }
+};
 // A channel of a token tensor: its bits, in a register of their own (held as 16 bits, the
 // compiler puts two into one as they arrive, and waits for it: 8% slower), and its value.
 template <class T>
-__device__ __forceinline__ uint32_t load_bits(const void* p, int64_t row, uint32_t lane_bytes) {
-    const T v = *reinterpret_cast<const T*>(static_cast<const char*>(p) + row + lane_bytes);
+__device__ __forceinline__ uint32_t load_bits(const void* p, int64_t head, uint32_t at) {
+    const T v = *reinterpret_cast<const T*>(static_cast<const char*>(p) + head + at);
     if constexpr (sizeof(T) == 2) return v;
     else return __float_as_uint(v);
 }
@@ -215,10 +235,10 @@ __device__ __forceinline__ float value(uint32_t bits) {
     return __uint_as_float(sizeof(T) == 2 ? bits << 16 : bits);
 }
 template <class T>
-__device__ __forceinline__ void store_one(void* p, int64_t row, uint32_t lane_bytes, float f) {
-    T* at = reinterpret_cast<T*>(static_cast<char*>(p) + row + lane_bytes);
-    if constexpr (sizeof(T) == 2) *at = __builtin_bit_cast(uint16_t, (bf16)f);
-    else *at = f;
+__device__ __forceinline__ void store_one(void* p, int64_t head, uint32_t at, float f) {
+    T* to = reinterpret_cast<T*>(static_cast<char*>(p) + head + at);
+    if constexpr (sizeof(T) == 2) *to = __builtin_bit_cast(uint16_t, (bf16)f);
+    else *to = f;
 }
 
 }  // namespace
@@ -381,16 +401,16 @@ __global__ __launch_bounds__(64 * WAVES, 8) void gated_scan_fwd_kernel(ScanArgs 
     const float enter = carry(bp, bs, in);
     float* states = a.states ? a.states + ((int64_t)b * a.n_states + t0 / GS_STATES) * a.C + c : nullptr;
     if (states && t0 < a.T) states[0] = enter;
-    RowWalk row(a, b, t0, row_bytes);
+    const Rows rows(a, b, t0, row_bytes, lane_bytes);
 #pragma unroll
-    for (int t = 0; t < FWD_STEPS; ++t, row.next()) {
+    for (int t = 0; t < FWD_STEPS; ++t) {
         if (t0 + t >= a.T) break;
         const float o = PACKED && after_fresh(t) ? sum[t] : fmaf(prod[t], enter, sum[t]);
         if (PACKED ? m.last >> t & 1 : t0 + t == a.T - 1) {
             if (a.h_final) a.h_final[(PACKED ? sequence(t) : (int64_t)b) * a.C + c] = o;
         }
         if (t == GS_STATES - 1 && states && t0 + GS_STATES < a.T) states[a.C] = o;
-        store_one<T>(a.o, row.at, lane_bytes, o);
+        store_one<T>(a.o, rows.head, rows.at(t), o);
     }
 }
 
@@ -399,8 +419,8 @@ __global__ __launch_bounds__(64 * WAVES, 8) void gated_scan_fwd_kernel(ScanArgs 
 // known, and there is little to do behind enter_tile.  A wave waits between its loads and
 // its stores, so that many of them are needed: two of the factors wait in LDS, and the decays
 // are formed again behind it, for 64 registers and four workgroups on a CU (16384 x 4096
-// bf16: 230 us; 246 with all factors in registers, three workgroups; 267 with the decays,
-// too, two).  Looking far takes 12 KB more of LDS, and leaves three.
+// bf16, before Rows: 230 us; 246 with all factors in registers, three workgroups; 267 with
+// the decays, too, two).  Looking far takes 12 KB more of LDS, and leaves three.
 template <class T, bool PACKED, bool far>
 __global__ __launch_bounds__(GS_THREADS, far ? 6 : 8) void gated_scan_bwd_kernel(ScanArgs a) {
     __shared__ float s_prod[GS_WAVES][64], s_sum[GS_WAVES][64];
@@ -418,15 +438,18 @@ __global__ __launch_bounds__(GS_THREADS, far ? 6 : 8) void gated_scan_bwd_kernel
     const uint32_t row_bytes = a.C * (uint32_t)sizeof(T), lane_bytes = c * (uint32_t)sizeof(T);
     const int t0 = k * BWD_TILE + w * BWD_STEPS;
     uint32_t rx[BWD_STEPS], rg[BWD_STEPS], ri[BWD_STEPS], rd[BWD_STEPS];
-    {
-        RowWalk row(a, b, t0, row_bytes);
+    const Rows rows(a, b, t0, row_bytes, lane_bytes);
+    const auto load = [&](int t, int64_t row, uint32_t at) {
+        rx[t] = load_bits<T>(a.x, row, at);
+        rg[t] = load_bits<T>(a.g, row, at);
+        ri[t] = load_bits<T>(a.gate, row, at);
+        rd[t] = load_bits<T>(a.d_o, row, at);
+    };
+    RowWalk row(a, b, t0, row_bytes);
 #pragma unroll
-        for (int t = 0; t < BWD_STEPS; ++t, row.next()) {
-            rx[t] = load_bits<T>(a.x, row.at, lane_bytes);
-            rg[t] = load_bits<T>(a.g, row.at, lane_bytes);
-            ri[t] = load_bits<T>(a.gate, row.at, lane_bytes);
-            rd[t] = load_bits<T>(a.d_o, row.at, lane_bytes);
-        }
+    for (int t = 0; t < BWD_STEPS; ++t, row.next()) {
+        if constexpr (PACKED) load(t, row.at, lane_bytes);
+        else load(t, rows.head, rows.at(t));
     }
     const float bias = a.dt_bias[c], amount = expf(a.A_log[c]);
     // (tokens behind the last one have none, and need none)
@@ -499,7 +522,6 @@ __global__ __launch_bounds__(GS_THREADS, far ? 6 : 8) void gated_scan_bwd_kernel
     if (w < GS_WAVES - 1) back = carry(bp, bs, in);
     else if (!PACKED && a.dh0 && k == 0 && active) a.dh0[(int64_t)b * a.C + c] = carry(bp, bs, in);
     float dA = 0.f, db = 0.f;
-    const int64_t head = ((int64_t)b * a.T + t0) * row_bytes;
 #pragma unroll
     for (int t = BWD_STEPS - 1; t >= 0; --t) {
         float dx = 0.f, dg = 0.f, di = 0.f;
@@ -518,10 +540,10 @@ __global__ __launch_bounds__(GS_THREADS, far ? 6 : 8) void gated_scan_bwd_kernel
         }
         if (PACKED && a.dh0 && active && m.start >> t & 1) a.dh0[sequence(t) * a.C + c] = back;
         if (active && t0 + t < a.T) {
-            const int64_t row = head + (int64_t)t * row_bytes;
-            store_one<T>(a.dx, row, lane_bytes, dx);
-            store_one<T>(a.dg, row, lane_bytes, dg);
-            store_one<T>(a.dgate, row, lane_bytes, di);
+            const uint32_t at = rows.at(t);
+            store_one<T>(a.dx, rows.head, at, dx);
+            store_one<T>(a.dg, rows.head, at, dg);
+            store_one<T>(a.dgate, rows.head, at, di);
         }
     }
     __syncthreads();
