@@ -933,6 +933,9 @@ def gated_norm_bwd(x, gate, weight, dy, activation="sigmoid", eps=1e-6, residual
 # ------------------------- around a block: recurrence, convolution, layer norm
 # What these calls cost on the host is of the size of their kernels for single tokens, so
 # checks that pass are one expression each, and torch's parts are looked up once.
+_MOST = (1 << 31) - 1
+
+
 class _Torch:
     parts = None
 
@@ -976,6 +979,8 @@ def _tokens(t, name, dims, what):
     shape = t.shape
     if dims and len(shape) != dims:
         raise ValueError(f"{name} must be {what}")
+    if t.numel() > _MOST and max(shape) > _MOST:  # (sizes are passed in 32 bits)
+        raise LibKdaError(1, status_str(1))
     return code, dtype, t.device, shape
 
 
@@ -988,6 +993,8 @@ def _sequences(B, cu_seqlens, dev):
         raise ValueError("cu_seqlens must be 1-D with num_seqs + 1 entries")
     if B != 1:
         raise ValueError("cu_seqlens needs B == 1 (sequences packed along T)")
+    if cu_seqlens.numel() - 1 > _MOST:
+        raise LibKdaError(1, status_str(1))
     return cu_seqlens.numel() - 1
 
 

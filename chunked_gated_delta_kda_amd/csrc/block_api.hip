@@ -16,6 +16,7 @@ constexpr size_t ALIGN = 256;
 constexpr int64_t I31 = (int64_t)1 << 31;
 constexpr int32_t MAX_CHANNELS = 1 << 20;  // 32-bit offsets within a row, and grids over channels
 constexpr int32_t MAX_WIDTH = 16384;       // channels of a row that a workgroup holds
+constexpr int32_t MAX_TOKENS = INT32_MAX - 64;  // of a row of the batch: a tile may reach beyond its end
 
 size_t align_up(size_t x) { return (x + ALIGN - 1) / ALIGN * ALIGN; }
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -27,7 +28,7 @@ bool known_type(int32_t dtype) { return dtype == KDA_BF16 || dtype == KDA_FP32; 
 
 // Sizes of a batch of tokens; a status.
 int check_batch(int32_t dtype, const int32_t* cu, int32_t num_seqs, int32_t B, int32_t T, int32_t C) {
-    if (B < 1 || T < 0 || C < 1 || !known_type(dtype)) return KDA_ERR_INVALID_ARG;
+    if (B < 1 || T < 0 || T > MAX_TOKENS || C < 1 || !known_type(dtype)) return KDA_ERR_INVALID_ARG;
     if (C % 8 || C > MAX_CHANNELS) return KDA_ERR_UNSUPPORTED;
     if ((int64_t)B * T >= I31) return KDA_ERR_INVALID_ARG;
     if (cu && (B != 1 || num_seqs < 1 || !aligned(cu, 4))) return KDA_ERR_INVALID_ARG;
@@ -35,7 +36,7 @@ int check_batch(int32_t dtype, const int32_t* cu, int32_t num_seqs, int32_t B, i
 }
 
 bool valid_batch(int32_t B, int32_t T, int32_t C) {
-    return B >= 1 && T >= 0 && C >= 8 && C % 8 == 0 && C <= MAX_CHANNELS && (int64_t)B * T < I31;
+    return B >= 1 && T >= 0 && T <= MAX_TOKENS && C >= 8 && C % 8 == 0 && C <= MAX_CHANNELS && (int64_t)B * T < I31;
 }
 
 int32_t scan_states(int32_t T) { return (int32_t)(((int64_t)T + kda::GS_STATES - 1) / kda::GS_STATES); }

@@ -526,8 +526,9 @@ int gated_norm_bwd(const uint16_t* x, const uint16_t* gate, const float* weight,
  *    parameters, their gradients and the recurrence's states are fp32, the
  *    convolution's states (they hold tokens) of the tokens' type.
  *  - C (and D) are multiples of 8, C at most 2^20 and D at most 16384, else
- *    KDA_ERR_UNSUPPORTED.  Alignment: token tensors and states 16 bytes,
- *    parameters and their gradients 4, workspaces 256.
+ *    KDA_ERR_UNSUPPORTED.  B T < 2^31, T at most 2^31 - 65.
+ *  - Alignment: token tensors and states 16 bytes, parameters and their
+ *    gradients 4, workspaces 256.
  *  - cu_seqlens as for kda_fwd (B = 1); every row of an output is written: rows
  *    outside every sequence get zeros, whatever the inputs hold there.
  *    num_seqs is read only with cu_seqlens.

@@ -24,7 +24,7 @@ def call(fn, base, over):
 
 SIZES = [
     (dict(B=0), 1), (dict(T=-1), 1), (dict(C=0), 1), (dict(C=12), 2), (dict(C=(1 << 20) + 8), 2), (dict(dtype=2), 1),
-    (dict(dtype=-1), 1), (dict(B=1 << 16, T=1 << 15), 1), (dict(cu=FAKE, B=2, N=2), 1), (dict(cu=FAKE, N=0), 1),
+    (dict(dtype=-1), 1), (dict(B=1 << 16, T=1 << 15), 1), (dict(T=(1 << 31) - 64, C=8), 1), (dict(cu=FAKE, B=2, N=2), 1), (dict(cu=FAKE, N=0), 1),
     (dict(cu=odd(2)), 1), (dict(x=None), 1), (dict(x=odd(8)), 1), (dict(h0=odd(8)), 1)]
 
 SCAN = dict(x=FAKE, g=FAKE, gate=FAKE, A=FAKE, b=FAKE, h0=None, hT=None, cu=None, N=1, dtype=0, B=1, T=300, C=64, o=FAKE,
@@ -130,7 +130,8 @@ def test_no_rows_is_no_call(lib):
 def test_sizes(lib):
     assert lib.gated_scan_states(2, 129, 64) == 2 * 17 * 64
     assert lib.gated_scan_states(1, 0, 64) == 0
-    for bad in ((0, 1, 64), (1, -1, 64), (1, 1, 12), (1, 1, (1 << 20) + 8), (1 << 16, 1 << 15, 64)):
+    assert lib.gated_scan_states(1, (1 << 31) - 65, 8) == ((1 << 31) - 64) // 8 * 8
+    for bad in ((0, 1, 64), (1, -1, 64), (1, (1 << 31) - 64, 8), (1, 1, 12), (1, 1, (1 << 20) + 8), (1 << 16, 1 << 15, 64)):
         assert lib.gated_scan_states(*bad) == -1
         assert kda.gated_scan_workspace_size(*bad) == kda.gated_scan_workspace_size(*bad, backward=True) == 0
         assert lib.short_conv_bwd_workspace_size(0, *bad, 4) == 0

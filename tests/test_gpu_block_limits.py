@@ -163,3 +163,12 @@ def test_rows_of_2_to_the_20_channels():
             assert torch.equal(r[k][..., cut], r1[k]), k
         assert torch.equal(y[..., cut], kda.short_conv_fwd(p, w)[0])
         assert torch.equal(g["dx"][..., cut], kda.short_conv_bwd(p, w, p)["dx"])
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    x = torch.empty(1, (1 << 32) + 5, 8, dtype=torch.bfloat16, device=DEV)  # (5 tokens in 32 bits)
+    p = torch.zeros(8, device=DEV)
+    for call in (lambda: kda.gated_scan_fwd(x, x, x, p, p), lambda: kda.short_conv_fwd(x, torch.zeros(8, 4, device=DEV)),
+                 lambda: kda.gated_scan_decode(x[0], x[0], x[0], p, p), lambda: kda.layer_norm_fwd(x, p)):
+        with pytest.raises(kda.LibKdaError):
+            call()
