@@ -172,3 +172,24 @@ def test_sizes_beyond_32_bits_are_refused():
                  lambda: kda.gated_scan_decode(x[0], x[0], x[0], p, p), lambda: kda.layer_norm_fwd(x, p)):
         with pytest.raises(kda.LibKdaError):
             call()
+
+
+def test_the_longest_row():
+    """2^31 - 65 tokens: its end is that of the last tokens alone, behind the state (or the
+    tokens) in front of them."""
+    T, C, n = (1 << 31) - 65, 8, 300
+    x = normal(26, 1, T, C)
+    A, bias = normal(27, C, dtype=torch.float32), normal(28, C, dtype=torch.float32)
+    taps = normal(29, C, 4, dtype=torch.float32)
+    say(f"[conv] {T} tokens")
+    y, f = kda.short_conv_fwd(x, taps)
+    end = x[:, T - n:].contiguous()
+    yw, fw = kda.short_conv_fwd(end, taps, initial_state=x[:, T - n - 3:T - n].contiguous())
+    assert torch.equal(y[:, T - n:], yw) and torch.equal(f, fw)
+    del y
+    say(f"[scan] {T} tokens")
+    o, f = kda.gated_scan_fwd(x, x, x, A, bias)
+    ow, fw = kda.gated_scan_fwd(end, end, end, A, bias, initial_state=o[:, T - n - 1].float().contiguous())
+    # the state in front comes rounded to bf16, and decays; outputs are rounded, too
+    assert ((o[:, T - n:].float() - ow.float()).abs() <= 2.0 ** -7 * (ow.float().abs() + fw.abs().max() + 1)).all()
+    assert torch.isfinite(f).all() and (f - fw).abs().max() <= 2.0 ** -7 * (fw.abs().max() + 1)
