@@ -83,16 +83,28 @@ struct InputGate {
     }
 };
 
-// (product, sum) applied to a state: behind a product of zero nothing of the state is
-// left, not even an infinity or a NaN of another sequence
-__device__ __forceinline__ float carry(float prod, float sum, float h) { return prod == 0.f ? sum : fmaf(prod, h, sum); }
-__device__ __forceinline__ float join(float prod, float before) { return prod == 0.f ? 0.f : prod * before; }
+// The product of what is cut off from the state before it, by a sequence's beginning: minus
+// zero, which stays itself under products of decays.  (Decays that underflow leave plus zero,
+// and a NaN or an infinity of their own sequence goes on.)
+constexpr float CUT = -0.f;
+__device__ __forceinline__ bool is_cut(float prod) { return __float_as_uint(prod) == 0x80000000u; }
+
+// (product, sum) applied to a state: behind a cut nothing of the state is left, not even an
+// infinity or a NaN of another sequence.  (cuts: whether the product may be one.)
+template <bool cuts = true>
+__device__ __forceinline__ float carry(float prod, float sum, float h) {
+    return cuts && is_cut(prod) ? sum : fmaf(prod, h, sum);
+}
+template <bool cuts = true>
+__device__ __forceinline__ float join(float prod, float before) {
+    return cuts && is_cut(prod) ? CUT : prod * before;
+}
 
 __host__ __device__ __forceinline__ int tiles_of(int T, int tile) { return (int)(((int64_t)T + tile - 1) / tile); }
 __device__ __forceinline__ int clamp_to(int v, int T) { return min(max(v, 0), T); }
 
 // What a tile makes of the state that enters it, as one 64-bit word that the tiles behind
-// it read while it runs: (product, sum), or (0, state left behind) once that is known.
+// it read while it runs: (product, sum), or (CUT, state left behind) once that is known.
 // One atomic word needs no order of stores; EMPTY is a product that no tile has.
 constexpr uint64_t EMPTY = ~0ull;
 
@@ -119,12 +131,12 @@ __device__ __forceinline__ void await_words(const uint64_t* own, int64_t step, i
         bool ready = true;
 #pragma unroll
         for (int i = 0; i < n; ++i)
-            ready = ready && (back + i * GS_WAVES == state ? word_prod(word[i]) == 0.f
+            ready = ready && (back + i * GS_WAVES == state ? is_cut(word_prod(word[i]))
                                                           : (uint32_t)word[i] != (uint32_t)EMPTY);
         if (__all(ready)) break;
         if (looks == 1 << 20) {
 #pragma unroll
-            for (int i = 0; i < n; ++i) word[i] = 0x7fc00000ull << 32;
+            for (int i = 0; i < n; ++i) word[i] = 0x7fc00000ull << 32 | 0x80000000u;  // (NaN, cut off)
             break;
         }
         __builtin_amdgcn_s_sleep(1);
@@ -159,7 +171,7 @@ __device__ __forceinline__ float enter_tile(const ScanArgs& a, int tiles, int or
         if (far && order > NEAR) {
             bool state = false;
 #pragma unroll
-            for (int j = 0; j < NEAR; ++j) state = state || word_prod(look[j][lane]) == 0.f;
+            for (int j = 0; j < NEAR; ++j) state = state || is_cut(word_prod(look[j][lane]));
             if (!__all(state)) {  // (the same words in every wave)
                 await_words<FAR / NEAR - 1>(own, step, order, w + NEAR, FAR - 1, lane, look);
                 __syncthreads();
@@ -172,7 +184,7 @@ __device__ __forceinline__ float enter_tile(const ScanArgs& a, int tiles, int or
             in = carry(word_prod(t), word_sum(t), in);
         }
     }
-    if (poster && order + 1 < tiles) post(own, 0.f, carry(prod, sum, in));
+    if (poster && order + 1 < tiles) post(own, CUT, carry(prod, sum, in));
     return in;
 }
 
@@ -371,7 +383,7 @@ __global__ __launch_bounds__(64 * WAVES, 8) void gated_scan_fwd_kernel(ScanArgs 
         const Decay d(value<T>(rg[t]) + bias, amount);
         const float in = __builtin_amdgcn_sqrtf(d.one_minus_square()) * sigmoid(value<T>(ri[t])) * value<T>(rx[t]);
         if (PACKED && fresh >> t & 1) {
-            p = 0.f;
+            p = CUT;
             h = m.start >> t & 1 ? fmaf(d.a, state_of(a.h0, t), in) : 0.f;
         } else {
             p *= d.a;
@@ -382,15 +394,15 @@ __global__ __launch_bounds__(64 * WAVES, 8) void gated_scan_fwd_kernel(ScanArgs 
     }
     // behind a fresh token nothing of the state before it is left, whatever it and the
     // decays are
-    if (PACKED && after_fresh(FWD_STEPS - 1)) p = 0.f;
+    if (PACKED && after_fresh(FWD_STEPS - 1)) p = CUT;
     s_prod[w][lane] = p;
     s_sum[w][lane] = h;
     __syncthreads();
     // what the waves before this one make of the tile's state; the last wave's is the tile's
     float bp = 1.f, bs = 0.f;
     for (int j = 0; j < w; ++j) {
-        bs = carry(s_prod[j][lane], s_sum[j][lane], bs);
-        bp = join(s_prod[j][lane], bp);
+        bs = carry<PACKED>(s_prod[j][lane], s_sum[j][lane], bs);
+        bp = join<PACKED>(s_prod[j][lane], bp);
     }
     const float first = k == 0 && !PACKED && a.h0 ? a.h0[(int64_t)b * a.C + c] : 0.f;
     float in = first;
@@ -398,7 +410,7 @@ __global__ __launch_bounds__(64 * WAVES, 8) void gated_scan_fwd_kernel(ScanArgs 
             in = enter_tile<far>(a, tiles, k, (int64_t)b * a.C + c, active, w, lane, join(p, bp), carry(p, h, bs), first, look);
     }
     if (!active) return;
-    const float enter = carry(bp, bs, in);
+    const float enter = carry<PACKED>(bp, bs, in);
     float* states = a.states ? a.states + ((int64_t)b * a.n_states + t0 / GS_STATES) * a.C + c : nullptr;
     if (states && t0 < a.T) states[0] = enter;
     const Rows rows(a, b, t0, row_bytes, lane_bytes);
@@ -497,14 +509,14 @@ __global__ __launch_bounds__(GS_THREADS, far ? 6 : 8) void gated_scan_bwd_kernel
 #pragma unroll
     for (int t = BWD_STEPS - 1; t >= 0; --t) {
         if (PACKED && ended >> t & 1) {
-            q = 0.f;
+            q = CUT;
             e = m.last >> t & 1 ? dec[t] * (value<T>(rd[t]) + state_of(a.d_final, t)) : 0.f;
         } else {
             q *= dec[t];
             e = dec[t] * (value<T>(rd[t]) + e);
         }
     }
-    if (PACKED && (ended & ((1u << BWD_STEPS) - 1))) q = 0.f;
+    if (PACKED && (ended & ((1u << BWD_STEPS) - 1))) q = CUT;
     s_prod[w][lane] = q;
     s_sum[w][lane] = e;
     __syncthreads();
@@ -513,14 +525,14 @@ __global__ __launch_bounds__(GS_THREADS, far ? 6 : 8) void gated_scan_bwd_kernel
     float bp = 1.f, bs = 0.f;
     const int until = w == GS_WAVES - 1 ? 0 : w + 1;
     for (int j = GS_WAVES - 1; j >= until; --j) {
-        bs = carry(s_prod[j][lane], s_sum[j][lane], bs);
-        bp = join(s_prod[j][lane], bp);
+        bs = carry<PACKED>(s_prod[j][lane], s_sum[j][lane], bs);
+        bp = join<PACKED>(s_prod[j][lane], bp);
     }
     const float first = order == 0 && !PACKED && a.d_final ? a.d_final[(int64_t)b * a.C + c] : 0.f;
     const float in = enter_tile<far>(a, tiles, order, (int64_t)b * a.C + c, active, w, lane, bp, bs, first, look);
     float back = in;
-    if (w < GS_WAVES - 1) back = carry(bp, bs, in);
-    else if (!PACKED && a.dh0 && k == 0 && active) a.dh0[(int64_t)b * a.C + c] = carry(bp, bs, in);
+    if (w < GS_WAVES - 1) back = carry<PACKED>(bp, bs, in);
+    else if (!PACKED && a.dh0 && k == 0 && active) a.dh0[(int64_t)b * a.C + c] = carry<PACKED>(bp, bs, in);
     float dA = 0.f, db = 0.f;
 #pragma unroll
     for (int t = BWD_STEPS - 1; t >= 0; --t) {

@@ -534,9 +534,10 @@ int gated_norm_bwd(const uint16_t* x, const uint16_t* gate, const float* weight,
  *    num_seqs is read only with cu_seqlens.
  *  - Arithmetic is fp32, each output is rounded once; sums over tokens or rows
  *    have a fixed order: equal calls give equal bits.
- *  - A NaN or an infinity stays in its channel and sequence (convolution: in the
- *    W tokens that see it; layer norm: in its row), and in the parameters'
- *    gradients of its channel (layer norm: of all channels, for dweight). */
+ *  - A NaN or an infinity does not leave its channel and sequence (recurrence: a
+ *    NaN goes on to the end, however fast the decays; convolution: the W tokens
+ *    that see it; layer norm: its row), but for the parameters' gradients of its
+ *    channel (layer norm: of all channels, for dweight). */
 enum kda_dtype { KDA_BF16 = 0, KDA_FP32 = 1 };
 
 /* Gated linear recurrence: per channel c, with KDA's decay gate,

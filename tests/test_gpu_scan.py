@@ -184,6 +184,30 @@ def test_nan_stays_in_its_channel_and_sequence():
     assert torch.equal(f[2], f2[2])
 
 
+@pytest.mark.parametrize("C", [72, 712])  # (few chains and many)
+@pytest.mark.parametrize("packed", [False, True])
+def test_nan_reaches_its_sequences_end_however_fast_it_forgets(packed, C):
+    """Decays whose products underflow within a tile, or that are zero: a NaN goes on all the
+    same, forward in the state and backward in its gradient."""
+    cu = offsets([40, 900, 70]) if packed else None
+    w = make(1, 1010, C, seed=23, cu=cu)
+    w["dt_bias"][:4] = 5.0
+    w["A_log"][:2] = 0.0
+    w["A_log"][2:4] = 5.0  # (exp(-148 L): zero)
+    clean = run(w)[0]
+    w["x"][0, 50, :4] = float("nan")
+    w["do"][0, 930, 8] = float("nan")
+    w["dt_bias"][8] = 40.0
+    o, f, r = run(w)
+    end = 940 if packed else 1010
+    assert o[0, 50:end, :4].isnan().all() and not o[0, :50, :4].isnan().any()
+    assert f[1 if packed else 0, :4].isnan().all()
+    first = 40 if packed else 0
+    assert r["dx"][0, first:931, 8].isnan().all() and not r["dx"][0, 931:, 8].isnan().any()
+    assert not r["dx"][0, :first, 8].isnan().any() and not o[0, end:].isnan().any()
+    assert torch.equal(o[..., 16:], clean[..., 16:])
+
+
 @pytest.mark.parametrize("packed", [False, True])
 def test_no_tokens(packed):
     cu = torch.zeros(4, dtype=torch.int32) if packed else None
