@@ -276,10 +276,15 @@ class _GatedScan:
             class GatedScanFunction(torch.autograd.Function):
                 @staticmethod
                 def forward(ctx, x, g, input_gate, A_log, dt_bias, initial_state, cu_seqlens,
-                            output_final_state):
-                    o, final, states = _b.gated_scan_fwd_save(
-                        x, g, input_gate, A_log, dt_bias, initial_state, output_final_state,
-                        cu_seqlens)
+                            output_final_state, recording):
+                    args = (x, g, input_gate, A_log, dt_bias, initial_state, output_final_state,
+                            cu_seqlens)
+                    states = None
+                    if recording and any(ctx.needs_input_grad):
+                        # keep what the backward pass needs
+                        o, final, states = _b.gated_scan_fwd_save(*args)
+                    else:
+                        o, final = _b.gated_scan_fwd(*args)
                     ctx.save_for_backward(x, g, input_gate, A_log, dt_bias, states, initial_state,
                                           cu_seqlens)
                     ctx.set_materialize_grads(False)
@@ -296,7 +301,7 @@ class _GatedScan:
                                           h0, None if dfinal is None else dfinal.contiguous(), cu,
                                           need_dh0=h0 is not None and ctx.needs_input_grad[5])
                     return (r["dx"], r["dg"], r["dinput_gate"], r["dA_log"], r["ddt_bias"],
-                            r["dh0"], None, None)
+                            r["dh0"], None, None, None)
 
             cls.fn = GatedScanFunction
         return cls.fn
@@ -376,11 +381,11 @@ def gated_scan(x, g, input_gate, A_log, dt_bias, initial_state=None, output_fina
     (o, final_state); final_state is None unless ``output_final_state``.  Gradients reach x,
     g, input_gate, A_log, dt_bias and initial_state; where none is asked for, the states
     that they need are not kept."""
-    leaves = (x, g, input_gate, A_log, dt_bias, initial_state)
-    if not (_torch().is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in leaves)):
-        return _b.gated_scan_fwd(*leaves, output_final_state, cu_seqlens)
+    # (always through the function: it refuses what it has no rule for, a forward-mode tangent
+    # or a batched tensor, where the plain call would drop it; inside of it gradients are off,
+    # so whether they are recorded is asked here)
     out = _GatedScan.get().apply(x, g, input_gate, A_log, dt_bias, initial_state, cu_seqlens,
-                                 bool(output_final_state))
+                                 bool(output_final_state), _torch().is_grad_enabled())
     return out if output_final_state else (out, None)
 
 
