@@ -26,6 +26,8 @@
 // those of 16384 x 4096 210 us, 4.6 TB/s.
 // What bounds the long call is the memory: a kernel that only moves such rows reaches
 // 4.7 TB/s (of 256 bytes: 5.1).  The gradients lose 13 us to three launches.
+#include <cfloat>
+
 #include "block_device.h"
 
 namespace kda {
@@ -463,7 +465,10 @@ __global__ __launch_bounds__(GS_THREADS, far ? 6 : 8) void gated_scan_bwd_kernel
         if constexpr (PACKED) load(t, row.at, lane_bytes);
         else load(t, rows.head, rows.at(t));
     }
-    const float bias = a.dt_bias[c], amount = expf(a.A_log[c]);
+    // (A bias of +infinity by a number: beside a gate of -infinity, below, it would be a NaN.
+    // g + FLT_MAX forgets everything, too, but for a g of -FLT_MAX itself.)
+    const float dt_bias = a.dt_bias[c], bias = dt_bias > FLT_MAX ? FLT_MAX : dt_bias;
+    const float amount = expf(a.A_log[c]);
     // (tokens behind the last one have none, and need none)
     float h = a.states[((int64_t)b * a.n_states + min(t0 / GS_STATES, a.n_states - 1)) * a.C + c];
     Marks m;
@@ -547,8 +552,11 @@ __global__ __launch_bounds__(GS_THREADS, far ? 6 : 8) void gated_scan_bwd_kernel
             dx = et * f.x;
             di = et * f.y;
             dg = pt * fg[t];
-            dA = fmaf(pt, L[t], dA);
-            db += dg;
+            // (a row behind the last token counts for nothing, however large what passes it)
+            if (PACKED || t0 + t < a.T) {
+                dA = fmaf(pt, L[t], dA);
+                db += dg;
+            }
         }
         if (PACKED && a.dh0 && active && m.start >> t & 1) a.dh0[sequence(t) * a.C + c] = back;
         if (active && t0 + t < a.T) {
