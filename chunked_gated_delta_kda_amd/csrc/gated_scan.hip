@@ -552,9 +552,10 @@ __global__ __launch_bounds__(GS_THREADS, far ? 6 : 8) void gated_scan_bwd_kernel
             dx = et * f.x;
             di = et * f.y;
             dg = pt * fg[t];
-            // (a row behind the last token counts for nothing, however large what passes it)
+            // (A row behind the last token counts for nothing, however large what passes it.  An
+            // L of infinity is a decay of zero: its part is zero, not 0 * inf.)
             if (PACKED || t0 + t < a.T) {
-                dA = fmaf(pt, L[t], dA);
+                dA = fmaf(pt, __builtin_amdgcn_fmed3f(L[t], 0.f, FLT_MAX), dA);
                 db += dg;
             }
         }

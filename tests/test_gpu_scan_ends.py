@@ -47,3 +47,46 @@ def test_a_large_gradient_of_the_last_state_meets_a_large_state(T):
     want = ref.scan_all(*args(w), w["h0"], None, w["do"], w["dfinal"])
     for got, name in GRADS:
         near(got, r[got], want[name])
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("C", [24, 712])  # (few chains and many)
+def test_tokens_that_reset_the_state(C, dtype, packed):
+    """A gate of the type's largest value or of +inf, or the product of a large one and a
+    large exp(A_log): L is infinite in fp32, the decay zero, and the token adds nothing to
+    any gradient through its gate.  In 64 bits that is so from L = 1e6 on."""
+    cu = torch.tensor([0, 40, 40, 131], dtype=torch.int32) if packed else None
+    w = make(1, 139, C, seed=107, dtype=dtype, cu=cu)
+    big = torch.finfo(w["g"].dtype).max
+    w["A_log"][2], w["dt_bias"][2] = 3.0, -6.0
+    resets = ((5, 1, big), (63, 1, INF), (64, 3, INF), (39, 4, big), (40, 4, INF), (130, 5, big), (20, 2, big / 4))
+    for t, c, v in resets:
+        w["g"][0, t, c] = v
+    o, f, r = run(w)
+    for t, c, _ in resets:
+        w["g"][0, t, c] = 1e6
+    want = ref.scan_all(*args(w), w["h0"], w["cu"], w["do"], w["dfinal"])
+    near("o", o, want["o"])
+    near("final", f, want["final"])
+    for got, name in GRADS:
+        near(got, r[got], want[name])
+    for t, c, _ in resets:
+        assert r["dg"][0, t, c] == 0
+
+
+@pytest.mark.parametrize("T", [64, 70])
+def test_a_channel_that_forgets_everything_has_no_gradient_of_its_decay(T):
+    w = make(2, T, 24, seed=109)
+    w["A_log"][5] = 0.0
+    w["dt_bias"][5] = INF
+    _, _, r = run(w)
+    assert r["dA_log"][5] == 0 and r["ddt_bias"][5] == 0 and torch.isfinite(r["dA_log"]).all()
+
+
+def test_a_nan_in_a_gate_still_reaches_its_channels_gradients():
+    w = make(1, 70, 24, seed=113)
+    w["g"][0, 30, 3] = float("nan")
+    _, _, r = run(w)
+    for n in ("dA_log", "ddt_bias"):
+        assert r[n][3].isnan() and torch.isfinite(r[n][:3]).all() and torch.isfinite(r[n][4:]).all()
