@@ -12,8 +12,9 @@
 // from the mean, and what the mean's own rounding leaves in them is taken out
 // (c = mean(u - mean)), so a row far from zero keeps its digits.  All arithmetic
 // is fp32; each output is rounded once.  The backward kernel's workgroups walk
-// over the rows and keep their lanes' channels of dweight and dbias in registers;
-// a second kernel adds the workgroups' sums in a fixed order, in 64 bits.
+// over the rows and keep their lanes' channels of dweight and dbias in registers, 64
+// rows at a time in fp32 (LN_CHAIN) and more of them in 64 bits in LDS; a second kernel
+// adds the workgroups' sums in a fixed order, in 64 bits.
 // Measured (16384 x 4096 bf16): forward with a residual 102 us, 5.3 TB/s, gradients 114 us,
 // 4.7 TB/s; 3001 x 1000 fp32 forward 7.3 us, gradients 13.1 and their sum 3.9 (its 24 MB
 // are in flight for too short a time: six rows a workgroup, one after the other).
@@ -230,13 +231,24 @@ __global__ __launch_bounds__(L > LN_THREADS ? L : LN_THREADS) void layer_norm_fw
     }
 }
 
+// Rows that a lane adds in fp32, one after the other: 64 roundings of a sum and those of
+// the rows side by side (32) and of what is left in part stay below 2^-17 of the terms'
+// sizes.  More rows go on in 64 bits, in LDS (LONG), where a workgroup's sums fit there
+// (131072 x 4096 bf16 with the forward pass: 1609 us, 1607 in fp32 alone).  Wider rows have
+// more workgroups instead, which leave more of part to write and to add (65536 x 16384 bf16:
+// 3402 us, 3360).
+constexpr int LN_CHAIN = 64;
+constexpr bool long_in_lds(int values, int threads) { return values * threads <= 8192; }  // (128 KB)
+
 // (In workgroups of 1024 threads the next row's loads do not fit beside the sums.)
-template <class T, int L, int K>
+template <class T, int L, int K, bool LONG>
 __global__ __launch_bounds__(L > LN_THREADS ? L : LN_THREADS) void layer_norm_bwd_kernel(LayerNormArgs a) {
     constexpr int V = Slice<T>::N, THREADS = L > LN_THREADS ? L : LN_THREADS, RPW = THREADS / L;
     constexpr bool KEEP = K * V <= 16 && THREADS < 1024, AHEAD = THREADS < 1024;
     __shared__ float red_t[2][16];
+    __shared__ double before[2][LONG ? K * V : 1][LONG ? THREADS : 1];  // (a thread's own)
     const int l = threadIdx.x % L;
+    int left = LN_CHAIN;
     float dw[K * V], db[K * V];
     Weights<K, V, KEEP> wt(a.weight);
     int count = 0;
@@ -246,7 +258,10 @@ __global__ __launch_bounds__(L > LN_THREADS ? L : LN_THREADS) void layer_norm_bw
         if (c < a.D) count = (k + 1) * V;
         wt.keep(k, c, c < a.D);
 #pragma unroll
-        for (int v = 0; v < V; ++v) dw[k * V + v] = db[k * V + v] = 0.f;
+        for (int v = 0; v < V; ++v) {
+            dw[k * V + v] = db[k * V + v] = 0.f;
+            if constexpr (LONG) before[0][k * V + v][threadIdx.x] = before[1][k * V + v][threadIdx.x] = 0.0;
+        }
     }
     const float inv = 1.f / (float)a.D;
     const int64_t step = (int64_t)a.groups * RPW;
@@ -331,6 +346,24 @@ __global__ __launch_bounds__(L > LN_THREADS ? L : LN_THREADS) void layer_norm_bw
                 Slice<T>::store(a.dx, at + c, dx);
             }
         }
+        if constexpr (LONG) {
+            if (--left == 0) {
+                left = LN_CHAIN;
+#pragma unroll
+                for (int i = 0; i < K * V; ++i) {
+                    before[0][i][threadIdx.x] += dw[i];
+                    before[1][i][threadIdx.x] += db[i];
+                    dw[i] = db[i] = 0.f;
+                }
+            }
+        }
+    }
+    if constexpr (LONG) {
+#pragma unroll
+        for (int i = 0; i < K * V; ++i) {
+            dw[i] = (float)(before[0][i][threadIdx.x] + dw[i]);
+            db[i] = (float)(before[1][i][threadIdx.x] + db[i]);
+        }
     }
     // the workgroup's sums: rows side by side are added through LDS
     if constexpr (RPW == 1) {
@@ -410,22 +443,24 @@ constexpr int threads_of(int L) { return L > LN_THREADS ? L : LN_THREADS; }
 // 167 with 4 and 137 with 16, which leave twice the sums to add.)
 constexpr int LN_FWD_WAVES = 16, LN_BWD_WAVES = 8;
 
-int32_t groups_of(int64_t rows, int32_t D, bool fp32, int waves) {
+int32_t groups_of(int64_t rows, int32_t D, bool fp32, int waves, bool backward) {
     int64_t g = 1;
-    by_type_and_row(fp32, D, [&](auto, auto l, auto) {
+    by_type_and_row(fp32, D, [&](auto t, auto l, auto k) {
         constexpr int L = decltype(l)::value, per = threads_of(L) / L;
         g = std::min<int64_t>((rows + per - 1) / per, std::max(1, waves * 64 / threads_of(L)) * 256);
+        if (backward && !long_in_lds(decltype(k)::value * Slice<decltype(t)>::N, threads_of(L)))
+            g = std::max(g, (rows + LN_CHAIN * per - 1) / (LN_CHAIN * per));
     });
     return (int32_t)std::max<int64_t>(g, 1);
 }
 
 }  // namespace
 
-int32_t layer_norm_groups(int64_t rows, int32_t D, bool fp32) { return groups_of(rows, D, fp32, LN_BWD_WAVES); }
+int32_t layer_norm_groups(int64_t rows, int32_t D, bool fp32) { return groups_of(rows, D, fp32, LN_BWD_WAVES, true); }
 
 void launch_layer_norm_fwd(const LayerNormArgs& args, bool fp32, hipStream_t stream) {
     LayerNormArgs a = args;
-    a.groups = groups_of(a.rows, a.D, fp32, LN_FWD_WAVES);
+    a.groups = groups_of(a.rows, a.D, fp32, LN_FWD_WAVES, false);
     by_type_and_row(fp32, a.D, [&](auto t, auto l, auto k) {
         constexpr int L = decltype(l)::value;
         hipLaunchKernelGGL((layer_norm_fwd_kernel<decltype(t), L, decltype(k)::value>), dim3((unsigned)a.groups),
@@ -435,9 +470,15 @@ void launch_layer_norm_fwd(const LayerNormArgs& args, bool fp32, hipStream_t str
 
 void launch_layer_norm_bwd(const LayerNormArgs& a, bool fp32, hipStream_t stream) {
     by_type_and_row(fp32, a.D, [&](auto t, auto l, auto k) {
-        constexpr int L = decltype(l)::value;
-        hipLaunchKernelGGL((layer_norm_bwd_kernel<decltype(t), L, decltype(k)::value>), dim3((unsigned)a.groups),
-                           dim3(threads_of(L)), 0, stream, a);
+        constexpr int L = decltype(l)::value, K = decltype(k)::value, threads = threads_of(L);
+        const dim3 grid((unsigned)a.groups);
+        if constexpr (long_in_lds(K * Slice<decltype(t)>::N, threads)) {
+            if (a.rows > (int64_t)a.groups * (threads / L) * LN_CHAIN) {
+                hipLaunchKernelGGL((layer_norm_bwd_kernel<decltype(t), L, K, true>), grid, dim3(threads), 0, stream, a);
+                return;
+            }
+        }
+        hipLaunchKernelGGL((layer_norm_bwd_kernel<decltype(t), L, K, false>), grid, dim3(threads), 0, stream, a);
     });
     hipLaunchKernelGGL(layer_norm_sum_kernel, dim3((unsigned)((a.D + 31) / 32 * 2)), dim3(256), 0, stream, a);
 }
