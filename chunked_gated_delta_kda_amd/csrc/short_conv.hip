@@ -34,8 +34,8 @@ __device__ __forceinline__ int clamp_tok(int v, int T) { return min(max(v, 0), T
 // The sequence that a strip's token belongs to: tokens [s, e) of its row of the batch.
 struct Seq {
     int n, s, e;
-    // the last sequence that begins at or before t (-1: none does), 64 candidates at a time:
-    // all lanes of the wave have to be there
+    // The last sequence that begins at or before t (-1: none does), 64 candidates at a time:
+    // all lanes of the wave have to be there.
     __device__ __forceinline__ void find(const ConvArgs& a, int b, int t) {
         if (!a.cu) {
             n = b;
@@ -43,10 +43,14 @@ struct Seq {
             e = a.T;
             return;
         }
+        search(a, t, 6);
+    }
+    // (2^w candidates: as many of the wave's lanes, from the first, are there; w > 0)
+    __device__ __forceinline__ void search(const ConvArgs& a, int t, int w) {
         const int lane = threadIdx.x & 63;
         uint32_t lo = 0, count = a.N, step;  // (N + 63 may pass 31 bits)
         do {
-            step = (count + 63) / 64;
+            step = (count + (1u << w) - 1) >> w;
             const uint32_t i = lane * step;
             const int before =
                 __popcll(__ballot(i < count && clamp_tok(a.cu[min(lo + i, (uint32_t)a.N)], a.T) <= t));
@@ -61,10 +65,15 @@ struct Seq {
         s = i < 0 ? -1 : i < a.N ? clamp_tok(a.cu[i], a.T) : a.T;
         e = i < 0 ? -1 : i < a.N ? max(clamp_tok(a.cu[i + 1], a.T), s) : a.T;
     }
-    // the sequence that begins at or behind e
+    // The next sequence that has a token, t or one behind it.  Where the one behind this has
+    // none it is searched for: offsets that repeat by the thousand (a batch padded to a fixed
+    // number of sequences) are passed in a few steps, not one by one.
     __device__ __forceinline__ void next(const ConvArgs& a, int t) {
-        if (!a.cu) return;
-        while (n < a.N && e <= t) set(a, n + 1);
+        if (!a.cu || n >= a.N) return;
+        set(a, n + 1);
+        if (n >= a.N || e > t) return;
+        search(a, t, 31 - __builtin_clz(__popcll(__ballot(true))));  // (channels come in eights)
+        if (e <= t) set(a, n + 1);
     }
 };
 
@@ -166,7 +175,6 @@ __global__ __launch_bounds__(SC_THREADS) void short_conv_fwd_kernel(ConvArgs a) 
 #pragma unroll
         for (int i = 0; i < SC_BATCH; ++i) rx[i] = next[i];
         if (tb + SC_BATCH < t1) fetch<S>(a.x, row0, tb + SC_BATCH, t1, a.C, c, next);
-        if (tb >= q.e) q.next(a, tb);
         if (tb > q.s && tb + SC_BATCH < q.e && tb + SC_BATCH <= t1) {
             float x[SC_BATCH + W - 1][V];
 #pragma unroll
@@ -289,7 +297,6 @@ __global__ __launch_bounds__(SC_THREADS, 4) void short_conv_bwd_kernel(ConvArgs 
                 fetch<S>(a.x, row0, tb + SC_BATCH, end, a.C, c, next_x);
                 fetch<S>(a.dy, row0, tb + SC_BATCH, end, a.C, c, next_y);
             }
-            if (tb >= q.e) q.next(a, tb);
             // (a batch behind the strip may have tokens from `end` on: their part is of
             // places that are not this strip's)
             if (tb >= q.s + W && tb + SC_BATCH < q.e && (tb >= t1 || tb + SC_BATCH <= t1)) {
