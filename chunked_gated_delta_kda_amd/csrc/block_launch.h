@@ -18,6 +18,11 @@ constexpr int GS_STATES = 8;
 constexpr int GS_ONE_TILE = 256;  // most tokens of a row that the forward pass has as one tile
 constexpr int GS_TICKET_BYTES = 64;  // counters do not share a line
 
+// Whether a chain of so many tiles has one of this number, which is a counter's: compared
+// without a sign, since a counter that something else wrote to may hold anything, and a
+// negative tile would be read and written in front of every array.
+__host__ __device__ constexpr bool is_tile(uint32_t number, int32_t tiles) { return number < (uint32_t)tiles; }
+
 struct ScanArgs {
     const void* x;          // [B, T, C] tokens
     const void* g;          // [B, T, C] tokens

@@ -119,8 +119,9 @@ __device__ __forceinline__ float word_sum(uint64_t w) { return __uint_as_float((
 
 // Waits until the tiles back, back + GS_WAVES, ... (n of them) before the one that posts at
 // `own` have posted, and tile `state` before it even knows the state behind it.  The number
-// of looks is bounded all the same: a workspace that someone else writes to gives NaN, not
-// a hang.
+// of looks is bounded all the same: words or counters that something else writes to while
+// the kernel runs give NaN or outputs that are not written, not a hang.  (A packed batch's
+// marks and sequences, in the same workspace, are indexes, and are trusted.)
 template <int n>
 __device__ __forceinline__ void await_words(const uint64_t* own, int64_t step, int order, int back, int state,
                                             int lane, uint64_t (*look)[64]) {
@@ -333,7 +334,7 @@ struct Place {
         const uint32_t wg = blockIdx.z * gridDim.x + blockIdx.x;  // (fewer than 2^31 have a tile)
         order = wg / chains;
         chain = wg % chains;
-        if (tiles == 1 || order >= tiles) return;
+        if (tiles == 1 || !is_tile(order, tiles)) return;
         if (chains % 8 == 0) chain = (chain & ~7u) + ((chain + order) & 7);
         if (threadIdx.x == 0) *ticket = atomicAdd(a.tickets + (int64_t)chain * TICKET_WORDS, 1u);
         __syncthreads();
@@ -351,8 +352,8 @@ __global__ __launch_bounds__(64 * WAVES, 8) void gated_scan_fwd_kernel(ScanArgs 
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t blocks = (a.C + 63) / 64;
     const Place place(a, tiles, a.B * blocks, look);
+    if (!is_tile(place.order, tiles)) return;
     const int k = place.order, b = place.chain / blocks, own = place.chain % blocks * 64 + lane;
-    if (k >= tiles) return;
     const bool active = own < a.C;
     const uint32_t c = active ? own : a.C - 1;
     const uint32_t row_bytes = a.C * (uint32_t)sizeof(T), lane_bytes = c * (uint32_t)sizeof(T);
@@ -444,9 +445,9 @@ __global__ __launch_bounds__(GS_THREADS, far ? 6 : 8) void gated_scan_bwd_kernel
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t blocks = (a.C + 63) / 64;
     const Place place(a, tiles, a.B * blocks, look);
+    if (!is_tile(place.order, tiles)) return;
     const int order = place.order, k = tiles - 1 - order;
     const int b = place.chain / blocks, own = place.chain % blocks * 64 + lane;
-    if (k < 0) return;
     const bool active = own < a.C;
     const uint32_t c = active ? own : a.C - 1;
     const uint32_t row_bytes = a.C * (uint32_t)sizeof(T), lane_bytes = c * (uint32_t)sizeof(T);
