@@ -1093,7 +1093,8 @@ def gated_scan_fwd(x, g, input_gate, A_log, dt_bias, initial_state=None, output_
     x, g, input_gate [B,T,C], all bf16 or all fp32 (C a multiple of 8); A_log, dt_bias [C]
     fp32; initial_state [N,C] fp32 or None; cu_seqlens int32 [N+1] or None (B must then be
     1; rows outside every sequence get zeros).  ``workspace`` (gated_scan_workspace_size
-    bytes), ``out`` and ``final_out`` optionally supply device buffers.  Returns (o [B,T,C]
+    bytes), ``out`` and ``final_out`` optionally supply device buffers; ``out`` may be x, g
+    or input_gate, and they share no memory with an input otherwise.  Returns (o [B,T,C]
     as x, final_state [N,C] fp32 or None)."""
     return _scan_fwd(x, g, input_gate, A_log, dt_bias, initial_state, output_final_state,
                      cu_seqlens, workspace, out, final_out, False)[:2]
@@ -1134,7 +1135,7 @@ def gated_scan_bwd(x, g, input_gate, A_log, dt_bias, do, states, initial_state=N
 def gated_scan_decode(x, g, input_gate, A_log, dt_bias, state=None, state_out=None, out=None):
     """One token of the recurrence for N sequences: x, g, input_gate [N,C], all bf16 or all
     fp32; state [N,C] fp32 or None (zeros).  ``state_out`` may be ``state`` (update in
-    place).  Returns (o [N,C] as x, new state [N,C] fp32)."""
+    place), and ``out`` x, g or input_gate.  Returns (o [N,C] as x, new state [N,C] fp32)."""
     code, dtype, dev, shape = _tokens(x, "x", 2, "[N, C]")
     N, C = shape
     fp32 = _Torch.parts.fp32
@@ -1177,8 +1178,9 @@ def short_conv_fwd(x, weight, bias=None, activation="silu", initial_state=None,
     x_{t-W+1+j}).  x [B,T,C] bf16 or fp32 (C a multiple of 8); weight [C,W] (W 2, 3 or 4),
     bias [C] or None, fp32; activation "silu" or "none"; initial_state [N,W-1,C] as x (the
     W - 1 tokens in front of each sequence, the oldest first) or None (zeros); cu_seqlens
-    int32 [N+1] or None (B must then be 1; rows outside every sequence get zeros).  Returns
-    (y [B,T,C] as x, final_state [N,W-1,C] as x or None)."""
+    int32 [N+1] or None (B must then be 1; rows outside every sequence get zeros).  ``out``
+    and ``final_out`` optionally supply device buffers, which share no memory with an input.
+    Returns (y [B,T,C] as x, final_state [N,W-1,C] as x or None)."""
     code, dtype, dev, (B, T, C) = _tokens(x, "x", 3, "[B, T, C]")
     N = _sequences(B, cu_seqlens, dev)
     W, act = _conv_parameters(C, weight, bias, activation, dev)
@@ -1216,8 +1218,8 @@ def short_conv_bwd(x, weight, dy, bias=None, activation="silu", initial_state=No
 
 def short_conv_decode(x, weight, state, bias=None, activation="silu", state_out=None, out=None):
     """One token of the convolution for N sequences: x [N,C] bf16 or fp32, state [N,W-1,C]
-    as x, the oldest token first.  ``state_out`` may be ``state`` (update in place).
-    Returns (y [N,C], new state [N,W-1,C]), as x."""
+    as x, the oldest token first.  ``state_out`` may be ``state`` (update in place), and
+    ``out`` x.  Returns (y [N,C], new state [N,W-1,C]), as x."""
     code, dtype, dev, (N, C) = _tokens(x, "x", 2, "[N, C]")
     W, act = _conv_parameters(C, weight, bias, activation, dev)
     _need_all((("state", _some(state, "state")), ("state_out", state_out)), dtype, (N, W - 1, C),

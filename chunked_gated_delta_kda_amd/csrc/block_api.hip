@@ -26,6 +26,33 @@ bool aligned(std::initializer_list<const void*> ps, size_t a) {
 int status() { return hipGetLastError() == hipSuccess ? KDA_OK : KDA_ERR_LAUNCH; }
 bool known_type(int32_t dtype) { return dtype == KDA_BF16 || dtype == KDA_FP32; }
 
+// An array of a call, null or not.
+struct Span {
+    const void* p;
+    size_t bytes;
+};
+bool meet(const Span& a, const Span& b) {
+    if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
+    const uintptr_t i = (uintptr_t)a.p, j = (uintptr_t)b.p;
+    return i < j + b.bytes && j < i + a.bytes;
+}
+// No output shares memory with an input or with another output.
+bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        if (std::any_of(ins.begin(), ins.end(), [&](const Span& i) { return meet(*o, i); })) return false;
+        if (std::any_of(o + 1, outs.end(), [&](const Span& q) { return meet(*o, q); })) return false;
+    }
+    return true;
+}
+// Each output is one of the inputs or shares no memory with them (for kernels in which
+// whoever writes an element has read it).
+bool in_place(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    for (const Span& o : outs)
+        if (std::any_of(ins.begin(), ins.end(), [&](const Span& i) { return o.p != i.p && meet(o, i); })) return false;
+    return true;
+}
+size_t token_bytes(int32_t dtype) { return dtype == KDA_FP32 ? 4 : 2; }
+
 // Sizes of a batch of tokens; a status.
 int check_batch(int32_t dtype, const int32_t* cu, int32_t num_seqs, int32_t B, int32_t T, int32_t C) {
     if (B < 1 || T < 0 || T > MAX_TOKENS || C < 1 || !known_type(dtype)) return KDA_ERR_INVALID_ARG;
@@ -171,6 +198,15 @@ int gated_scan_fwd(const void* x, const void* g, const void* input_gate, const f
     const ScanSpace sp = scan_space(B, T, C, cu_seqlens != nullptr, false);
     st = check_workspace(workspace, workspace_bytes, sp.total);
     if (st != KDA_OK) return st;
+    const size_t tokens = (size_t)B * T * C * token_bytes(dtype), row = (size_t)C * sizeof(float);
+    const size_t N = cu_seqlens ? num_seqs : B;
+    const Span so{o, tokens}, sf{final_state, N * row}, ss{states, (size_t)B * scan_states(T) * row};
+    const Span sw{workspace, sp.total}, sx{x, tokens}, sg{g, tokens}, si{input_gate, tokens};
+    const Span sA{A_log, row}, sb{dt_bias, row}, s0{initial_state, N * row};
+    const Span sc{cu_seqlens, (N + 1) * sizeof(int32_t)};
+    if (!in_place({so}, {sx, sg, si}) || !apart({so, sf, ss, sw}, {sA, sb, s0, sc}) ||
+        !apart({sf, ss, sw}, {sx, sg, si}))
+        return KDA_ERR_INVALID_ARG;
     kda::ScanArgs a =
         scan_args(x, g, input_gate, A_log, dt_bias, initial_state, cu_seqlens, num_seqs, B, T, C, sp, workspace);
     a.h_final = final_state;
@@ -194,6 +230,16 @@ int gated_scan_bwd(const void* x, const void* g, const void* input_gate, const f
     const ScanSpace sp = scan_space(B, T, C, cu_seqlens != nullptr, true);
     st = check_workspace(workspace, workspace_bytes, sp.total);
     if (st != KDA_OK) return st;
+    const size_t tokens = (size_t)B * T * C * token_bytes(dtype), row = (size_t)C * sizeof(float);
+    const size_t N = cu_seqlens ? num_seqs : B;
+    const Span gx{dx, tokens}, gg{dg, tokens}, gi{dinput_gate, tokens}, gA{dA_log, row}, gb{ddt_bias, row};
+    const Span g0{dh0, N * row}, sw{workspace, sp.total};
+    const Span sx{x, tokens}, sg{g, tokens}, si{input_gate, tokens}, sd{d_o, tokens};
+    const Span sA{A_log, row}, sb{dt_bias, row}, s0{initial_state, N * row}, sf{d_final, N * row};
+    const Span ss{states, (size_t)B * scan_states(T) * row}, sc{cu_seqlens, (N + 1) * sizeof(int32_t)};
+    if (!in_place({gx, gg, gi}, {sx, sg, si, sd}) ||
+        !apart({gx, gg, gi, gA, gb, g0, sw}, {sA, sb, s0, sf, ss, sc}) || !apart({gA, gb, g0, sw}, {sx, sg, si, sd}))
+        return KDA_ERR_INVALID_ARG;
     kda::ScanArgs a =
         scan_args(x, g, input_gate, A_log, dt_bias, initial_state, cu_seqlens, num_seqs, B, T, C, sp, workspace);
     a.d_o = d_o;
@@ -218,6 +264,13 @@ int gated_scan_decode(const void* x, const void* g, const void* input_gate, cons
     if (!x || !g || !input_gate || !A_log || !dt_bias || !state_out || !o) return KDA_ERR_INVALID_ARG;
     if (!aligned({x, g, input_gate, state_in, state_out, o}, 16) || !aligned({A_log, dt_bias}, 4))
         return KDA_ERR_INVALID_ARG;
+    const size_t tokens = (size_t)N * C * token_bytes(dtype), states = (size_t)N * C * sizeof(float);
+    const Span so{o, tokens}, sn{state_out, states}, s0{state_in, states};
+    const Span sx{x, tokens}, sg{g, tokens}, si{input_gate, tokens};
+    const Span sA{A_log, C * sizeof(float)}, sb{dt_bias, C * sizeof(float)};
+    if (!in_place({so}, {sx, sg, si}) || !in_place({sn}, {s0}) || !apart({so, sn}, {sA, sb}) || !apart({so}, {s0}) ||
+        !apart({sn}, {sx, sg, si}))
+        return KDA_ERR_INVALID_ARG;
     kda::ScanDecodeArgs a{};
     a.x = x;
     a.g = g;
@@ -240,6 +293,12 @@ int short_conv_fwd(const void* x, const float* weight, const float* bias, int32_
     const int st = check_conv(x, weight, bias, activation, initial_state, cu_seqlens, num_seqs, dtype, B, T, C, W);
     if (st != KDA_OK) return st;
     if ((T > 0 && !y) || !aligned({y, final_state}, 16)) return KDA_ERR_INVALID_ARG;
+    const size_t tokens = (size_t)B * T * C * token_bytes(dtype), row = (size_t)C * sizeof(float);
+    const size_t N = cu_seqlens ? num_seqs : B, states = N * (W - 1) * C * token_bytes(dtype);
+    if (!apart({{y, tokens}, {final_state, states}},
+               {{x, tokens}, {initial_state, states}, {weight, W * row}, {bias, row},
+                {cu_seqlens, (N + 1) * sizeof(int32_t)}}))
+        return KDA_ERR_INVALID_ARG;
     kda::ConvArgs a = conv_args(x, weight, bias, activation, initial_state, cu_seqlens, num_seqs, B, T, C);
     a.h_final = final_state;
     a.y = y;
@@ -263,8 +322,15 @@ int short_conv_bwd(const void* x, const float* weight, const float* bias, int32_
     if (st != KDA_OK) return st;
     if (!dweight || (bias && !dbias) || (T > 0 && (!dy || !dx))) return KDA_ERR_INVALID_ARG;
     if (!aligned({dy, d_final, dx, dh0}, 16) || !aligned({dweight, dbias}, 4)) return KDA_ERR_INVALID_ARG;
-    st = check_workspace(workspace, workspace_bytes, short_conv_bwd_workspace_size(dtype, B, T, C, W));
+    const size_t need = short_conv_bwd_workspace_size(dtype, B, T, C, W);
+    st = check_workspace(workspace, workspace_bytes, need);
     if (st != KDA_OK) return st;
+    const size_t tokens = (size_t)B * T * C * token_bytes(dtype), row = (size_t)C * sizeof(float);
+    const size_t N = cu_seqlens ? num_seqs : B, states = N * (W - 1) * C * token_bytes(dtype);
+    if (!apart({{dx, tokens}, {dweight, W * row}, {dbias, row}, {dh0, states}, {workspace, need}},
+               {{x, tokens}, {dy, tokens}, {initial_state, states}, {d_final, states}, {weight, W * row}, {bias, row},
+                {cu_seqlens, (N + 1) * sizeof(int32_t)}}))
+        return KDA_ERR_INVALID_ARG;
     kda::ConvArgs a = conv_args(x, weight, bias, activation, initial_state, cu_seqlens, num_seqs, B, T, C);
     a.dy = dy;
     a.d_final = d_final;
@@ -284,6 +350,11 @@ int short_conv_decode(const void* x, const float* weight, const float* bias, int
     const int st = check_conv(x, weight, bias, activation, state_in, nullptr, 0, dtype, N, 1, C, W);
     if (st != KDA_OK) return st;
     if (!state_in || !state_out || !y || !aligned({state_out, y}, 16)) return KDA_ERR_INVALID_ARG;
+    const size_t tokens = (size_t)N * C * token_bytes(dtype), row = (size_t)C * sizeof(float);
+    const Span sy{y, tokens}, sn{state_out, tokens * (W - 1)}, sx{x, tokens}, s0{state_in, tokens * (W - 1)};
+    if (!in_place({sy}, {sx}) || !in_place({sn}, {s0}) || !apart({sy, sn}, {{weight, W * row}, {bias, row}}) ||
+        !apart({sy}, {s0}) || !apart({sn}, {sx}))
+        return KDA_ERR_INVALID_ARG;
     kda::ConvDecodeArgs a{};
     a.x = x;
     a.weight = weight;
@@ -306,7 +377,10 @@ int layer_norm_fwd(const void* x, const void* residual, const float* weight, con
     if (rows > 0 && (!x || !y || (residual && !sum))) return KDA_ERR_INVALID_ARG;
     if (!aligned({x, residual, y, sum}, 16) || !aligned(bias, 4)) return KDA_ERR_INVALID_ARG;
     if (rows == 0) return KDA_OK;
-    if (residual && y == sum) return KDA_ERR_INVALID_ARG;
+    const size_t tokens = (size_t)rows * D * token_bytes(dtype), row = (size_t)D * sizeof(float);
+    const Span sy{y, tokens}, ss{residual ? sum : nullptr, tokens};
+    if (!in_place({sy, ss}, {{x, tokens}, {residual, tokens}}) || !apart({sy, ss}, {{weight, row}, {bias, row}}))
+        return KDA_ERR_INVALID_ARG;
     kda::LayerNormArgs a{};
     a.x = x;
     a.res = residual;
@@ -334,8 +408,15 @@ int layer_norm_bwd(const void* sum, const float* weight, float eps, int32_t dtyp
     if (st != KDA_OK) return st;
     if (!dweight || (rows > 0 && (!sum || !dy || !dx))) return KDA_ERR_INVALID_ARG;
     if (!aligned({sum, dy, dsum, dx}, 16) || !aligned({dweight, dbias}, 4)) return KDA_ERR_INVALID_ARG;
-    st = check_workspace(workspace, workspace_bytes, layer_norm_bwd_workspace_size(dtype, rows, D));
+    const size_t need = layer_norm_bwd_workspace_size(dtype, rows, D);
+    st = check_workspace(workspace, workspace_bytes, need);
     if (st != KDA_OK) return st;
+    const size_t tokens = (size_t)rows * D * token_bytes(dtype), row = (size_t)D * sizeof(float);
+    const Span gx{dx, tokens}, gw{dweight, row}, gb{dbias, row}, sw{workspace, need};
+    const Span su{sum, tokens}, sd{dy, tokens}, ss{dsum, tokens};
+    if (!in_place({gx}, {su, sd, ss}) || !apart({gx, gw, gb, sw}, {{weight, row}}) ||
+        !apart({gw, gb, sw}, {su, sd, ss}))
+        return KDA_ERR_INVALID_ARG;
     kda::LayerNormArgs a{};
     a.x = sum;
     a.weight = weight;

@@ -532,6 +532,12 @@ int gated_norm_bwd(const uint16_t* x, const uint16_t* gate, const float* weight,
  *  - cu_seqlens as for kda_fwd (B = 1); every row of an output is written: rows
  *    outside every sequence get zeros, whatever the inputs hold there.
  *    num_seqs is read only with cu_seqlens.
+ *  - An output shares no memory with an input, another output or the workspace,
+ *    else KDA_ERR_INVALID_ARG, but that it may be one of these, from its beginning:
+ *    o of gated_scan_fwd and gated_scan_decode x, g or input_gate; the token
+ *    gradients of gated_scan_bwd one of x, g, input_gate and d_o; y of
+ *    short_conv_decode x; state_out state_in; y and sum of layer_norm_fwd x or
+ *    residual; dx of layer_norm_bwd sum, dy or dsum.
  *  - Arithmetic is fp32, each output is rounded once; sums over tokens or rows
  *    have a fixed order: equal calls give equal bits.
  *  - A NaN or an infinity does not leave its channel and sequence (recurrence: a
@@ -620,11 +626,9 @@ int short_conv_decode(const void* x, const float* weight, const float* bias, int
  *   y = (u - mean(u)) / sqrt(mean((u - mean(u))^2) + eps) weight + bias.
  * x, residual, y, sum [rows, D] tokens; weight [D], bias [D] (NULL: none) fp32.
  * residual NULL: u = x, and sum is not written.  eps >= 0; rows < 2^31, rows = 0
- * is allowed (row tensors may then be NULL).  y may be x or residual, and sum may
- * be x or residual (each row is read before it is written), y and sum are two
- * arrays.  Rows of any size keep their precision: where their squares would leave
- * fp32's range they are scaled by a power of two first.  A row of equal values
- * with eps = 0 gives NaN. */
+ * is allowed (row tensors may then be NULL).  Rows of any size keep their
+ * precision: where their squares would leave fp32's range they are scaled by a
+ * power of two first.  A row of equal values with eps = 0 gives NaN. */
 int layer_norm_fwd(const void* x, const void* residual, const float* weight, const float* bias,
                    float eps, int32_t dtype, int64_t rows, int32_t D, void* y, void* sum,
                    void* stream);
