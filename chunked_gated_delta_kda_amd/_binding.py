@@ -1247,7 +1247,9 @@ def layer_norm_fwd(x, weight, bias=None, eps=1e-5, residual=None, out=None, sum_
     to 16384): u = x + residual (if given; rounded to x's type), y = (u - mean(u)) /
     sqrt(var(u) + eps) weight + bias.  residual as x; weight [D], bias [D] or None, fp32.
     ``out`` and ``sum_out`` may be ``x`` or ``residual``, one each.  Returns (y, u), both as
-    x; u is ``x`` itself without a residual."""
+    x; u is ``x`` itself without a residual, and ``sum_out`` is refused."""
+    if residual is None and sum_out is not None:
+        raise ValueError("sum_out needs a residual: without one the sum is x itself")
     code, dtype, dev, shape, rows, D = _rows(x, "x", weight)
     if bias is not None:
         _need(bias, "bias", _Torch.parts.fp32, (D,), dev)

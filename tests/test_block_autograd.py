@@ -73,3 +73,9 @@ def test_states_are_kept_only_where_a_gradient_is_recorded(calls, final):
         o, f = kda.gated_scan(leaves[0], x, leaves[1], leaves[2], p, output_final_state=final)
         assert o.requires_grad and (f is None) != final
     assert calls[2:] == ["save"] * 3
+
+
+def test_a_sum_that_would_not_be_written_is_refused():
+    x, p = torch.zeros(4, C), torch.zeros(C)
+    with pytest.raises(ValueError, match="residual"):
+        kda.layer_norm_fwd(x, p, sum_out=torch.zeros(4, C))
