@@ -979,7 +979,9 @@ def _tokens(t, name, dims, what):
     shape = t.shape
     if dims and len(shape) != dims:
         raise ValueError(f"{name} must be {what}")
-    if t.numel() > _MOST and max(shape) > _MOST:  # (sizes are passed in 32 bits)
+    n = t.numel()
+    # (sizes are passed in 32 bits; rows of any dims are counted, and there may be none)
+    if (n > _MOST or n == 0 and dims) and max(shape) > _MOST:
         raise LibKdaError(1, status_str(1))
     return code, dtype, t.device, shape
 
