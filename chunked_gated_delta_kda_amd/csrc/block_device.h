@@ -36,8 +36,7 @@ struct Word<float> {
 
 // A sigmoid s = 1 / (1 + e^-z) as e^min(z, 0) / (1 + e^-|z|), to a few ulps where it is
 // normal, and subnormal below z = -87: 2^t by the hardware is not, the square of 2^(t / 2)
-// is.  `side` is s (1 - s).  For a NaN both are numbers: what they are multiplied by z for
-// is one.
+// is.  `side` is s (1 - s).  For a NaN both are NaN.
 struct BlockSigmoid {
     float s, side;
     __device__ __forceinline__ explicit BlockSigmoid(float z) {
