@@ -3,7 +3,8 @@ gradients of fixed lengths that fill no tile."""
 import pytest
 import torch
 
-from block_util import near
+import chunked_gated_delta_kda_amd as kda
+from block_util import near, to_gpu
 from oracle import block as ref
 from test_gpu_scan import args, make, run
 
@@ -90,3 +91,38 @@ def test_a_nan_in_a_gate_still_reaches_its_channels_gradients():
     _, _, r = run(w)
     for n in ("dA_log", "ddt_bias"):
         assert r[n][3].isnan() and torch.isfinite(r[n][:3]).all() and torch.isfinite(r[n][4:]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T", [1, 70, 300])
+def test_a_channel_that_keeps_everything(T, dtype):
+    """dt_bias = -inf: nothing enters and nothing is forgotten, and no gradient passes the
+    gate; the initial state has the sum of the outputs' gradients."""
+    w = make(2, T, 24, seed=127, dtype=dtype)
+    w["dt_bias"][7] = -INF
+    o, f, r = run(w)
+    assert torch.equal(f[:, 7].cpu(), w["h0"][:, 7])
+    assert torch.equal(o[..., 7].cpu(), w["h0"][:, None, 7].expand(2, T).to(w["x"].dtype))
+    for n in ("dx", "dg", "dinput_gate"):
+        assert not r[n][..., 7].any() and torch.isfinite(r[n]).all()
+    assert r["dA_log"][7] == 0 and r["ddt_bias"][7] == 0
+    do = w["do"][..., 7].double()
+    want = do.sum(1) + w["dfinal"][:, 7]
+    # a sum of T + 1 terms in fp32, 2^-24 of each partial sum
+    assert ((r["dh0"][:, 7].double().cpu() - want).abs()
+            <= (T + 1) * 2.0 ** -24 * (do.abs().sum(1) + w["dfinal"][:, 7].abs())).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_single_tokens_with_infinite_gates(dtype):
+    w = to_gpu(make(3, 1, 16, seed=131, dtype=dtype))
+    tok = [w[k][:, 0].contiguous() for k in ("x", "g", "gate")]
+    w["dt_bias"][0], w["dt_bias"][1] = INF, -INF
+    tok[1][:, 2], tok[1][:, 3], tok[1][:, 4] = INF, -INF, torch.finfo(tok[1].dtype).max
+    o, s = kda.gated_scan_decode(*tok, w["A_log"], w["dt_bias"], w["h0"])
+    assert torch.isfinite(s).all()
+    assert torch.equal(s[:, [1, 3]], w["h0"][:, [1, 3]])
+    forgets = [0, 2, 4]
+    want = (torch.sigmoid(tok[2].double()) * tok[0].double())[:, forgets]
+    assert ((s[:, forgets].double() - want).abs() <= 2.0 ** -20 * want.abs()).all()
+    assert torch.equal(o, s.to(o.dtype))
