@@ -1,5 +1,5 @@
 // gated_scan.hip -- the gated linear recurrence over channels (gfx950): per
-// channel c of a sequence, with the decay gate of KDA and a gate on the input,
+// channel c of a sequence, with the decay gate of KDA (no lower bound) and a gate on the input,
 //   L_t = exp(A_log[c]) softplus(g_t + dt_bias[c]),  a_t = exp(-L_t),
 //   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t,  o_t = h_t.
 // Gradients, with e_t = dL/dh_t = do_t + a_{t+1} e_{t+1}, m = sqrt(1 - a^2),
@@ -22,10 +22,12 @@
 // 2 x 2048 x 4096 the same to 1%.  Tiles of 256 tokens halve what tiles exchange, and end
 // later: 443 and 448 us, packed prompts 268 and 254.
 // Measured (bf16): 131072 x 2048 454 us, 4.7 TB/s; 2 x 2048 x 4096 with the states kept
-// 38 us, 3.7 TB/s; their gradients 61 us with the launches before and behind, 4.1 TB/s;
-// those of 16384 x 4096 210 us, 4.6 TB/s.
-// What bounds the long call is the memory: a kernel that only moves such rows reaches
-// 4.7 TB/s (of 256 bytes: 5.1).  The gradients lose 13 us to three launches.
+// 37 us, 3.8 TB/s; their gradients 59 us with the launches before and behind, 4.1 TB/s;
+// those of 16384 x 4096 220 us, 4.4 TB/s.
+// What bounds the long call is the memory, with the arithmetic close behind: a kernel that
+// only moves such rows reaches 4.7 TB/s (of 256 bytes: 5.1), and the VALU is active for 91%
+// of the cycles (2 x 2048 x 4096: 72%, its gradients 83%; there the workgroups of a round
+// load, compute and store at the same time).  The gradients lose 13 us to three launches.
 #include <cfloat>
 
 #include "block_device.h"
@@ -627,7 +629,8 @@ void launch_prepare(const ScanArgs& a, int tiles, int64_t chains, const float* s
 // Few chains are short of tiles that can end, and a tile looks far; with more of them the
 // words that it reads cost more (bf16, 131072 x 512, 8 chains: forward 138 us, 176 without,
 // gradients 301 and 359; 65536 x 640, 10 chains: 89 and 103, 196 and 206; 32768 x 768, 12
-// chains: 57 and 61, 123 and 118; 16384 x 1024: 39 and 38, 79 and 67).
+// chains: 57 and 61, 123 and 118; 16384 x 1024: 39 and 38, 79 and 67).  All of these are
+// rows of one length; packed batches go by the same number.
 constexpr int64_t FAR_CHAINS = 10;
 
 int64_t chains_of(const ScanArgs& a) { return (int64_t)a.B * ((a.C + 63) / 64); }

@@ -15,9 +15,10 @@
 // over the rows and keep their lanes' channels of dweight and dbias in registers, 64
 // rows at a time in fp32 (LN_CHAIN) and more of them in 64 bits in LDS; a second kernel
 // adds the workgroups' sums in a fixed order, in 64 bits.
-// Measured (16384 x 4096 bf16): forward with a residual 102 us, 5.3 TB/s, gradients 114 us,
-// 4.7 TB/s; 3001 x 1000 fp32 forward 7.3 us, gradients 13.1 and their sum 3.9 (its 24 MB
-// are in flight for too short a time: six rows a workgroup, one after the other).
+// Measured (16384 x 4096 bf16, calls of one kind): forward with a residual 101 us, 5.3 TB/s,
+// gradients with the launch behind 113 us, 4.8 TB/s; one behind the other, in a trace, 93,
+// 123 and 5 us.  3001 x 1000 fp32: forward 7.7 us, gradients 13.6 and their sum 4.0 (its 24
+// MB are in flight for too short a time: six rows a workgroup, one after the other).
 #include <algorithm>
 
 #include "block_device.h"
@@ -438,8 +439,8 @@ void by_type_and_row(bool fp32, int32_t D, F&& f) {
 
 constexpr int threads_of(int L) { return L > LN_THREADS ? L : LN_THREADS; }
 
-// Workgroups: as many as are in flight at once, `waves` waves of them on each CU.
-// (16384 x 4096 bf16: forward 101 us, 125 with 8 and 105 with 32 waves; gradients 114 us,
+// Workgroups: as many as are in flight at once, `waves` waves of them on each CU, for every
+// width and type by what one size took.  (16384 x 4096 bf16: forward 101 us, 125 with 8 and 105 with 32 waves; gradients 114 us,
 // 167 with 4 and 137 with 16, which leave twice the sums to add.)
 constexpr int LN_FWD_WAVES = 16, LN_BWD_WAVES = 8;
 

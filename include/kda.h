@@ -540,18 +540,24 @@ int gated_norm_bwd(const uint16_t* x, const uint16_t* gate, const float* weight,
  *    residual; dx of layer_norm_bwd sum, dy or dsum.
  *  - Arithmetic is fp32, each output is rounded once; sums over tokens or rows
  *    have a fixed order: equal calls give equal bits.
+ *  - A sigmoid of the recurrence or a softplus below 2^-126 counts as zero
+ *    (arguments below -87, where exp(A_log) times it is as small).
  *  - A NaN or an infinity does not leave its channel and sequence (recurrence: a
  *    NaN goes on to the end, however fast the decays; convolution: the W tokens
  *    that see it; layer norm: its row), but for the parameters' gradients of its
  *    channel (layer norm: of all channels, for dweight). */
 enum kda_dtype { KDA_BF16 = 0, KDA_FP32 = 1 };
 
-/* Gated linear recurrence: per channel c, with KDA's decay gate,
+/* Gated linear recurrence: per channel c, with kda_fwd's decay gate but for its
+ * lower_bound (there is none),
  *   L_t = exp(A_log[c]) softplus(g_t + dt_bias[c]),  a_t = exp(-L_t),
  *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(input_gate_t) x_t,  o_t = h_t.
  * x, g, input_gate, o [B, T, C] tokens; A_log, dt_bias [C]; states
  * [N, C].  initial_state NULL: zeros; final_state NULL: not written; a sequence
- * without a token returns its initial state.  exp(A_log[c]) has to be finite.
+ * without a token returns its initial state.  exp(A_log[c]) has to be finite;
+ * g or dt_bias may be infinite (a is one or zero, and what it cuts off has no
+ * gradient), not both with opposite signs, nor dt_bias +infinity with an fp32 g
+ * of -FLT_MAX, whose gradients take the sum for zero.
  * B ceil(T / 64) ceil(C / 64) < 2^31.
  * states (NULL: not kept): gated_scan_states(B, T, C) fp32 numbers, what
  * gated_scan_bwd needs of the forward pass (the state that enters every 8th
