@@ -26,7 +26,7 @@
 // those of 16384 x 4096 220 us, 4.4 TB/s.
 // What bounds the long call is the memory, with the arithmetic close behind: a kernel that
 // only moves such rows reaches 4.7 TB/s (of 256 bytes: 5.1), and the VALU is active for 91%
-// of the cycles (2 x 2048 x 4096: 72%, its gradients 83%; there the workgroups of a round
+// of the cycles (2 x 2048 x 4096: 72%, its gradients 83%; there the workgroups that run together
 // load, compute and store at the same time).  The gradients lose 13 us to three launches.
 #include <cfloat>
 
